@@ -395,6 +395,118 @@ MOE_API moe_status_t moe_forward_nvfp4(const moe_bf16_t *x_perm, const int32_t *
 MOE_API moe_status_t moe_quantize_nvfp4_rows(const moe_bf16_t *v, int64_t rows, int K, int pow2, uint8_t *q,
                                      uint8_t *sb, float *scale, moe_stream_t stream);
 
+/* moe_forward_w8a8_rows -- moe_forward_w8a8 on token rows that are E4M3 already:
+ * xq [T, H] uint8 codes and x_scale [T] fp32 row scales, as moe_add_rmsnorm or
+ * moe_quantize_act_rows writes them.  The weights apply at the output (topk_w
+ * NULL: weight 1 for every kept pair); row t's codes are copied to the rows of its
+ * pairs (pair_row), where moe_forward_w8a8 would place the codes it makes.  x
+ * [T, H] bf16 is read only by the shared experts' gate (it may be NULL without
+ * shared_gate_w).  xq must be 16-byte aligned.  Everything else as
+ * moe_forward_w8a8; with the rows and scales of moe_quantize_act_rows(x) the
+ * result is bitwise that of moe_forward_w8a8 on x. */
+MOE_API moe_status_t moe_forward_w8a8_rows(const uint8_t *xq, const float *x_scale, const int32_t *offsets,
+                                   int S_local, int64_t P_cap, const uint8_t *W1q, const float *W1_scale,
+                                   const uint8_t *W2q, const float *W2_scale, int H, int I,
+                                   const int32_t *pair_row, const float *topk_w, int64_t T, int k,
+                                   const moe_bf16_t *x, const uint8_t *W1sq, const float *W1s_scale,
+                                   const uint8_t *W2sq, const float *W2s_scale, int I_shared_total,
+                                   const moe_bf16_t *shared_gate_w, moe_bf16_t *out, void *ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* moe_add_rmsnorm -- the norm in front of the layer.                        */
+/* ------------------------------------------------------------------------ */
+/* The source pages have no counterpart; it makes the rows the layer reads.  Per
+ * row of x [T, H]:
+ *     r = residual + x             (binary32; x alone when residual is NULL)
+ *     y = r / sqrt(sum(r^2) / H + eps) * weight
+ *     residual_out = r, y_out = bf16(y)
+ *     scale = 2^e, e the smallest integer >= -126 with max|y| <= 448 * 2^e
+ *     q = e4m3(y / scale)          (to nearest, ties to even)
+ * The norm is that of the unrounded r, and y is rounded once for each output: q is
+ * not the E4M3 code of the rounded y_out.
+ *
+ *   x        [T, H] bf16
+ *   residual [T, H] bf16 (residual_f32 = 0) or fp32 (1), or NULL
+ *   weight   [H] bf16
+ *   eps      added to the mean square, >= 0 and finite
+ *   residual_out [T, H] of residual's type, or NULL (required NULL when residual is)
+ *   y        [T, H] bf16 out, or NULL
+ *   q        [T, H] uint8 out (E4M3), scale [T] fp32 out, or both NULL
+ * residual_out may be residual and y may be x (in place); no other overlap.  At
+ * least one output is given.  H: a multiple of 8, at most 16384
+ * (MOE_ERR_UNSUPPORTED otherwise).  Every pointer 16-byte aligned, q 8-byte, scale
+ * 4-byte.  A row of zeros gives y = 0, q = 0, scale 2^-126; a row holding an
+ * infinity or a NaN gives what these formulas give in binary32 (E4M3 NaN codes for
+ * NaN values).  No workspace; asynchronous on `stream`; one launch. */
+MOE_API moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const void *residual, int residual_f32,
+                                   const moe_bf16_t *weight, float eps, int64_t T, int H, void *residual_out,
+                                   moe_bf16_t *y, uint8_t *q, float *scale, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* 4-bit weights with group scales, bf16 activations.                        */
+/* ------------------------------------------------------------------------ */
+/* A matrix W [N, K] is stored as codes c in -8 .. 7 and one bf16 scale per `group`
+ * consecutive elements of a row, W[n][k] = scale[n][k / group] * c[n][k]; group is
+ * 32, 64 or 128 and K a multiple of it.
+ *   q     [N, K/2] uint8   eight elements per 32-bit little-endian word: element 2i
+ *                          of the eight in nibble i, element 2i + 1 in nibble i + 4,
+ *                          each as c + 8 (nibble 0: the word's lowest four bits)
+ *   scale [N, K/group] bf16
+ * Expert weights [S, R, K] are one [S*R, K] matrix.  (The formats of
+ * moe_forward_nvfp4 quantise the activations too; here they stay bf16.) */
+
+/* Quantise a bf16 matrix w [rows, K]: per group scale = bf16(amax / 7) and
+ * c = w / scale rounded to the nearest integer (ties to even) and clamped to
+ * -8 .. 7, both divisions in IEEE binary32; a group of zeros gets scale 0 and
+ * c = 0.  w must be 16-byte, q 4-byte and scale 2-byte aligned.  group other than
+ * 32, 64, 128 or K not a multiple of it -> MOE_ERR_UNSUPPORTED.  Asynchronous on
+ * `stream`; allocates nothing. */
+MOE_API moe_status_t moe_quantize_w4_rows(const moe_bf16_t *w, int64_t rows, int K, int group, uint8_t *q,
+                                   moe_bf16_t *scale, moe_stream_t stream);
+
+/* moe_matvec_w4 -- y [M, N] bf16 = x [M, K] bf16 times W^T, W [N, K] in the format
+ * above: products with a few rows (made for M up to about 16; larger M gives the
+ * same values with the weights read from L2 again for every 16 rows).  Sums in
+ * fp32, one rounding at the end; a row's result does not depend on M.  x and q
+ * 16-byte, scale and y 2-byte aligned; M, N < 2^31.  No workspace. */
+MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const moe_bf16_t *scale, int64_t M, int N,
+                                   int K, int group, moe_bf16_t *y, moe_stream_t stream);
+
+/* moe_forward_w4 -- moe_forward on 4-bit experts at decode: per kept pair of token
+ * t and slot s (row r of the permutation, t = perm_src[r] / k)
+ *     h[r] = bf16( silu(x[t] W1[s]_gate^T) * (x[t] W1[s]_up^T) ),  y[r] = h[r] W2[s]^T
+ *     out[t] = bf16( sum_j topk_w[t,j] * y[pair_row[t,j]] + g_t * shared(x[t]) )
+ * with y and the combine in fp32 (h is the one intermediate rounding), the shared
+ * experts and g_t as in moe_forward.  Token rows are read through perm_src, so
+ * moe_permute needs no x_perm.
+ *
+ *   x        [T, H] bf16, perm_src [P_cap] int32 and offsets, pair_row, topk_w as
+ *            moe_permute writes them (topk_w NULL: weight 1)
+ *   W1q [S_local, 2I, H/2] uint8 (I gate rows, then I up rows), W1_scale [S_local, 2I, H/group] bf16
+ *   W2q [S_local, H, I/2] uint8, W2_scale [S_local, H, I/group] bf16
+ *   W1sq [2*I_shared_total, H/2], W1s_scale; W2sq [H, I_shared_total/2], W2s_scale (or NULL)
+ *   ws       at least moe_workspace_size_w4 bytes
+ * H, I and I_shared_total multiples of 64 and of group.  Entries of perm_src
+ * outside [0, T*k) and of pair_row outside [-1, P_cap) are dropped and flagged.
+ * Meant for decode batches (up to about 16 rows per slot); larger batches are
+ * right, but each 16 rows of a slot read its weights again (from L2).  The other
+ * arguments and errors as moe_forward. */
+MOE_API moe_status_t moe_forward_w4(const moe_bf16_t *x, const int32_t *offsets, int S_local, int64_t P_cap,
+                                   const int32_t *perm_src, const uint8_t *W1q, const moe_bf16_t *W1_scale,
+                                   const uint8_t *W2q, const moe_bf16_t *W2_scale, int H, int I, int group,
+                                   const int32_t *pair_row, const float *topk_w, int64_t T, int k,
+                                   const uint8_t *W1sq, const moe_bf16_t *W1s_scale, const uint8_t *W2sq,
+                                   const moe_bf16_t *W2s_scale, int I_shared_total,
+                                   const moe_bf16_t *shared_gate_w, moe_bf16_t *out, void *ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
+/* Bytes of workspace moe_forward_w4 needs for up to max_T tokens (the header, h and
+ * the fp32 outputs of every pair, and the shared experts'); a layer that calls
+ * moe_route and moe_permute with the same buffer takes the larger of this and
+ * moe_workspace_size.  Returns 0 for invalid sizes. */
+MOE_API size_t moe_workspace_size_w4(int64_t max_T, int H, int I, int k, int I_shared_total);
+
 /* ---- the three stages of moe_forward ------------------------------------ */
 
 /* FC1 + SwiGLU on the tcgen05 tensor cores.  Routed problem: for each of the G

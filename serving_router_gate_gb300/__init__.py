@@ -31,7 +31,8 @@ __all__ = [
     "moe_launch_events_mark", "moe_launch_events_used", "EXPORTED_SYMBOLS", "moe_a2a_regroup",
     "moe_grouped_fc2_scatter", "moe_ep_signal", "moe_ep_reduce", "moe_ipc_export", "moe_ipc_import",
     "moe_ipc_close", "MOE_IPC_HANDLE_BYTES",
-    "MOE_A2A_TO_GEMM", "MOE_A2A_TO_EXCHANGE",
+    "MOE_A2A_TO_GEMM", "MOE_A2A_TO_EXCHANGE", "moe_add_rmsnorm", "moe_forward_w8a8_rows", "moe_quantize_w4_rows",
+    "moe_matvec_w4", "moe_forward_w4", "moe_workspace_size_w4",
 ]
 
 MOE_OK = 0
@@ -59,7 +60,8 @@ EXPORTED_SYMBOLS = (
     "moe_forward_w8a8", "moe_quantize_act_rows", "moe_grouped_fc1_w8a8", "moe_grouped_fc2_w8a8",
     "moe_launch_events_arm", "moe_launch_events_mark", "moe_launch_events_used", "moe_a2a_regroup",
     "moe_grouped_fc2_scatter", "moe_ep_signal", "moe_ep_reduce", "moe_ipc_export", "moe_ipc_import",
-    "moe_ipc_close",
+    "moe_ipc_close", "moe_add_rmsnorm", "moe_forward_w8a8_rows", "moe_quantize_w4_rows", "moe_matvec_w4",
+    "moe_forward_w4", "moe_workspace_size_w4",
 )
 
 
@@ -116,6 +118,14 @@ def _load():
         "moe_ipc_export": ([P, P, P], i32),
         "moe_ipc_import": ([P, i64, P], i32),
         "moe_ipc_close": ([P, i64], i32),
+        "moe_add_rmsnorm": ([P, P, i32, P, ctypes.c_float, i64, i32, P, P, P, P, P], i32),
+        "moe_forward_w8a8_rows": ([P, P, P, i32, i64, P, P, P, P, i32, i32, P, P, i64, i32, P, P, P, P, P, i32, P, P,
+                                   P, sz, P], i32),
+        "moe_quantize_w4_rows": ([P, i64, i32, i32, P, P, P], i32),
+        "moe_matvec_w4": ([P, P, P, i64, i32, i32, i32, P, P], i32),
+        "moe_forward_w4": ([P, P, i32, i64, P, P, P, P, P, i32, i32, i32, P, P, i64, i32, P, P, P, P, i32, P, P, P, sz,
+                            P], i32),
+        "moe_workspace_size_w4": ([i64, i32, i32, i32, i32], sz),
         "moe_debug_wait_timeout": ([P, sz, u64, P], i32),
         "moe_set_wait_timeout_ns": ([u64], None),
         "moe_route_noalloc": ([P, P, P, i64, i32, i32, i32, i32, P, P, P], i32),
@@ -495,6 +505,108 @@ def moe_finalize(y, pair_row, topk_w, y_shared, x, shared_gate_w, out, ws, strea
                            _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True),
                            _ptr(out, "out", _bf16, (T, H)), _ptr(ws, "ws", torch.uint8), ws.numel(), _stream(stream))
     _check("moe_finalize", st)
+
+
+def moe_forward_w8a8_rows(xq, x_scale, offsets, W1q, s1, W2q, s2, pair_row, topk_w, x, W1sq, s1s, W2sq, s2s,
+                          shared_gate_w, out, ws, stream=None):
+    """moe_forward_w8a8 on token rows that are E4M3 already (moe_add_rmsnorm's q and scale): xq [T, H] uint8,
+    x_scale [T] fp32.  x (bf16) is read only by the shared experts' gate and may be None without one."""
+    S_local = offsets.shape[0] - 1
+    I = W2q.shape[2]
+    T, k = pair_row.shape
+    H = xq.shape[1]
+    I_sh = 0 if W2sq is None else W2sq.shape[1]
+    u8 = torch.uint8
+    st = _lib.moe_forward_w8a8_rows(
+        _ptr(xq, "xq", u8, (T, H)), _ptr(x_scale, "x_scale", _f32, (T,)), _ptr(offsets, "offsets", _i32), S_local,
+        T * k, _ptr(W1q, "W1q", u8, (S_local, 2 * I, H)), _ptr(s1, "W1_scale", _f32, (S_local, 2 * I)),
+        _ptr(W2q, "W2q", u8, (S_local, H, I)), _ptr(s2, "W2_scale", _f32, (S_local, H)), H, I,
+        _ptr(pair_row, "pair_row", _i32), _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), T, k,
+        _ptr(x, "x", _bf16, (T, H), allow_none=True), _ptr(W1sq, "W1sq", u8, (2 * I_sh, H), allow_none=True),
+        _ptr(s1s, "W1s_scale", _f32, (2 * I_sh,), allow_none=True),
+        _ptr(W2sq, "W2sq", u8, (H, I_sh), allow_none=True),
+        _ptr(s2s, "W2s_scale", _f32, (H,), allow_none=True), I_sh,
+        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), _ptr(out, "out", _bf16, (T, H)),
+        _ptr(ws, "ws", u8), ws.numel(), _stream(stream))
+    _check("moe_forward_w8a8_rows", st)
+
+
+def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y, q=None, scale=None, stream=None):
+    """r = residual + x (x alone when residual is None), y = bf16(r / sqrt(mean(r^2) + eps) * weight), and with q and
+    scale the same values in E4M3 (uint8) with one power-of-two scale per row.  x [T, H] bf16; residual [T, H] bf16 or
+    fp32; weight [H] bf16; residual_out [T, H] of residual's type (it may be residual) or None; y [T, H] bf16 (it may
+    be x) or None; q [T, H] uint8 and scale [T] fp32, or None."""
+    T, H = x.shape
+    f32 = residual is not None and residual.dtype is _f32
+    rt = _f32 if f32 else _bf16
+    st = _lib.moe_add_rmsnorm(_ptr(x, "x", _bf16, (T, H)), _ptr(residual, "residual", rt, (T, H), allow_none=True),
+                              f32, _ptr(weight, "weight", _bf16, (H,)), eps, T, H,
+                              _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True),
+                              _ptr(y, "y", _bf16, (T, H), allow_none=True),
+                              _ptr(q, "q", torch.uint8, (T, H), allow_none=True),
+                              _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream))
+    _check("moe_add_rmsnorm", st)
+
+
+def moe_quantize_w4_rows(w, q, scale, stream=None):
+    """4-bit quantisation of a bf16 tensor [..., K] with one bf16 scale per group: q [..., K/2] uint8, scale
+    [..., K/group] bf16; the group (32, 64 or 128) is read off scale's shape."""
+    K = w.shape[-1]
+    rows = w.numel() // K
+    lead = tuple(w.shape[:-1])
+    group = max(1, K // max(1, scale.shape[-1]))
+    st = _lib.moe_quantize_w4_rows(_ptr(w, "w", _bf16), rows, K, group,
+                                   _ptr(q, "q", torch.uint8, lead + (K // 2,)),
+                                   _ptr(scale, "scale", _bf16, lead + (K // group,)), _stream(stream))
+    _check("moe_quantize_w4_rows", st)
+
+
+def moe_matvec_w4(x, q, scale, y, stream=None):
+    """y [M, N] bf16 = x [M, K] bf16 times the transpose of the 4-bit matrix q [N, K/2] uint8, scale [N, K/group]
+    bf16 (moe_quantize_w4_rows)."""
+    M, K = x.shape
+    N, ng = scale.shape
+    group = max(1, K // max(1, ng))
+    st = _lib.moe_matvec_w4(_ptr(x, "x", _bf16), _ptr(q, "q", torch.uint8, (N, K // 2)),
+                            _ptr(scale, "scale", _bf16, (N, K // group)), M, N, K, group,
+                            _ptr(y, "y", _bf16, (M, N)), _stream(stream))
+    _check("moe_matvec_w4", st)
+
+
+def moe_workspace_size_w4(max_T, H, I, k, I_shared_total=0) -> int:
+    """Bytes of workspace moe_forward_w4 needs for up to max_T tokens."""
+    n = _lib.moe_workspace_size_w4(max_T, H, I, k, I_shared_total)
+    if n == 0:
+        raise MoEError("moe_workspace_size_w4", MOE_ERR_UNSUPPORTED)
+    return int(n)
+
+
+def moe_forward_w4(x, offsets, perm_src, W1q, s1, W2q, s2, pair_row, topk_w, W1sq, s1s, W2sq, s2s, shared_gate_w,
+                   out, ws, stream=None):
+    """The experts on 4-bit weights with bf16 group scales (moe_quantize_w4_rows) and bf16 activations, for decode:
+    x [T, H] bf16, the tables moe_permute writes, W1q [S, 2I, H/2] / s1 [S, 2I, H/group], W2q [S, H, I/2] / s2
+    [S, H, I/group], the shared experts' likewise (or None), out [T, H] bf16."""
+    T, H = x.shape
+    S_local = offsets.shape[0] - 1
+    I = 2 * W2q.shape[2]
+    k = pair_row.shape[1]
+    P_cap = perm_src.shape[0]
+    I_sh = 0 if W2sq is None else 2 * W2sq.shape[1]
+    group = max(1, H // max(1, s1.shape[2]))
+    u8 = torch.uint8
+    gh, gi = H // group, I // group
+    st = _lib.moe_forward_w4(
+        _ptr(x, "x", _bf16), _ptr(offsets, "offsets", _i32), S_local, P_cap, _ptr(perm_src, "perm_src", _i32),
+        _ptr(W1q, "W1q", u8, (S_local, 2 * I, H // 2)), _ptr(s1, "W1_scale", _bf16, (S_local, 2 * I, gh)),
+        _ptr(W2q, "W2q", u8, (S_local, H, I // 2)), _ptr(s2, "W2_scale", _bf16, (S_local, H, gi)), H, I, group,
+        _ptr(pair_row, "pair_row", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), T, k,
+        _ptr(W1sq, "W1sq", u8, (2 * I_sh, H // 2), allow_none=True),
+        _ptr(s1s, "W1s_scale", _bf16, (2 * I_sh, gh), allow_none=True),
+        _ptr(W2sq, "W2sq", u8, (H, I_sh // 2), allow_none=True),
+        _ptr(s2s, "W2s_scale", _bf16, (H, I_sh // group), allow_none=True), I_sh,
+        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), _ptr(out, "out", _bf16, (T, H)),
+        _ptr(ws, "ws", u8), ws.numel(), _stream(stream))
+    _check("moe_forward_w4", st)
 
 
 def moe_a2a_regroup(recv_counts, src, dst, direction, offsets, ws, stream=None, row_map=None):

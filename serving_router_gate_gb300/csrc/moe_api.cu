@@ -3,6 +3,7 @@
 // (except the two explicit status readers).
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -588,7 +589,7 @@ static moe_status_t forward_impl(const moe_bf16_t* x_perm, const int32_t* offset
                                  const moe_bf16_t* x, const void* W1s, const float* s1s, const void* W2s,
                                  const float* s2s, int I_shared_total, const moe_bf16_t* shared_gate_w,
                                  moe_bf16_t* out, void* ws, size_t ws_bytes, moe_stream_t stream,
-                                 bool act8 = false) {
+                                 bool act8 = false, const uint8_t* xq = nullptr, const float* x_scale = nullptr) {
     if (T < 0 || k <= 0 || S_local <= 0 || P_cap < 0 || H <= 0 || I <= 0 || I_shared_total < 0)
         return MOE_ERR_INVALID_ARG;
     if (!dim_ok(H) || !dim_ok(I) || (I_shared_total > 0 && !dim_ok(I_shared_total)) || k > 32 || S_local > 1024 ||
@@ -597,9 +598,9 @@ static moe_status_t forward_impl(const moe_bf16_t* x_perm, const int32_t* offset
     if (T == 0) return MOE_OK;
     // E4M3 activations with the weights applied at the output: the token rows of x may
     // stand in for x_perm (each quantised once and placed at its pairs' rows)
-    const bool from_tokens = act8 && topk_w && x;
+    const bool from_tokens = act8 && ((topk_w && x) || xq);
     if ((!x_perm && !from_tokens) || !offsets || !W1 || !W2 || !pair_row || !out) return MOE_ERR_INVALID_ARG;
-    if (I_shared_total > 0 && (!x || !W1s || !W2s)) return MOE_ERR_INVALID_ARG;
+    if (I_shared_total > 0 && ((!x && !xq) || !W1s || !W2s)) return MOE_ERR_INVALID_ARG;
     if (shared_gate_w && (I_shared_total == 0 || !x)) return MOE_ERR_INVALID_ARG;
     const bool fp8 = s1 != nullptr;
     if (fp8 && (!s2 || (I_shared_total > 0 && (!s1s || !s2s)))) return MOE_ERR_INVALID_ARG;
@@ -623,7 +624,12 @@ static moe_status_t forward_impl(const moe_bf16_t* x_perm, const int32_t* offset
         const int64_t T_sh = I_shared_total > 0 ? T : 0;
         auto u8 = [&](size_t off) { return reinterpret_cast<uint8_t*>(base + off); };
         auto f32 = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
-        if (from_tokens && (T > 64 || !x_perm)) {
+        if (xq) {
+            // the token rows come quantised: placed at their pairs' rows; the shared
+            // experts read them where they are
+            const PlaceRowsLaunch p = {xq, x_scale, T, H, k, pair_row, u8(FL.xq), f32(FL.sxq), P_cap};
+            st = cuda_status(launch_place_rows(p, sms, s));
+        } else if (from_tokens && (T > 64 || !x_perm)) {
             // weights applied at the output: the expert input rows are copies of token
             // rows, so each token row is quantised once and its codes are placed at its
             // pairs' rows (and kept for the shared experts); small batches quantise the
@@ -641,10 +647,11 @@ static moe_status_t forward_impl(const moe_bf16_t* x_perm, const int32_t* offset
             st = cuda_status(launch_quantize_act_rows(qx, 2, sms, s));
         }
         if (st != MOE_OK) return st;
+        const uint8_t* xs = xq ? xq : u8(FL.xsq);
         st = gemm_call(true, reinterpret_cast<const moe_bf16_t*>(u8(FL.xq)), P_cap, offsets, S_local,
-                       static_cast<const moe_bf16_t*>(W1), H, I, reinterpret_cast<const moe_bf16_t*>(u8(FL.xsq)), T,
+                       static_cast<const moe_bf16_t*>(W1), H, I, reinterpret_cast<const moe_bf16_t*>(xs), T,
                        static_cast<const moe_bf16_t*>(W1s), I_shared_total, h, h_sh, ws, s, nullptr, 1, T, s1, s1s,
-                       f32(FL.sxq), f32(FL.sxs));
+                       f32(FL.sxq), xq ? x_scale : f32(FL.sxs));
         if (st != MOE_OK) return st;
         const ActQuantSeg qh[2] = {{h, P_cap, offsets + S_local, I, u8(FL.hq), f32(FL.shq)},
                                    {h_sh, T_sh, nullptr, I_shared_total, u8(FL.hsq), f32(FL.shs)}};
@@ -700,6 +707,164 @@ moe_status_t moe_forward_w8a8(const moe_bf16_t* x_perm, const int32_t* offsets, 
     return forward_impl(x_perm, offsets, S_local, P_cap, W1q, W1_scale, W2q, W2_scale, H, I, pair_row, topk_w, T, k,
                         x, W1sq, W1s_scale, W2sq, W2s_scale, I_shared_total, shared_gate_w, out, ws, ws_bytes,
                         stream, true);
+}
+
+moe_status_t moe_forward_w8a8_rows(const uint8_t* xq, const float* x_scale, const int32_t* offsets, int S_local,
+                                   int64_t P_cap, const uint8_t* W1q, const float* W1_scale, const uint8_t* W2q,
+                                   const float* W2_scale, int H, int I, const int32_t* pair_row, const float* topk_w,
+                                   int64_t T, int k, const moe_bf16_t* x, const uint8_t* W1sq, const float* W1s_scale,
+                                   const uint8_t* W2sq, const float* W2s_scale, int I_shared_total,
+                                   const moe_bf16_t* shared_gate_w, moe_bf16_t* out, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream) {
+    MOE_NVTX("moe_forward_w8a8_rows");
+    if (!W1_scale || !W2_scale) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!xq || !x_scale || !aligned(xq, 16) || !aligned(x_scale, 4))) return MOE_ERR_INVALID_ARG;
+    return forward_impl(nullptr, offsets, S_local, P_cap, W1q, W1_scale, W2q, W2_scale, H, I, pair_row, topk_w, T, k,
+                        x, W1sq, W1s_scale, W2sq, W2s_scale, I_shared_total, shared_gate_w, out, ws, ws_bytes,
+                        stream, true, xq, x_scale);
+}
+
+// longest row the norm takes (a CTA holds one in registers)
+constexpr int kNormMaxH = 16384;
+
+moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const void* residual, int residual_f32, const moe_bf16_t* weight,
+                             float eps, int64_t T, int H, void* residual_out, moe_bf16_t* y, uint8_t* q, float* scale,
+                             moe_stream_t stream) {
+    MOE_NVTX("moe_add_rmsnorm");
+    if (T < 0 || H <= 0 || (residual_f32 != 0 && residual_f32 != 1) || !(eps >= 0.f && eps <= FLT_MAX))
+        return MOE_ERR_INVALID_ARG;
+    if (H % 8 != 0 || H > kNormMaxH || T >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight || (residual_out && !residual) || (q == nullptr) != (scale == nullptr) ||
+        (!residual_out && !y && !q))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
+        !aligned(y, 16) || !aligned(q, 8) || !aligned(scale, 4))
+        return MOE_ERR_INVALID_ARG;
+    const NormLaunch L = {x, residual, weight, residual_out, y, q, scale, T, H, eps, residual_f32 == 1};
+    return cuda_status(launch_add_rmsnorm(L, device_sms(), (cudaStream_t)stream));
+}
+
+static bool w4_group_ok(int K, int group) { return (group == 32 || group == 64 || group == 128) && K % group == 0; }
+
+moe_status_t moe_quantize_w4_rows(const moe_bf16_t* w, int64_t rows, int K, int group, uint8_t* q, moe_bf16_t* scale,
+                                  moe_stream_t stream) {
+    MOE_NVTX("moe_quantize_w4_rows");
+    if (rows < 0 || K <= 0 || group <= 0) return MOE_ERR_INVALID_ARG;
+    if (!w4_group_ok(K, group)) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!w || !q || !scale || !aligned(w, 16) || !aligned(q, 4) || !aligned(scale, 2)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_quantize_w4_rows(w, rows, K, group, q, scale, device_sms(), (cudaStream_t)stream));
+}
+
+moe_status_t moe_matvec_w4(const moe_bf16_t* x, const uint8_t* q, const moe_bf16_t* scale, int64_t M, int N, int K,
+                           int group, moe_bf16_t* y, moe_stream_t stream) {
+    MOE_NVTX("moe_matvec_w4");
+    if (M < 0 || N <= 0 || K <= 0 || group <= 0) return MOE_ERR_INVALID_ARG;
+    if (!w4_group_ok(K, group) || K > (1 << 20) || M >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    if (!x || !q || !scale || !y || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 2) || !aligned(y, 2))
+        return MOE_ERR_INVALID_ARG;
+    W4Launch L;
+    L.name = "matvec_w4";
+    L.swiglu = false;
+    L.group = group;
+    L.sh.x = x;
+    L.sh.wq = q;
+    L.sh.ws = scale;
+    L.sh.K = K;
+    L.sh.N_out = N;
+    L.sh.out_bf16 = y;
+    L.rows_sh = M;
+    return cuda_status(launch_w4_gemm(L, device_sms(), (cudaStream_t)stream));
+}
+
+namespace {
+// moe_forward_w4's workspace: bf16 h and fp32 outputs of the pairs and of the shared experts
+struct W4Layout {
+    size_t h, h_sh, y, y_sh, total;
+};
+W4Layout w4_layout(int64_t P_cap, int64_t T, int H, int I, int I_sh) {
+    W4Layout L;
+    const size_t T_sh = I_sh > 0 ? (size_t)T : 0;
+    L.h = kWsHeaderBytes;
+    L.h_sh = L.h + a256((size_t)P_cap * (size_t)I * 2);
+    L.y = L.h_sh + a256(T_sh * (size_t)I_sh * 2);
+    L.y_sh = L.y + a256((size_t)P_cap * (size_t)H * 4);
+    L.total = L.y_sh + a256(T_sh * (size_t)H * 4);
+    return L;
+}
+}  // namespace
+
+size_t moe_workspace_size_w4(int64_t max_T, int H, int I, int k, int I_shared_total) {
+    if (max_T < 0 || !dim_ok(H) || !dim_ok(I) || k < 1 || k > 32 || I_shared_total < 0 ||
+        (I_shared_total > 0 && !dim_ok(I_shared_total)))
+        return 0;
+    return w4_layout(max_T * k, max_T, H, I, I_shared_total).total;
+}
+
+moe_status_t moe_forward_w4(const moe_bf16_t* x, const int32_t* offsets, int S_local, int64_t P_cap,
+                            const int32_t* perm_src, const uint8_t* W1q, const moe_bf16_t* W1_scale,
+                            const uint8_t* W2q, const moe_bf16_t* W2_scale, int H, int I, int group,
+                            const int32_t* pair_row, const float* topk_w, int64_t T, int k, const uint8_t* W1sq,
+                            const moe_bf16_t* W1s_scale, const uint8_t* W2sq, const moe_bf16_t* W2s_scale,
+                            int I_shared_total, const moe_bf16_t* shared_gate_w, moe_bf16_t* out, void* ws,
+                            size_t ws_bytes, moe_stream_t stream) {
+    MOE_NVTX("moe_forward_w4");
+    if (T < 0 || k <= 0 || S_local <= 0 || P_cap < 0 || H <= 0 || I <= 0 || I_shared_total < 0 || group <= 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!dim_ok(H) || !dim_ok(I) || (I_shared_total > 0 && !dim_ok(I_shared_total)) || !w4_group_ok(H, group) ||
+        !w4_group_ok(I, group) || (I_shared_total > 0 && !w4_group_ok(I_shared_total, group)) || k > 32 ||
+        S_local > 1024 || P_cap >= (int64_t(1) << 31) || T * (int64_t)k >= (int64_t(1) << 31))
+        return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !offsets || !perm_src || !W1q || !W1_scale || !W2q || !W2_scale || !pair_row || !out)
+        return MOE_ERR_INVALID_ARG;
+    if (I_shared_total > 0 && (!W1sq || !W1s_scale || !W2sq || !W2s_scale)) return MOE_ERR_INVALID_ARG;
+    if (shared_gate_w && I_shared_total == 0) return MOE_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W1q, 16) || !aligned(W2q, 16) || !aligned(W1sq, 16) || !aligned(W2sq, 16) ||
+        !aligned(W1_scale, 2) || !aligned(W2_scale, 2) || !aligned(W1s_scale, 2) || !aligned(W2s_scale, 2) ||
+        !aligned(shared_gate_w, 16) || !aligned(out, 16) || !aligned(ws, 16))
+        return MOE_ERR_INVALID_ARG;
+    const W4Layout WL = w4_layout(P_cap, T, H, I, I_shared_total);
+    if (!ws || ws_bytes < WL.total) return MOE_ERR_WORKSPACE;
+    char* base = static_cast<char*>(ws);
+    cudaStream_t s = (cudaStream_t)stream;
+    const int sms = device_sms();
+    int32_t* status = &static_cast<WsHeader*>(ws)->status;
+    moe_bf16_t* h = reinterpret_cast<moe_bf16_t*>(base + WL.h);
+    moe_bf16_t* h_sh = reinterpret_cast<moe_bf16_t*>(base + WL.h_sh);
+    float* y = reinterpret_cast<float*>(base + WL.y);
+    float* y_sh = reinterpret_cast<float*>(base + WL.y_sh);
+
+    W4Launch L;
+    L.name = "w4_fc1";
+    L.swiglu = true;
+    L.group = group;
+    L.rt = {x, W1q, W1_scale, H, I, h, nullptr};
+    L.offsets = offsets;
+    L.G = P_cap > 0 ? S_local : 0;
+    L.rows_cap = P_cap;
+    L.perm_src = perm_src;
+    L.T = T;
+    L.k = k;
+    if (I_shared_total > 0) {
+        L.sh = {x, W1sq, W1s_scale, H, I_shared_total, h_sh, nullptr};
+        L.rows_sh = T;
+    }
+    L.status = status;
+    moe_status_t st = cuda_status(launch_w4_gemm(L, sms, s));
+    if (st != MOE_OK) return st;
+    L.name = "w4_fc2";
+    L.swiglu = false;
+    L.perm_src = nullptr;
+    L.rt = {h, W2q, W2_scale, I, H, nullptr, y};
+    if (I_shared_total > 0) L.sh = {h_sh, W2sq, W2s_scale, I_shared_total, H, nullptr, y_sh};
+    st = cuda_status(launch_w4_gemm(L, sms, s));
+    if (st != MOE_OK) return st;
+    const W4CombineLaunch C = {y, P_cap, pair_row, topk_w, T, k, H, I_shared_total > 0 ? y_sh : nullptr, x,
+                               shared_gate_w, out, status};
+    return cuda_status(launch_w4_combine(C, s));
 }
 
 // longest row the NVFP4 quantiser takes (its CTA holds a row in registers)

@@ -590,6 +590,82 @@ cudaError_t launch_quantize_nvfp4_rows(const Nvfp4QuantSeg* seg, int nseg, int n
 // bytes of one row of NVFP4 block scales
 __host__ __device__ constexpr int nvfp4_sf_row_bytes(int K) { return 16 * ((K + 255) / 256); }
 
+// Copy E4M3 token rows xq [T, H] and their scales to the rows of their pairs,
+// dst row pair_row[t * k + j] (-1 and rows past dst_rows skipped).
+struct PlaceRowsLaunch {
+    const uint8_t* xq;
+    const float* x_scale;
+    int64_t T;
+    int H, k;
+    const int32_t* pair_row;
+    uint8_t* dst;
+    float* dst_scale;
+    int64_t dst_rows;
+};
+cudaError_t launch_place_rows(const PlaceRowsLaunch& L, int num_sms, cudaStream_t s);
+
+// The residual's addition, the norm and its E4M3 rows (moe_add_rmsnorm).
+struct NormLaunch {
+    const uint16_t* x;        // [T, H] bf16
+    const void* residual;     // [T, H] bf16 or (f32) fp32, or null
+    const uint16_t* weight;   // [H] bf16
+    void* residual_out;       // of residual's type, or null
+    uint16_t* y;              // [T, H] bf16, or null
+    uint8_t* q;               // [T, H] E4M3, or null
+    float* scale;             // [T] with q
+    int64_t T;
+    int H;
+    float eps;
+    bool f32;
+};
+cudaError_t launch_add_rmsnorm(const NormLaunch& L, int num_sms, cudaStream_t s);
+
+// Products with 4-bit weights (moe_matvec_w4, moe_forward_w4): one problem has A rows
+// x [., K] and packed weights of 2 N_out (SwiGLU: gate, then up) or N_out rows per slot.
+struct W4Problem {
+    const uint16_t* x = nullptr;
+    const uint8_t* wq = nullptr;   // [slots][rows][K / 2]
+    const uint16_t* ws = nullptr;  // [slots][rows][K / group] bf16
+    int K = 0, N_out = 0;
+    uint16_t* out_bf16 = nullptr;  // [., N_out]
+    float* out_f32 = nullptr;      // or this
+};
+struct W4Launch {
+    const char* name;
+    bool swiglu;
+    int group;
+    // routed problem: rows offsets[g] .. offsets[g+1]-1 of slot g (G = 0: none); A row of
+    // row r is token perm_src[r] / k, or r itself without perm_src
+    W4Problem rt;
+    const int32_t* offsets = nullptr;
+    int G = 0;
+    int64_t rows_cap = 0;
+    const int32_t* perm_src = nullptr;
+    int64_t T = 0;
+    int k = 1;
+    // dense problem on rows_sh rows (wq null: none)
+    W4Problem sh;
+    int64_t rows_sh = 0;
+    int32_t* status = nullptr;
+};
+cudaError_t launch_w4_gemm(const W4Launch& L, int num_sms, cudaStream_t s);
+struct W4CombineLaunch {
+    const float* y;            // [rows_cap, H]
+    int64_t rows_cap;
+    const int32_t* pair_row;   // [T, k]
+    const float* w;            // [T, k] or null
+    int64_t T;
+    int k, H;
+    const float* y_sh;         // [T, H] or null
+    const uint16_t* x;         // [T, H], with gate_w
+    const uint16_t* gate_w;    // [H] or null
+    uint16_t* out;
+    int32_t* status;
+};
+cudaError_t launch_w4_combine(const W4CombineLaunch& L, cudaStream_t s);
+cudaError_t launch_quantize_w4_rows(const uint16_t* w, int64_t rows, int K, int group, uint8_t* q, uint16_t* scale,
+                                    int num_sms, cudaStream_t s);
+
 // Whether kernels are launched with programmatic stream serialization (set by
 // moe_set_pdl; defined in moe_api.cu).
 bool pdl_enabled();

@@ -321,6 +321,51 @@ cudaError_t launch_quantize_act_rows(const ActQuantSeg* seg, int nseg, int num_s
     return launch_k("quantize_act_rows", quantize_act_rows_kernel, dim3(grid), dim3(QA_THREADS), 0, s, a);
 }
 
+namespace {
+
+// Rows that are E4M3 already, copied to their pairs' rows (each read once): one warp
+// per token row at a time, 16-byte pieces.
+__global__ void __launch_bounds__(QZ_WARPS * 32) place_rows_kernel(const __grid_constant__ PlaceRowsLaunch a) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int vec = a.H / 16;
+    for (int64_t t = (int64_t)blockIdx.x * QZ_WARPS + (threadIdx.x >> 5); t < a.T;
+         t += (int64_t)gridDim.x * QZ_WARPS) {
+        // lane j holds the row of pair j (k <= 32)
+        int32_t mine = lane < a.k ? __ldg(a.pair_row + t * a.k + lane) : -1;
+        if ((int64_t)mine >= a.dst_rows) mine = -1;
+        if (mine >= 0) a.dst_scale[mine] = __ldg(a.x_scale + t);
+        const uint4* src = reinterpret_cast<const uint4*>(a.xq + t * a.H);
+        for (int v0 = 0; v0 < vec; v0 += 128) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int v = v0 + i * 32 + lane;
+                u[i] = v < vec ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
+            }
+            for (int j = 0; j < a.k; ++j) {
+                const int32_t r = __shfl_sync(0xffffffffu, mine, j);
+                if (r < 0) continue;
+                uint4* dst = reinterpret_cast<uint4*>(a.dst + (int64_t)r * a.H);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int v = v0 + i * 32 + lane;
+                    if (v < vec) dst[v] = u[i];
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_place_rows(const PlaceRowsLaunch& L, int num_sms, cudaStream_t s) {
+    const int64_t want = (L.T + QZ_WARPS - 1) / QZ_WARPS;
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)num_sms * 8));
+    return launch_k("place_rows", place_rows_kernel, dim3(grid), dim3(QZ_WARPS * 32), 0, s, L);
+}
+
 cudaError_t launch_quantize_fp8_rows(const uint16_t* w, int64_t rows, int K, uint8_t* q, float* scale, int num_sms,
                                      cudaStream_t s) {
     const int64_t want = (rows + QZ_WARPS - 1) / QZ_WARPS;

@@ -14,9 +14,10 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_NONLOCAL_SKIP, moe_forward, moe_forward_fp8, moe_forward_nvfp4, moe_forward_w8a8, moe_permute,
-               moe_quantize_fp8_rows, moe_quantize_nvfp4_rows, moe_route, moe_route_grouped, moe_workspace_init,
-               moe_workspace_size, nvfp4_sf_row_bytes)
+from . import (MOE_NONLOCAL_SKIP, moe_add_rmsnorm, moe_forward, moe_forward_fp8, moe_forward_nvfp4, moe_forward_w4,
+               moe_forward_w8a8, moe_forward_w8a8_rows, moe_permute, moe_quantize_fp8_rows, moe_quantize_nvfp4_rows,
+               moe_quantize_w4_rows, moe_route, moe_route_grouped, moe_workspace_init, moe_workspace_size,
+               moe_workspace_size_w4, nvfp4_sf_row_bytes)
 
 
 class MoELayer:
@@ -27,7 +28,8 @@ class MoELayer:
                  nonlocal_mode: int = MOE_NONLOCAL_SKIP, W1s: Optional[torch.Tensor] = None,
                  W2s: Optional[torch.Tensor] = None, shared_gate_w: Optional[torch.Tensor] = None,
                  on_input: bool = False, n_group: int = 1, topk_group: int = 1, fp8: bool = False,
-                 act8: bool = False, fp4: bool = False):
+                 act8: bool = False, fp4: bool = False, w4: int = 0, norm_w: Optional[torch.Tensor] = None,
+                 norm_eps: float = 1e-6):
         self.Wg, self.W1, self.W2 = Wg, W1, W2
         # routing applied on the input: rows scaled by the weights, outputs summed unweighted
         self.on_input = bool(on_input)
@@ -58,6 +60,14 @@ class MoELayer:
         self.x_perm = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
         self.out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
         nbytes = moe_workspace_size(T, H, self.I, self.E, max(self.S, self.S_local), k, self.I_sh)
+        # 4-bit experts with one bf16 scale per group of w4 elements (32, 64 or 128; 0: off)
+        self.w4 = int(w4)
+        if self.w4:
+            if fp8 or fp4:
+                raise ValueError("one weight format at a time")
+            if self.on_input:
+                raise ValueError("4-bit experts apply the routing weights at the output")
+            nbytes = max(nbytes, moe_workspace_size_w4(T, H, self.I, k, self.I_sh))
         self.ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
         moe_workspace_init(self.ws)
         # E4M3 expert weights with one fp32 scale per row, quantised once here
@@ -98,6 +108,27 @@ class MoELayer:
                 self.W1sf = quant4(W1s)
                 self.W2sf = quant4(W2s)
 
+        self.W1w4 = self.W2w4 = self.W1sw4 = self.W2sw4 = None
+        if self.w4:
+            def quant_w4(w):
+                K = w.shape[-1]
+                q = torch.empty(w.shape[:-1] + (K // 2,), dtype=torch.uint8, device=dev)
+                sc = torch.empty(w.shape[:-1] + (K // self.w4,), dtype=torch.bfloat16, device=dev)
+                moe_quantize_w4_rows(w, q, sc)
+                return q, sc
+            self.W1w4, self.W2w4 = quant_w4(W1), quant_w4(W2)
+            if W1s is not None:
+                self.W1sw4, self.W2sw4 = quant_w4(W1s), quant_w4(W2s)
+        # the norm in front of the layer (block()): its rows in bf16 for the router and, for
+        # E4M3 activations with the weights at the output, in E4M3 for the experts
+        self.norm_w, self.norm_eps = norm_w, float(norm_eps)
+        self.x_norm = self.x_q = self.x_scale = None
+        if norm_w is not None:
+            self.x_norm = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+            if self.act8 and not self.on_input:
+                self.x_q = torch.empty((T, H), dtype=torch.uint8, device=dev)
+                self.x_scale = torch.empty((T,), dtype=torch.float32, device=dev)
+
     def views(self, T: int) -> dict:
         k = self.k
         return dict(topk_ids=self.topk_ids[:T], topk_w=self.topk_w[:T], slot_ids=self.slot_ids[:T],
@@ -116,12 +147,12 @@ class MoELayer:
     def rows_from_tokens(self, T: int) -> bool:
         """Whether the expert input rows are read from the token rows through pair_row, with
         the weights applied at the output: quantised activations (NVFP4, or E4M3 with E4M3
-        weights) are made once per token row and placed at its pairs' rows, so moe_permute
-        copies no rows into x_perm (at every batch size this saves more in the permute than
+        weights) are made once per token row and placed at its pairs' rows, and 4-bit weights'
+        products read x itself, so moe_permute copies no rows into x_perm (at every batch size this saves more in the permute than
         the token-row quantiser gives up in parallelism)."""
         if self.on_input:
             return False
-        return self.fp4 or self.act8
+        return self.fp4 or self.act8 or self.w4 > 0
 
     def permute(self, x: torch.Tensor, stream=None) -> dict:
         v = self.views(x.shape[0])
@@ -131,13 +162,24 @@ class MoELayer:
                     v["perm_src"], v["pair_row"], xp, self.ws, stream, on_input=self.on_input)
         return v
 
-    def expert_forward(self, x: torch.Tensor, stream=None, out: Optional[torch.Tensor] = None) -> dict:
+    def expert_forward(self, x: torch.Tensor, stream=None, out: Optional[torch.Tensor] = None, x_q=None,
+                       x_scale=None) -> dict:
+        """x_q, x_scale: x's rows in E4M3 already (E4M3 activations only), else made from x."""
         v = self.views(x.shape[0])
         if out is not None:
             v["out"] = out
         w = None if self.on_input else v["topk_w"]
         xs = x if (self.I_sh > 0) else None
-        if self.fp4:
+        if self.w4:
+            q1s = s1s = q2s = s2s = None
+            if self.W1sw4 is not None:
+                (q1s, s1s), (q2s, s2s) = self.W1sw4, self.W2sw4
+            moe_forward_w4(x, v["offsets"], v["perm_src"], *self.W1w4, *self.W2w4, v["pair_row"], w, q1s, s1s, q2s,
+                           s2s, self.gate, v["out"], self.ws, stream)
+        elif x_q is not None:
+            moe_forward_w8a8_rows(x_q, x_scale, v["offsets"], self.W1q, self.s1, self.W2q, self.s2, v["pair_row"], w,
+                                  x, self.W1sq, self.s1s, self.W2sq, self.s2s, self.gate, v["out"], self.ws, stream)
+        elif self.fp4:
             (q1, f1, s1), (q2, f2, s2) = self.W1f, self.W2f
             q1s = f1s = s1s = q2s = f2s = s2s = None
             if self.W1sf is not None:
@@ -197,6 +239,25 @@ class MoELayer:
         self.route(x, stream)
         self.permute(x, stream)
         return self.expert_forward(x, stream, out)["out"]
+
+
+    def block(self, x: torch.Tensor, residual: torch.Tensor, stream=None,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The norm and the layer: residual [T, H] (bf16 or fp32) becomes residual + x in place, and the layer's
+        forward of its RMS norm (norm_w, norm_eps) is returned.  With E4M3 activations the experts read the norm's own
+        E4M3 rows (rounded once, from the unrounded norm)."""
+        if self.norm_w is None:
+            raise ValueError("block() needs norm_w")
+        T = x.shape[0]
+        assert T <= self.max_T and x.shape[1] == self.H
+        if T == 0:
+            return self.out[:0] if out is None else out
+        xn = self.x_norm[:T]
+        xq, xs = (None, None) if self.x_q is None else (self.x_q[:T], self.x_scale[:T])
+        moe_add_rmsnorm(x, residual, self.norm_w, self.norm_eps, residual, xn, xq, xs, stream)
+        self.route(xn, stream)
+        self.permute(xn, stream)
+        return self.expert_forward(xn, stream, out, xq, xs)["out"]
 
 
 class HostPipeline:
