@@ -13,6 +13,8 @@
 // (exact: bf16 has seven fraction bits), in the order in which the activations lie
 // in memory.
 #include <algorithm>
+#include <atomic>
+#include <cmath>
 
 #include "moe_internal.cuh"
 
@@ -56,81 +58,342 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 }
 
 // ---------------------------------------------------------------------------
-// Products, one warp per (row, output)
+// Products on mma.sync: a warp owns 32 weight rows (FC1: 16 gate and the matching
+// 16 up rows) times up to 8 C activation rows
 // ---------------------------------------------------------------------------
-constexpr int W4_WARPS = 8;
+constexpr int W4_THREADS = 256;
+constexpr int W4_WARPS = W4_THREADS / 32;
+constexpr int W4_RING = 4;           // stages of 128 elements x 32 rows in each warp's ring
+constexpr int W4_STAGE = 2048;       // bytes of a stage
+constexpr int W4_MAXG = 1024;        // slots
 
-// Lane-strided dot product of one weight row with one activation row; every lane
-// gets the sum.
-__device__ __forceinline__ float w4_dot(const uint8_t* wq, const uint16_t* ws, const uint16_t* x, int K, int group) {
-    const int lane = threadIdx.x & 31;
-    float acc = 0.f;
-    for (int v = lane; v < K / 8; v += 32) {
-        const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(wq) + v);
-        float f[8];
-        unpack8(*(reinterpret_cast<const uint4*>(x) + v), f);
-        float p = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            p = fmaf((float)((int)((word >> (4 * (j / 2 + 4 * (j & 1)))) & 15u) - 8), f[j], p);
-        acc = fmaf(bf16_bits_to_float(__ldg(ws + v * 8 / group)), p, acc);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    return acc;
+__host__ __device__ constexpr size_t w4_smem_bytes(int C) {
+    // ring of every warp, then two buffers of 32 x 8 C partial sums per warp
+    return (size_t)W4_WARPS * (W4_RING * W4_STAGE + 2 * 32 * 8 * C * 4);
 }
 
-__device__ __forceinline__ void w4_output(const W4Problem& p, int64_t slot, const uint16_t* x, int64_t out_row, int n,
-                                          bool swiglu, int group) {
-    const int64_t rows = swiglu ? 2 * (int64_t)p.N_out : p.N_out;
-    const uint8_t* wq = p.wq + slot * rows * (p.K / 2);
-    const uint16_t* ws = p.ws + slot * rows * (p.K / group);
-    float v = w4_dot(wq + (int64_t)n * (p.K / 2), ws + (int64_t)n * (p.K / group), x, p.K, group);
-    if (swiglu) {
-        const int64_t u = (int64_t)p.N_out + n;
-        const float up = w4_dot(wq + u * (p.K / 2), ws + u * (p.K / group), x, p.K, group);
-        v = v / (1.0f + expf(-v)) * up;
-    }
-    if ((threadIdx.x & 31) == 0) {
-        if (p.out_f32)
-            p.out_f32[out_row * p.N_out + n] = v;
+__device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src, bool valid) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void w4_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void w4_cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t w4_lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// D += A B, A 16 x 16 (row), B 16 x 8 (column), bf16 inputs, fp32 sums
+__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Elements 2j and 2j + 1 of a packed word as bf16 128 + (c + 8)
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j) {
+    return ((word >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+}
+
+// The KS warps of a group (KS = 1: one warp) meet
+__device__ __forceinline__ void w4_group_sync(int id, int KS) {
+    if (KS == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(KS * 32) : "memory");
+}
+
+// One unit: 32 weight rows of one slot times m <= 8 C activation rows.
+struct W4Unit {
+    const W4Problem* p;
+    const uint8_t* wq;      // the slot's packed weights
+    const uint16_t* ws;     // and scales
+    int n0;                 // first output
+    int64_t row0;           // first output row
+    int m;                  // rows
+    bool routed;
+};
+
+template <bool SWIGLU, int GS, int C>
+__device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, int KS, int ks, uint32_t ring,
+                                            float* red, int group_warp0, int group_id, int buf) {
+    constexpr int TN = SWIGLU ? 16 : 32;
+    constexpr int NF = 4 / GS;  // groups in a stage
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int K = u.p->K, N = u.p->N_out;
+    const int Kb = K / 2;
+    const int nst_all = (K + 127) / 128;
+    const int nst = ks < nst_all ? (nst_all - ks + KS - 1) / KS : 0;
+
+    // this lane's share of the weight copies: row lane / 4 of each eight, 16-byte piece lane % 4
+    const uint8_t* wsrc[4];
+    const uint16_t* ssrc[4];  // scales of accumulator rows g, g + 8 of both 16-row tiles
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int r = u.n0 + i * 8 + (lane >> 2);
+        if (SWIGLU)
+            r = i < 2 ? r : r - 16 + N;  // tile 1: the up rows
         else
-            p.out_bf16[out_row * p.N_out + n] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+            r = min(r, N - 1);
+        wsrc[i] = u.wq + (int64_t)r * Kb + t * 16;
+        ssrc[i] = u.ws + (int64_t)r * (K / (32 * GS));
     }
-}
+    const uint32_t dst = ring + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+    auto issue = [&](int i) {
+        const int k0 = (ks + i * KS) * 128;
+        const bool ok = i < nst && k0 + t * 32 < K;
+        const uint32_t d = dst + (i % W4_RING) * W4_STAGE;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w4_cp16(d + q * 512, wsrc[q] + (ok ? k0 / 2 : 0), ok);
+        w4_cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < W4_RING - 1; ++i) issue(i);
 
-__global__ void __launch_bounds__(W4_WARPS * 32) w4_gemm_kernel(const __grid_constant__ W4Launch a) {
-    pdl_wait();
-    pdl_trigger();
-    const int64_t step = (int64_t)gridDim.x * W4_WARPS;
-    const int64_t first = (int64_t)blockIdx.x * W4_WARPS + (threadIdx.x >> 5);
-    if (a.sh.wq)
-        for (int64_t i = first; i < a.rows_sh * a.sh.N_out; i += step) {
-            const int64_t r = i / a.sh.N_out;
-            w4_output(a.sh, 0, a.sh.x + r * a.sh.K, r, (int)(i - r * a.sh.N_out), a.swiglu, a.group);
-        }
-    if (a.G == 0) return;
-    const int64_t rows = min((int64_t)max(0, __ldg(a.offsets + a.G)), a.rows_cap);
-    for (int64_t i = first; i < rows * a.rt.N_out; i += step) {
-        const int64_t r = i / a.rt.N_out;
-        int lo = 0, hi = a.G - 1;  // the last slot whose rows begin at or before r
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (__ldg(a.offsets + mid) <= r)
-                lo = mid;
-            else
-                hi = mid - 1;
-        }
-        int64_t xr = r;
-        if (a.perm_src) {
-            const int32_t p = a.perm_src[r];
+    // activation rows of this lane's B columns (column g of each tile of eight)
+    const uint16_t* xsrc[C];
+    bool xok[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = c * 8 + g;
+        xok[c] = col < u.m;
+        int64_t xr = u.row0 + (xok[c] ? col : 0);
+        if (u.routed && a.perm_src) {
+            const int32_t p = a.perm_src[xr];
             if (p < 0 || (int64_t)p >= a.T * a.k) {
                 report(a.status, MOE_ERR_DEVICE_BOUNDS);
-                continue;
+                xok[c] = false;
+                xr = 0;
+            } else {
+                xr = p / a.k;
             }
-            xr = p / a.k;
         }
-        w4_output(a.rt, lo, a.rt.x + xr * a.rt.K, r, (int)(i - r * a.rt.N_out), a.swiglu, a.group);
+        xsrc[c] = u.p->x + xr * K + t * 8;
+    }
+    uint4 xb[C][4];
+    uint16_t sb[NF][4];
+    auto load_x = [&](int c, int j, int k0) {
+        xb[c][j] = xok[c] && k0 + j * 32 < K ? *reinterpret_cast<const uint4*>(xsrc[c] + k0 + j * 32)
+                                             : make_uint4(0, 0, 0, 0);
+    };
+    auto load_s = [&](int f, int k0) {
+        const bool ok = k0 + f * 32 * GS < K;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sb[f][i] = ok ? __ldg(ssrc[i] + k0 / (32 * GS) + f) : (uint16_t)0;
+    };
+    if (nst > 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_x(c, j, ks * 128);
+#pragma unroll
+        for (int f = 0; f < NF; ++f) load_s(f, ks * 128);
+    }
+
+    float acc[2][C][4], tmp[2][C][4], xs[C][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][c][i] = 0.f;
+
+    const uint32_t rd = ring + g * 64 + t * 4;
+    const int sw = (g >> 1) & 3;
+    for (int i = 0; i < nst; ++i) {
+        issue(i + W4_RING - 1);
+        w4_cp_wait<W4_RING - 1>();
+        __syncwarp();
+        const int k0 = (ks + i * KS) * 128;
+        const int k1 = i + 1 < nst ? k0 + KS * 128 : K;  // the next stage's elements (K: none)
+        const uint32_t st = rd + (i % W4_RING) * W4_STAGE;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (k0 + j * 32 < K) {
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = w4_lds32(st + ((j ^ sw) << 4) + q * 512);
+                if (j % GS == 0) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            tmp[0][c][e] = 0.f;
+                            tmp[1][c][e] = 0.f;
+                            xs[c][e] = 0.f;
+                        }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a00 = w4_pair(w[0], 2 * h), a01 = w4_pair(w[1], 2 * h),
+                                   a02 = w4_pair(w[0], 2 * h + 1), a03 = w4_pair(w[1], 2 * h + 1);
+                    const uint32_t a10 = w4_pair(w[2], 2 * h), a11 = w4_pair(w[3], 2 * h),
+                                   a12 = w4_pair(w[2], 2 * h + 1), a13 = w4_pair(w[3], 2 * h + 1);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        const uint32_t b0 = h ? xb[c][j].z : xb[c][j].x, b1 = h ? xb[c][j].w : xb[c][j].y;
+                        w4_mma(tmp[0][c], a00, a01, a02, a03, b0, b1);
+                        w4_mma(tmp[1][c], a10, a11, a12, a13, b0, b1);
+                        w4_mma(xs[c], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
+                    }
+                }
+                if ((j + 1) % GS == 0) {
+                    const int f = j / GS;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float s0 = bf16_bits_to_float(sb[f][2 * r]), s1 = bf16_bits_to_float(sb[f][2 * r + 1]);
+#pragma unroll
+                        for (int c = 0; c < C; ++c) {
+                            acc[r][c][0] = fmaf(s0, fmaf(-136.f, xs[c][0], tmp[r][c][0]), acc[r][c][0]);
+                            acc[r][c][1] = fmaf(s0, fmaf(-136.f, xs[c][1], tmp[r][c][1]), acc[r][c][1]);
+                            acc[r][c][2] = fmaf(s1, fmaf(-136.f, xs[c][0], tmp[r][c][2]), acc[r][c][2]);
+                            acc[r][c][3] = fmaf(s1, fmaf(-136.f, xs[c][1], tmp[r][c][3]), acc[r][c][3]);
+                        }
+                    }
+                }
+            }
+            // the same registers take the next stage's values
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_x(c, j, k1);
+            if ((j + 1) % GS == 0) load_s(j / GS, k1);
+        }
+        __syncwarp();  // the ring slot just read is the next one written
+    }
+    w4_cp_wait<0>();
+
+    // partial sums of the group's warps, added in order of their K ranges
+    float* mine = red + (buf * W4_WARPS + warp) * (32 * 8 * C);
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float* p = mine + (r * 16 + g) * (8 * C) + c * 8 + 2 * t;
+            *reinterpret_cast<float2*>(p) = make_float2(acc[r][c][0], acc[r][c][1]);
+            *reinterpret_cast<float2*>(p + 8 * 8 * C) = make_float2(acc[r][c][2], acc[r][c][3]);
+        }
+    w4_group_sync(group_id, KS);
+    const float* all = red + (buf * W4_WARPS + group_warp0) * (32 * 8 * C);
+    for (int o = ks * 32 + lane; o < TN * u.m; o += KS * 32) {
+        const int f = o % TN, col = o / TN;
+        float v = 0.f, up = 0.f;
+        for (int q = 0; q < KS; ++q) {
+            const float* p = all + q * (32 * 8 * C);
+            v += p[f * (8 * C) + col];
+            if (SWIGLU) up += p[(16 + f) * (8 * C) + col];
+        }
+        if (SWIGLU) v = v / (1.0f + expf(-v)) * up;
+        const int n = u.n0 + f;
+        if (n < N) {
+            const int64_t at = (u.row0 + col) * N + n;
+            if (u.p->out_f32)
+                u.p->out_f32[at] = v;
+            else
+                u.p->out_bf16[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+        }
+    }
+}
+
+template <bool SWIGLU, int GS, int C>
+__global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_constant__ W4Launch a, int KS) {
+    extern __shared__ __align__(128) uint8_t w4_smem[];
+    __shared__ int32_t s_pre[W4_MAXG];  // units of the routed slots before each slot
+    __shared__ int32_t s_part[W4_WARPS];
+    constexpr int TN = SWIGLU ? 16 : 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t ring = smem_u32(w4_smem) + warp * (W4_RING * W4_STAGE);
+    float* red = reinterpret_cast<float*>(w4_smem + W4_WARPS * W4_RING * W4_STAGE);
+    pdl_wait();
+    pdl_trigger();
+
+    const int tiles_sh = a.sh.wq ? (a.sh.N_out + TN - 1) / TN : 0;
+    const int ct_sh = (int)((a.rows_sh + 8 * C - 1) / (8 * C));
+    const int units_sh = tiles_sh * ct_sh;
+    const int tiles = a.G > 0 ? (a.rt.N_out + TN - 1) / TN : 0;
+    int units = units_sh;
+    if (a.G > 0) {
+        // exclusive scan of the slots' units, four slots a thread
+        const int s0 = threadIdx.x * (W4_MAXG / W4_THREADS);
+        int n[W4_MAXG / W4_THREADS], sum = 0;
+        int64_t lo = s0 <= a.G ? __ldg(a.offsets + s0) : 0;
+#pragma unroll
+        for (int i = 0; i < W4_MAXG / W4_THREADS; ++i) {
+            n[i] = 0;
+            if (s0 + i < a.G) {
+                const int64_t hi = __ldg(a.offsets + s0 + i + 1);
+                const int64_t m = max((int64_t)0, min(hi, a.rows_cap) - max(lo, (int64_t)0));
+                n[i] = (int)((m + 8 * C - 1) / (8 * C)) * tiles;
+                lo = hi;
+            }
+            sum += n[i];
+        }
+        int inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += v;
+        }
+        if (lane == 31) s_part[warp] = inc;
+        __syncthreads();
+        int base = inc - sum, total = 0;
+#pragma unroll
+        for (int w = 0; w < W4_WARPS; ++w) {
+            base += w < warp ? s_part[w] : 0;
+            total += s_part[w];
+        }
+#pragma unroll
+        for (int i = 0; i < W4_MAXG / W4_THREADS; ++i) {
+            if (s0 + i < a.G) s_pre[s0 + i] = base;
+            base += n[i];
+        }
+        units += total;
+        __syncthreads();
+    }
+
+    const int groups = W4_WARPS / KS;
+    const int grp = warp / KS, ks = warp - grp * KS;
+    int buf = 0;
+    for (int64_t v = (int64_t)grp * gridDim.x + blockIdx.x; v < units; v += (int64_t)groups * gridDim.x, buf ^= 1) {
+        W4Unit u;
+        if (v < units_sh) {
+            const int c = (int)v % ct_sh;
+            u.p = &a.sh;
+            u.wq = a.sh.wq;
+            u.ws = a.sh.ws;
+            u.n0 = ((int)v / ct_sh) * TN;
+            u.row0 = (int64_t)c * 8 * C;
+            u.m = (int)min((int64_t)(8 * C), a.rows_sh - u.row0);
+            u.routed = false;
+        } else {
+            const int w = (int)v - units_sh;
+            int lo = 0, hi = a.G - 1;  // the last slot whose units begin at or before w
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (s_pre[mid] <= w)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int64_t first = max(0, __ldg(a.offsets + lo));
+            const int64_t end = min((int64_t)__ldg(a.offsets + lo + 1), a.rows_cap);
+            const int ct = (int)((end - first + 8 * C - 1) / (8 * C));
+            const int q = w - s_pre[lo];
+            const int64_t wrows = SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out;
+            u.p = &a.rt;
+            u.wq = a.rt.wq + lo * wrows * (a.rt.K / 2);
+            u.ws = a.rt.ws + lo * wrows * (a.rt.K / (32 * GS));
+            u.n0 = (q / ct) * TN;
+            u.row0 = first + (int64_t)(q % ct) * 8 * C;
+            u.m = (int)min((int64_t)(8 * C), end - u.row0);
+            u.routed = true;
+        }
+        w4_run_unit<SWIGLU, GS, C>(a, u, KS, ks, ring, red, grp * KS, grp + 1, buf);
     }
 }
 
@@ -212,9 +475,60 @@ cudaError_t launch_quantize_w4_rows(const uint16_t* w, int64_t rows, int K, int 
                     group / 8, reinterpret_cast<uint32_t*>(q), scale);
 }
 
+template <bool SWIGLU, int GS, int C>
+static cudaError_t launch_w4_mma(const W4Launch& L, int num_sms, cudaStream_t s) {
+    // the shared-memory limit is set once per device
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const size_t smem = w4_smem_bytes(C);
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(w4_mma_kernel<SWIGLU, GS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    // Warps of a unit split its K among them: more of them shorten a unit, fewer waste
+    // less on its ends.  KS minimises the list-scheduling bound over groups of KS warps,
+    // sum of the units' stages / groups + the longest unit, a unit's ends counted as
+    // three stages.  The routed units are bounded by one row tile per slot with pairs.
+    constexpr int TN = SWIGLU ? 16 : 32;
+    const double u_sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + 8 * C - 1) / (8 * C)) : 0.0;
+    const double u_rt = L.G > 0 ? (double)((L.rt.N_out + TN - 1) / TN) * std::min<int64_t>(L.rows_cap, L.G) : 0.0;
+    const int n_sh = (L.sh.K + 127) / 128, n_rt = (L.rt.K + 127) / 128;
+    int KS = 1;
+    double best = 0.0;
+    for (int ks = 1; ks <= W4_WARPS; ks *= 2) {
+        const double groups = 2.0 * num_sms * W4_WARPS / ks;
+        const double l_sh = (n_sh + ks - 1) / ks + 3, l_rt = (n_rt + ks - 1) / ks + 3;
+        const double cost = (u_sh * l_sh + u_rt * l_rt) / groups + std::max(u_sh > 0 ? l_sh : 0.0, u_rt > 0 ? l_rt : 0.0);
+        if (ks == 1 || cost < best) {
+            best = cost;
+            KS = ks;
+        }
+    }
+    const double want = std::ceil((u_sh + u_rt) * KS / W4_WARPS);
+    const unsigned grid = (unsigned)std::max(1.0, std::min(want, 2.0 * num_sms));
+    return launch_k(L.name, w4_mma_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), smem, s, L, KS);
+}
+
+template <bool SWIGLU, int GS>
+static cudaError_t launch_w4_rows(const W4Launch& L, int num_sms, cudaStream_t s) {
+    // a slot has at most as many rows as there are tokens
+    const int64_t most = std::max<int64_t>(L.sh.wq ? L.rows_sh : 0, L.G > 0 ? std::min(L.T, L.rows_cap) : 0);
+    return most <= 8 ? launch_w4_mma<SWIGLU, GS, 1>(L, num_sms, s) : launch_w4_mma<SWIGLU, GS, 2>(L, num_sms, s);
+}
+
+template <bool SWIGLU>
+static cudaError_t launch_w4_group(const W4Launch& L, int num_sms, cudaStream_t s) {
+    if (L.group == 32) return launch_w4_rows<SWIGLU, 1>(L, num_sms, s);
+    if (L.group == 64) return launch_w4_rows<SWIGLU, 2>(L, num_sms, s);
+    return launch_w4_rows<SWIGLU, 4>(L, num_sms, s);
+}
+
 cudaError_t launch_w4_gemm(const W4Launch& L, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)num_sms * 8;
-    return launch_k(L.name, w4_gemm_kernel, dim3(grid), dim3(W4_WARPS * 32), 0, s, L);
+    return L.swiglu ? launch_w4_group<true>(L, num_sms, s) : launch_w4_group<false>(L, num_sms, s);
 }
 
 cudaError_t launch_w4_combine(const W4CombineLaunch& L, cudaStream_t s) {
