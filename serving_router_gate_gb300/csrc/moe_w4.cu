@@ -72,28 +72,40 @@ __host__ __device__ constexpr size_t w4_smem_bytes(int C) {
     return (size_t)W4_WARPS * (W4_RING * W4_STAGE + 2 * 32 * 8 * C * 4);
 }
 
-__device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
+__device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void w4_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void w4_cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t w4_lds32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+// n consecutive words of shared memory
+template <int n>
+__device__ __forceinline__ void w4_lds(uint32_t (&v)[n], uint32_t addr) {
+    if constexpr (n == 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                     : "r"(addr)
+                     : "memory");
+    else if constexpr (n == 2)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
 }
 
-// D += A B, A 16 x 16 (row), B 16 x 8 (column), bf16 inputs, fp32 sums
-__device__ __forceinline__ void w4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
+// D += A B (first: D = A B), A 16 x 16 (row), B 16 x 8 (column), bf16 inputs, fp32 sums
+__device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void w4_mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Elements 2j and 2j + 1 of a packed word as bf16 128 + (c + 8)
@@ -128,76 +140,90 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int K = u.p->K, N = u.p->N_out;
-    const int Kb = K / 2;
+    // this warp's stages: a contiguous range, so its rows' cache lines and scales follow each other
     const int nst_all = (K + 127) / 128;
-    const int nst = ks < nst_all ? (nst_all - ks + KS - 1) / KS : 0;
+    const int st0 = ks * nst_all / KS, nst = (ks + 1) * nst_all / KS - st0;
+    // elements past the range's last whole stage (a row may end inside a stage, at a group's end)
+    const int tail = min(K - (st0 + nst - 1) * 128, 128);
 
-    // this lane's share of the weight copies: row lane / 4 of each eight, 16-byte piece lane % 4
+    // weight copies: row lane / 4 of each eight, 16-byte piece lane % 4
     const uint8_t* wsrc[4];
     const uint16_t* ssrc[4];  // scales of accumulator rows g, g + 8 of both 16-row tiles
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        int r = u.n0 + i * 8 + (lane >> 2);
+        int r = u.n0 + i * 8 + g;
         if (SWIGLU)
             r = i < 2 ? r : r - 16 + N;  // tile 1: the up rows
         else
             r = min(r, N - 1);
-        wsrc[i] = u.wq + (int64_t)r * Kb + t * 16;
-        ssrc[i] = u.ws + (int64_t)r * (K / (32 * GS));
+        wsrc[i] = u.wq + (int64_t)r * (K / 2) + st0 * 64 + t * 16;
+        ssrc[i] = u.ws + (int64_t)r * (K / (32 * GS)) + st0 * NF;
     }
-    const uint32_t dst = ring + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
-    auto issue = [&](int i) {
-        const int k0 = (ks + i * KS) * 128;
-        const bool ok = i < nst && k0 + t * 32 < K;
-        const uint32_t d = dst + (i % W4_RING) * W4_STAGE;
+    // pieces rotate within a row so that the reads below meet every bank once
+    const int sw = ((g >> 1) & 1) * 2 + (g >> 2);
+    const uint32_t dst = ring + g * 64 + ((t ^ sw) << 4);
+    const int lane_nst = t * 32 < tail ? nst : nst - 1;  // stages that hold this lane's piece
+#define W4_ISSUE(i, off)                                                                                       \
+    do {                                                                                                       \
+        if ((i) < lane_nst) {                                                                                  \
+            _Pragma("unroll") for (int q_ = 0; q_ < 4; ++q_)                                                   \
+                w4_cp16(dst + ((off) % W4_RING) * W4_STAGE + q_ * 512, wsrc[q_] + (off) * 64);                 \
+        }                                                                                                      \
+        w4_cp_commit();                                                                                        \
+    } while (0)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w4_cp16(d + q * 512, wsrc[q] + (ok ? k0 / 2 : 0), ok);
-        w4_cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < W4_RING - 1; ++i) issue(i);
+    for (int i = 0; i < W4_RING - 1; ++i) W4_ISSUE(i, i);
 
     // activation rows of this lane's B columns (column g of each tile of eight)
     const uint16_t* xsrc[C];
-    bool xok[C];
+    int x_nst[C][NF];  // stages that hold the lane's elements of each group
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int col = c * 8 + g;
-        xok[c] = col < u.m;
-        int64_t xr = u.row0 + (xok[c] ? col : 0);
+        bool ok = col < u.m;
+        int64_t xr = u.row0 + (ok ? col : 0);
         if (u.routed && a.perm_src) {
             const int32_t p = a.perm_src[xr];
             if (p < 0 || (int64_t)p >= a.T * a.k) {
                 report(a.status, MOE_ERR_DEVICE_BOUNDS);
-                xok[c] = false;
+                ok = false;
                 xr = 0;
             } else {
                 xr = p / a.k;
             }
         }
-        xsrc[c] = u.p->x + xr * K + t * 8;
+        xsrc[c] = u.p->x + xr * K + st0 * 128 + t * 8 * GS;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) x_nst[c][f] = !ok ? 0 : f * 32 * GS < tail ? nst : nst - 1;
     }
     uint4 xb[C][4];
-    uint16_t sb[NF][4];
-    auto load_x = [&](int c, int j, int k0) {
-        xb[c][j] = xok[c] && k0 + j * 32 < K ? *reinterpret_cast<const uint4*>(xsrc[c] + k0 + j * 32)
-                                             : make_uint4(0, 0, 0, 0);
-    };
-    auto load_s = [&](int f, int k0) {
-        const bool ok = k0 + f * 32 * GS < K;
+    uint32_t sb[NF][4];
+#define W4_LOAD_X(i, off, f)                                                                                   \
+    do {                                                                                                       \
+        _Pragma("unroll") for (int c_ = 0; c_ < C; ++c_) {                                                     \
+            if ((i) < x_nst[c_][f]) {                                                                          \
+                _Pragma("unroll") for (int j_ = 0; j_ < GS; ++j_) xb[c_][(f) * GS + j_] =                      \
+                    *reinterpret_cast<const uint4*>(xsrc[c_] + (off) * 128 + (f) * 32 * GS + j_ * 8);          \
+            }                                                                                                  \
+        }                                                                                                      \
+    } while (0)
+#define W4_LOAD_S(i, off, f)                                                                                   \
+    do {                                                                                                       \
+        if ((i) < (NF == 1 || (f) * 32 * GS < tail ? nst : nst - 1)) {                                         \
+            _Pragma("unroll") for (int q_ = 0; q_ < 4; ++q_) sb[f][q_] = __ldg(ssrc[q_] + (off) * NF + (f));   \
+        }                                                                                                      \
+    } while (0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sb[f][i] = ok ? __ldg(ssrc[i] + k0 / (32 * GS) + f) : (uint16_t)0;
-    };
-    if (nst > 0) {
+    for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) xb[c][j] = make_uint4(0, 0, 0, 0);  // unused columns stay zero
 #pragma unroll
-            for (int c = 0; c < C; ++c) load_x(c, j, ks * 128);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) load_s(f, ks * 128);
+    for (int f = 0; f < NF; ++f) {
+        W4_LOAD_X(0, 0, f);
+        W4_LOAD_S(0, 0, f);
     }
 
-    float acc[2][C][4], tmp[2][C][4], xs[C][4];
+    float acc[2][C][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -205,68 +231,90 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[r][c][i] = 0.f;
 
-    const uint32_t rd = ring + g * 64 + t * 4;
-    const int sw = (g >> 1) & 3;
-    for (int i = 0; i < nst; ++i) {
-        issue(i + W4_RING - 1);
-        w4_cp_wait<W4_RING - 1>();
-        __syncwarp();
-        const int k0 = (ks + i * KS) * 128;
-        const int k1 = i + 1 < nst ? k0 + KS * 128 : K;  // the next stage's elements (K: none)
-        const uint32_t st = rd + (i % W4_RING) * W4_STAGE;
+    const uint32_t rd = ring + g * 64;
+    // the stages, four at a time so that every address is a register and a constant
+    for (int i0 = 0; i0 < nst; i0 += W4_RING) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (k0 + j * 32 < K) {
-                uint32_t w[4];
+        for (int v = 0; v < W4_RING; ++v) {
+            const int i = i0 + v;
+            if (i < nst) {
+                W4_ISSUE(i + W4_RING - 1, v + W4_RING - 1);
+                w4_cp_wait<W4_RING - 1>();
+                __syncwarp();
+                const int left = i + 1 < nst ? 128 : tail;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = w4_lds32(st + ((j ^ sw) << 4) + q * 512);
-                if (j % GS == 0) {
+                for (int f = 0; f < NF; ++f) {
+                    if (NF == 1 || f * 32 * GS < left) {
+                        // words 0 .. GS-1 of this lane in the group: elements t * 8 GS .. of the rows g + 8 q
+                        uint32_t w[4][GS];
 #pragma unroll
-                    for (int c = 0; c < C; ++c)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            tmp[0][c][e] = 0.f;
-                            tmp[1][c][e] = 0.f;
-                            xs[c][e] = 0.f;
+                        for (int q = 0; q < 4; ++q) {
+                            const int byte = f * 16 * GS;  // of the group in the row; the lane's at + t * 4 GS
+                            const uint32_t at = rd + v * W4_STAGE + q * 512 +
+                                                ((((byte + t * 4 * GS) >> 4) ^ sw) << 4) + ((t * 4 * GS) & 15);
+                            w4_lds<GS>(w[q], at);
                         }
-                }
+                        float tmp[2][C][4], xs[C][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t a00 = w4_pair(w[0], 2 * h), a01 = w4_pair(w[1], 2 * h),
-                                   a02 = w4_pair(w[0], 2 * h + 1), a03 = w4_pair(w[1], 2 * h + 1);
-                    const uint32_t a10 = w4_pair(w[2], 2 * h), a11 = w4_pair(w[3], 2 * h),
-                                   a12 = w4_pair(w[2], 2 * h + 1), a13 = w4_pair(w[3], 2 * h + 1);
+                        for (int j = 0; j < GS; ++j)
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const uint32_t b0 = h ? xb[c][j].z : xb[c][j].x, b1 = h ? xb[c][j].w : xb[c][j].y;
-                        w4_mma(tmp[0][c], a00, a01, a02, a03, b0, b1);
-                        w4_mma(tmp[1][c], a10, a11, a12, a13, b0, b1);
-                        w4_mma(xs[c], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, b0, b1);
-                    }
-                }
-                if ((j + 1) % GS == 0) {
-                    const int f = j / GS;
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t A[2][4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float s0 = bf16_bits_to_float(sb[f][2 * r]), s1 = bf16_bits_to_float(sb[f][2 * r + 1]);
+                                for (int r = 0; r < 2; ++r) {
+                                    A[r][0] = w4_pair(w[2 * r][j], 2 * h);
+                                    A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h);
+                                    A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1);
+                                    A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1);
+                                }
+                                const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            acc[r][c][0] = fmaf(s0, fmaf(-136.f, xs[c][0], tmp[r][c][0]), acc[r][c][0]);
-                            acc[r][c][1] = fmaf(s0, fmaf(-136.f, xs[c][1], tmp[r][c][1]), acc[r][c][1]);
-                            acc[r][c][2] = fmaf(s1, fmaf(-136.f, xs[c][0], tmp[r][c][2]), acc[r][c][2]);
-                            acc[r][c][3] = fmaf(s1, fmaf(-136.f, xs[c][1], tmp[r][c][3]), acc[r][c][3]);
+                                for (int c = 0; c < C; ++c) {
+                                    const uint4 b = xb[c][f * GS + j];
+                                    const uint32_t b0 = h ? b.z : b.x, b1 = h ? b.w : b.y;
+                                    if (j == 0 && h == 0) {
+                                        w4_mma_first(tmp[0][c], A[0], b0, b1);
+                                        w4_mma_first(tmp[1][c], A[1], b0, b1);
+                                        w4_mma_first(xs[c], one, b0, b1);
+                                    } else {
+                                        w4_mma(tmp[0][c], A[0], b0, b1);
+                                        w4_mma(tmp[1][c], A[1], b0, b1);
+                                        w4_mma(xs[c], one, b0, b1);
+                                    }
+                                }
+                            }
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float s0 = bf16_bits_to_float(sb[f][2 * r]);
+                            const float s1 = bf16_bits_to_float(sb[f][2 * r + 1]);
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                acc[r][c][0] = fmaf(s0, fmaf(-136.f, xs[c][0], tmp[r][c][0]), acc[r][c][0]);
+                                acc[r][c][1] = fmaf(s0, fmaf(-136.f, xs[c][1], tmp[r][c][1]), acc[r][c][1]);
+                                acc[r][c][2] = fmaf(s1, fmaf(-136.f, xs[c][0], tmp[r][c][2]), acc[r][c][2]);
+                                acc[r][c][3] = fmaf(s1, fmaf(-136.f, xs[c][1], tmp[r][c][3]), acc[r][c][3]);
+                            }
                         }
                     }
+                    // the same registers take the next stage's values
+                    W4_LOAD_X(i + 1, v + 1, f);
+                    W4_LOAD_S(i + 1, v + 1, f);
                 }
+                __syncwarp();  // the ring slot just read is the next one written
             }
-            // the same registers take the next stage's values
-#pragma unroll
-            for (int c = 0; c < C; ++c) load_x(c, j, k1);
-            if ((j + 1) % GS == 0) load_s(j / GS, k1);
         }
-        __syncwarp();  // the ring slot just read is the next one written
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            wsrc[q] += W4_RING * 64;
+            ssrc[q] += W4_RING * NF;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) xsrc[c] += W4_RING * 128;
     }
     w4_cp_wait<0>();
+#undef W4_ISSUE
+#undef W4_LOAD_X
+#undef W4_LOAD_S
 
     // partial sums of the group's warps, added in order of their K ranges
     float* mine = red + (buf * W4_WARPS + warp) * (32 * 8 * C);
