@@ -109,8 +109,11 @@ __device__ __forceinline__ void w4_mma_first(float (&d)[4], const uint32_t (&a)[
 }
 
 // Elements 2j and 2j + 1 of a packed word as bf16 128 + (c + 8)
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j) {
-    return ((word >> (4 * j)) & 0x000F000Fu) | 0x43004300u;
+// (magic: 0x43004300 in a register, which keeps mask and or one instruction).
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j, uint32_t magic) {
+    uint32_t v;
+    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(word >> (4 * j)), "r"(magic));
+    return v;
 }
 
 // The KS warps of a group (KS = 1: one warp) meet
@@ -134,7 +137,7 @@ struct W4Unit {
 
 template <bool SWIGLU, int GS, int C>
 __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, int KS, int ks, uint32_t ring,
-                                            float* red, int group_warp0, int group_id, int buf) {
+                                            float* red, int group_warp0, int group_id, int buf, uint32_t magic) {
     constexpr int TN = SWIGLU ? 16 : 32;
     constexpr int NF = 4 / GS;  // groups in a stage
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -262,10 +265,10 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
                                 uint32_t A[2][4];
 #pragma unroll
                                 for (int r = 0; r < 2; ++r) {
-                                    A[r][0] = w4_pair(w[2 * r][j], 2 * h);
-                                    A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h);
-                                    A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1);
-                                    A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1);
+                                    A[r][0] = w4_pair(w[2 * r][j], 2 * h, magic);
+                                    A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h, magic);
+                                    A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1, magic);
+                                    A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1, magic);
                                 }
                                 const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
@@ -349,7 +352,8 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
 }
 
 template <bool SWIGLU, int GS, int C>
-__global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_constant__ W4Launch a, int KS) {
+__global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_constant__ W4Launch a, int KS,
+                                                                uint32_t magic) {
     extern __shared__ __align__(128) uint8_t w4_smem[];
     __shared__ int32_t s_pre[W4_MAXG];  // units of the routed slots before each slot
     __shared__ int32_t s_part[W4_WARPS];
@@ -441,7 +445,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_cons
             u.m = (int)min((int64_t)(8 * C), end - u.row0);
             u.routed = true;
         }
-        w4_run_unit<SWIGLU, GS, C>(a, u, KS, ks, ring, red, grp * KS, grp + 1, buf);
+        w4_run_unit<SWIGLU, GS, C>(a, u, KS, ks, ring, red, grp * KS, grp + 1, buf, magic);
     }
 }
 
@@ -558,7 +562,8 @@ static cudaError_t launch_w4_mma(const W4Launch& L, int num_sms, cudaStream_t s)
     }
     const double want = std::ceil((u_sh + u_rt) * KS / W4_WARPS);
     const unsigned grid = (unsigned)std::max(1.0, std::min(want, 2.0 * num_sms));
-    return launch_k(L.name, w4_mma_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), smem, s, L, KS);
+    return launch_k(L.name, w4_mma_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), smem, s, L, KS,
+                    0x43004300u);
 }
 
 template <bool SWIGLU, int GS>
