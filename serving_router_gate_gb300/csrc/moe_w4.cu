@@ -7,11 +7,9 @@
 // (moe_forward_w4: FC1 + SwiGLU, FC2, weighted combine, an optional shared expert).
 //
 // Packing: eight consecutive elements of a row share a 32-bit word (little-endian),
-// element 2i in nibble i and element 2i + 1 in nibble i + 4, each as c + 8.  Masking
-// a word shifted by 4i with 0x000F000F leaves elements 2i and 2i + 1 in the two
-// 16-bit halves, and or-ing 0x4300 into each makes them the bf16 values 128 + (c + 8)
-// (exact: bf16 has seven fraction bits), in the order in which the activations lie
-// in memory.
+// element 2i in nibble i and element 2i + 1 in nibble i + 4, each as c + 8: a mask
+// leaves elements 2i and 2i + 1 in the two 16-bit halves, in the order in which the
+// activations lie in memory.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -108,11 +106,17 @@ __device__ __forceinline__ void w4_mma_first(float (&d)[4], const uint32_t (&a)[
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Elements 2j and 2j + 1 of a packed word as bf16 128 + (c + 8)
-// (magic: 0x43004300 in a register, which keeps mask and or one instruction).
-__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j, uint32_t magic) {
+// Elements 2j and 2j + 1 of a packed word as bf16 c / 64.  With a nibble n = c + 8 at
+// bits 0-3 or 4-7 of a half, the half read as bf16 is n 2^-133 or n 2^-129: exponent
+// fields 0 and 1 are one linear range (the lower one subnormal).  One fused
+// multiply-add brings it to n / 64 - 8 / 64, exactly, on the FMA pipe; the ALU pipe,
+// which the masks keep busiest, has five instructions a word.
+__device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j) {
+    const uint32_t n = (j & 2 ? word >> 8 : word) & (j & 1 ? 0x00F000F0u : 0x000F000Fu);
     uint32_t v;
-    asm("lop3.b32 %0, %1, 0x000F000F, %2, 0xEA;" : "=r"(v) : "r"(word >> (4 * j)), "r"(magic));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(v)
+        : "r"(n), "r"(j & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(0xBE00BE00u));  // 2^123 or 2^127, -1/8
     return v;
 }
 
@@ -137,7 +141,7 @@ struct W4Unit {
 
 template <bool SWIGLU, int GS, int C>
 __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, int KS, int ks, uint32_t ring,
-                                            float* red, int group_warp0, int group_id, int buf, uint32_t magic) {
+                                            float* red, int group_warp0, int group_id, int buf) {
     constexpr int TN = SWIGLU ? 16 : 32;
     constexpr int NF = 4 / GS;  // groups in a stage
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -257,7 +261,7 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
                                                 ((((byte + t * 4 * GS) >> 4) ^ sw) << 4) + ((t * 4 * GS) & 15);
                             w4_lds<GS>(w[q], at);
                         }
-                        float tmp[2][C][4], xs[C][4];
+                        float tmp[2][C][4];
 #pragma unroll
                         for (int j = 0; j < GS; ++j)
 #pragma unroll
@@ -265,12 +269,11 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
                                 uint32_t A[2][4];
 #pragma unroll
                                 for (int r = 0; r < 2; ++r) {
-                                    A[r][0] = w4_pair(w[2 * r][j], 2 * h, magic);
-                                    A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h, magic);
-                                    A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1, magic);
-                                    A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1, magic);
+                                    A[r][0] = w4_pair(w[2 * r][j], 2 * h);
+                                    A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h);
+                                    A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1);
+                                    A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1);
                                 }
-                                const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
                                 for (int c = 0; c < C; ++c) {
                                     const uint4 b = xb[c][f * GS + j];
@@ -278,11 +281,9 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
                                     if (j == 0 && h == 0) {
                                         w4_mma_first(tmp[0][c], A[0], b0, b1);
                                         w4_mma_first(tmp[1][c], A[1], b0, b1);
-                                        w4_mma_first(xs[c], one, b0, b1);
                                     } else {
                                         w4_mma(tmp[0][c], A[0], b0, b1);
                                         w4_mma(tmp[1][c], A[1], b0, b1);
-                                        w4_mma(xs[c], one, b0, b1);
                                     }
                                 }
                             }
@@ -292,10 +293,10 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
                             const float s1 = bf16_bits_to_float(sb[f][2 * r + 1]);
 #pragma unroll
                             for (int c = 0; c < C; ++c) {
-                                acc[r][c][0] = fmaf(s0, fmaf(-136.f, xs[c][0], tmp[r][c][0]), acc[r][c][0]);
-                                acc[r][c][1] = fmaf(s0, fmaf(-136.f, xs[c][1], tmp[r][c][1]), acc[r][c][1]);
-                                acc[r][c][2] = fmaf(s1, fmaf(-136.f, xs[c][0], tmp[r][c][2]), acc[r][c][2]);
-                                acc[r][c][3] = fmaf(s1, fmaf(-136.f, xs[c][1], tmp[r][c][3]), acc[r][c][3]);
+                                acc[r][c][0] = fmaf(s0, tmp[r][c][0], acc[r][c][0]);
+                                acc[r][c][1] = fmaf(s0, tmp[r][c][1], acc[r][c][1]);
+                                acc[r][c][2] = fmaf(s1, tmp[r][c][2], acc[r][c][2]);
+                                acc[r][c][3] = fmaf(s1, tmp[r][c][3], acc[r][c][3]);
                             }
                         }
                     }
@@ -326,8 +327,8 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float* p = mine + (r * 16 + g) * (8 * C) + c * 8 + 2 * t;
-            *reinterpret_cast<float2*>(p) = make_float2(acc[r][c][0], acc[r][c][1]);
-            *reinterpret_cast<float2*>(p + 8 * 8 * C) = make_float2(acc[r][c][2], acc[r][c][3]);
+            *reinterpret_cast<float2*>(p) = make_float2(64.f * acc[r][c][0], 64.f * acc[r][c][1]);
+            *reinterpret_cast<float2*>(p + 8 * 8 * C) = make_float2(64.f * acc[r][c][2], 64.f * acc[r][c][3]);
         }
     w4_group_sync(group_id, KS);
     const float* all = red + (buf * W4_WARPS + group_warp0) * (32 * 8 * C);
@@ -352,8 +353,7 @@ __device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, 
 }
 
 template <bool SWIGLU, int GS, int C>
-__global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_constant__ W4Launch a, int KS,
-                                                                uint32_t magic) {
+__global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_constant__ W4Launch a, int KS) {
     extern __shared__ __align__(128) uint8_t w4_smem[];
     __shared__ int32_t s_pre[W4_MAXG];  // units of the routed slots before each slot
     __shared__ int32_t s_part[W4_WARPS];
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_cons
             u.m = (int)min((int64_t)(8 * C), end - u.row0);
             u.routed = true;
         }
-        w4_run_unit<SWIGLU, GS, C>(a, u, KS, ks, ring, red, grp * KS, grp + 1, buf, magic);
+        w4_run_unit<SWIGLU, GS, C>(a, u, KS, ks, ring, red, grp * KS, grp + 1, buf);
     }
 }
 
@@ -562,8 +562,7 @@ static cudaError_t launch_w4_mma(const W4Launch& L, int num_sms, cudaStream_t s)
     }
     const double want = std::ceil((u_sh + u_rt) * KS / W4_WARPS);
     const unsigned grid = (unsigned)std::max(1.0, std::min(want, 2.0 * num_sms));
-    return launch_k(L.name, w4_mma_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), smem, s, L, KS,
-                    0x43004300u);
+    return launch_k(L.name, w4_mma_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), smem, s, L, KS);
 }
 
 template <bool SWIGLU, int GS>
