@@ -817,6 +817,8 @@ moe_status_t moe_forward_w4(const moe_bf16_t* x, const int32_t* offsets, int S_l
         !w4_group_ok(I, group) || (I_shared_total > 0 && !w4_group_ok(I_shared_total, group)) || k > 32 ||
         S_local > 1024 || P_cap >= (int64_t(1) << 31) || T * (int64_t)k >= (int64_t(1) << 31))
         return MOE_ERR_UNSUPPORTED;
+    // the product kernels count 16-output tiles of 8-row pieces in 32 bits
+    if ((P_cap / 8 + S_local) * (std::max(H, I) / 16) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !offsets || !perm_src || !W1q || !W1_scale || !W2q || !W2_scale || !pair_row || !out)
         return MOE_ERR_INVALID_ARG;
@@ -858,6 +860,7 @@ moe_status_t moe_forward_w4(const moe_bf16_t* x, const int32_t* offsets, int S_l
     L.name = "w4_fc2";
     L.swiglu = false;
     L.perm_src = nullptr;
+    L.early = true;  // FC1 waited for whatever wrote the tables before it let FC2 start
     L.rt = {h, W2q, W2_scale, I, H, nullptr, y};
     if (I_shared_total > 0) L.sh = {h_sh, W2sq, W2s_scale, I_shared_total, H, nullptr, y_sh};
     st = cuda_status(launch_w4_gemm(L, sms, s));

@@ -646,6 +646,9 @@ struct W4Launch {
     // dense problem on rows_sh rows (wq null: none)
     W4Problem sh;
     int64_t rows_sh = 0;
+    // offsets and weights were written before the previous kernel on the stream began, so
+    // only the A rows wait for it
+    bool early = false;
     int32_t* status = nullptr;
 };
 cudaError_t launch_w4_gemm(const W4Launch& L, int num_sms, cudaStream_t s);

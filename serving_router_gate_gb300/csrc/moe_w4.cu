@@ -56,19 +56,40 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 }
 
 // ---------------------------------------------------------------------------
-// Products on mma.sync: a warp owns 32 weight rows (FC1: 16 gate and the matching
-// 16 up rows) times up to 8 C activation rows
+// Products on mma.sync.  The work is a list of tiles, 32 weight rows of one slot
+// (FC1: 16 gate rows and the matching 16 up rows) times up to 8 C activation rows;
+// a tile's K is cut into stages of 128.  One CTA per SM takes a contiguous range of
+// the list, about the same number of stages each, and its 16 warps take equal
+// contiguous ranges of those stages, whatever tiles they fall into.  A warp streams
+// its stages through a ring of its own without a break at a tile's end; it stores
+// the tiles that are all its own, and leaves its part of the at most two that it
+// shares with its neighbours in shared memory, where the warp that ends a tile adds
+// the parts in stage order.
 // ---------------------------------------------------------------------------
-constexpr int W4_THREADS = 256;
-constexpr int W4_WARPS = W4_THREADS / 32;
-constexpr int W4_RING = 4;           // stages of 128 elements x 32 rows in each warp's ring
-constexpr int W4_STAGE = 2048;       // bytes of a stage
-constexpr int W4_MAXG = 1024;        // slots
+constexpr int W4_STAGE = 2048;  // bytes of a stage: 32 rows of 128 elements
+constexpr int W4_MAXG = 1024;   // slots
+
+// The narrow kernel (C = 1) runs 16 warps: eight columns leave the tensor cores idle and
+// the masks and the multiply-adds that widen the codes bound it, which more warps hide.
+// The wide one (C = 4) keeps four column tiles of sums and activations in the registers
+// of 8 warps.  Both have 128 KB of weights in their rings.
+__host__ __device__ constexpr int w4_warps(int C) { return C == 1 ? 16 : 8; }
+__host__ __device__ constexpr int w4_ring(int C) { return 64 / w4_warps(C); }  // stages in each warp's ring
 
 __host__ __device__ constexpr size_t w4_smem_bytes(int C) {
-    // ring of every warp, then two buffers of 32 x 8 C partial sums per warp
-    return (size_t)W4_WARPS * (W4_RING * W4_STAGE + 2 * 32 * 8 * C * 4);
+    // every warp's ring, then its parts of two shared tiles (16 C sums a lane)
+    return (size_t)w4_warps(C) * (w4_ring(C) * W4_STAGE + 2 * 32 * 8 * C * 4);
 }
+
+struct W4Tile {
+    const uint8_t* wq;   // packed weights and scales of its first row
+    const uint16_t* ws;
+    int64_t row0;        // first output row
+    int n0, m;           // first output, rows
+    int ct;              // row tiles of its slot
+    int x;               // where its activation rows stand
+    bool routed;
+};
 
 __device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -120,267 +141,125 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j) {
     return v;
 }
 
-// The KS warps of a group (KS = 1: one warp) meet
-__device__ __forceinline__ void w4_group_sync(int id, int KS) {
-    if (KS == 1)
-        __syncwarp();
-    else
-        asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(KS * 32) : "memory");
-}
-
-// One unit: 32 weight rows of one slot times m <= 8 C activation rows.
-struct W4Unit {
-    const W4Problem* p;
-    const uint8_t* wq;      // the slot's packed weights
-    const uint16_t* ws;     // and scales
-    int n0;                 // first output
-    int64_t row0;           // first output row
-    int m;                  // rows
-    bool routed;
-};
-
-template <bool SWIGLU, int GS, int C>
-__device__ __forceinline__ void w4_run_unit(const W4Launch& a, const W4Unit& u, int KS, int ks, uint32_t ring,
-                                            float* red, int group_warp0, int group_id, int buf) {
-    constexpr int TN = SWIGLU ? 16 : 32;
-    constexpr int NF = 4 / GS;  // groups in a stage
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, t = lane & 3;
-    const int K = u.p->K, N = u.p->N_out;
-    // this warp's stages: a contiguous range, so its rows' cache lines and scales follow each other
-    const int nst_all = (K + 127) / 128;
-    const int st0 = ks * nst_all / KS, nst = (ks + 1) * nst_all / KS - st0;
-    // elements past the range's last whole stage (a row may end inside a stage, at a group's end)
-    const int tail = min(K - (st0 + nst - 1) * 128, 128);
-
-    // weight copies: row lane / 4 of each eight, 16-byte piece lane % 4
-    const uint8_t* wsrc[4];
-    const uint16_t* ssrc[4];  // scales of accumulator rows g, g + 8 of both 16-row tiles
+// One group of a stage: acc += scales * (codes x activations), C8 of the C column tiles
+// of eight.  w: the lane's words of rows g + 8 q, xb: its activations, [column tile][4].
+template <int GS, int C8, int C>
+__device__ __forceinline__ void w4_group(float (&acc)[2][C][4], const uint32_t (&w)[4][GS], const uint4* xb,
+                                         const uint32_t (&sb)[4]) {
+    float tmp[2][C8][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        int r = u.n0 + i * 8 + g;
-        if (SWIGLU)
-            r = i < 2 ? r : r - 16 + N;  // tile 1: the up rows
-        else
-            r = min(r, N - 1);
-        wsrc[i] = u.wq + (int64_t)r * (K / 2) + st0 * 64 + t * 16;
-        ssrc[i] = u.ws + (int64_t)r * (K / (32 * GS)) + st0 * NF;
-    }
-    // pieces rotate within a row so that the reads below meet every bank once
-    const int sw = ((g >> 1) & 1) * 2 + (g >> 2);
-    const uint32_t dst = ring + g * 64 + ((t ^ sw) << 4);
-    const int lane_nst = t * 32 < tail ? nst : nst - 1;  // stages that hold this lane's piece
-#define W4_ISSUE(i, off)                                                                                       \
-    do {                                                                                                       \
-        if ((i) < lane_nst) {                                                                                  \
-            _Pragma("unroll") for (int q_ = 0; q_ < 4; ++q_)                                                   \
-                w4_cp16(dst + ((off) % W4_RING) * W4_STAGE + q_ * 512, wsrc[q_] + (off) * 64);                 \
-        }                                                                                                      \
-        w4_cp_commit();                                                                                        \
-    } while (0)
+    for (int j = 0; j < GS; ++j)
 #pragma unroll
-    for (int i = 0; i < W4_RING - 1; ++i) W4_ISSUE(i, i);
-
-    // activation rows of this lane's B columns (column g of each tile of eight)
-    const uint16_t* xsrc[C];
-    int x_nst[C][NF];  // stages that hold the lane's elements of each group
+        for (int h = 0; h < 2; ++h) {
+            uint32_t A[2][4];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int col = c * 8 + g;
-        bool ok = col < u.m;
-        int64_t xr = u.row0 + (ok ? col : 0);
-        if (u.routed && a.perm_src) {
-            const int32_t p = a.perm_src[xr];
-            if (p < 0 || (int64_t)p >= a.T * a.k) {
-                report(a.status, MOE_ERR_DEVICE_BOUNDS);
-                ok = false;
-                xr = 0;
-            } else {
-                xr = p / a.k;
+            for (int r = 0; r < 2; ++r) {
+                A[r][0] = w4_pair(w[2 * r][j], 2 * h);
+                A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h);
+                A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1);
+                A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1);
+            }
+#pragma unroll
+            for (int c = 0; c < C8; ++c) {
+                const uint4 b = xb[c * 4 + j];
+                const uint32_t b0 = h ? b.z : b.x, b1 = h ? b.w : b.y;
+                if (j == 0 && h == 0) {
+                    w4_mma_first(tmp[0][c], A[0], b0, b1);
+                    w4_mma_first(tmp[1][c], A[1], b0, b1);
+                } else {
+                    w4_mma(tmp[0][c], A[0], b0, b1);
+                    w4_mma(tmp[1][c], A[1], b0, b1);
+                }
             }
         }
-        xsrc[c] = u.p->x + xr * K + st0 * 128 + t * 8 * GS;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) x_nst[c][f] = !ok ? 0 : f * 32 * GS < tail ? nst : nst - 1;
+    for (int r = 0; r < 2; ++r) {
+        const float s0 = bf16_bits_to_float(sb[2 * r]), s1 = bf16_bits_to_float(sb[2 * r + 1]);
+#pragma unroll
+        for (int c = 0; c < C8; ++c) {
+            acc[r][c][0] = fmaf(s0, tmp[r][c][0], acc[r][c][0]);
+            acc[r][c][1] = fmaf(s0, tmp[r][c][1], acc[r][c][1]);
+            acc[r][c][2] = fmaf(s1, tmp[r][c][2], acc[r][c][2]);
+            acc[r][c][3] = fmaf(s1, tmp[r][c][3], acc[r][c][3]);
+        }
     }
-    uint4 xb[C][4];
-    uint32_t sb[NF][4];
-#define W4_LOAD_X(i, off, f)                                                                                   \
-    do {                                                                                                       \
-        _Pragma("unroll") for (int c_ = 0; c_ < C; ++c_) {                                                     \
-            if ((i) < x_nst[c_][f]) {                                                                          \
-                _Pragma("unroll") for (int j_ = 0; j_ < GS; ++j_) xb[c_][(f) * GS + j_] =                      \
-                    *reinterpret_cast<const uint4*>(xsrc[c_] + (off) * 128 + (f) * 32 * GS + j_ * 8);          \
-            }                                                                                                  \
-        }                                                                                                      \
-    } while (0)
-#define W4_LOAD_S(i, off, f)                                                                                   \
-    do {                                                                                                       \
-        if ((i) < (NF == 1 || (f) * 32 * GS < tail ? nst : nst - 1)) {                                         \
-            _Pragma("unroll") for (int q_ = 0; q_ < 4; ++q_) sb[f][q_] = __ldg(ssrc[q_] + (off) * NF + (f));   \
-        }                                                                                                      \
-    } while (0)
+}
+
+// The outputs of a tile from its accumulators: this lane has rows g, g + 8 of both
+// 16-row halves and columns 2t, 2t + 1 of every eight.
+template <bool SWIGLU, int C>
+__device__ __forceinline__ void w4_store(const W4Problem& p, const W4Tile& d, const float (&acc)[2][C][4]) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const int64_t N = p.N_out;
+    auto put = [&](int64_t at, float v) {
+        if (p.out_f32)
+            p.out_f32[at] = v;
+        else
+            p.out_bf16[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
+    };
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) xb[c][j] = make_uint4(0, 0, 0, 0);  // unused columns stay zero
+        for (int e = 0; e < 2; ++e) {
+            const int col = c * 8 + 2 * t + e;
+            if (col >= d.m) continue;
+            const int64_t at = (d.row0 + col) * N + d.n0 + g;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        W4_LOAD_X(0, 0, f);
-        W4_LOAD_S(0, 0, f);
-    }
-
-    float acc[2][C][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][c][i] = 0.f;
-
-    const uint32_t rd = ring + g * 64;
-    // the stages, four at a time so that every address is a register and a constant
-    for (int i0 = 0; i0 < nst; i0 += W4_RING) {
-#pragma unroll
-        for (int v = 0; v < W4_RING; ++v) {
-            const int i = i0 + v;
-            if (i < nst) {
-                W4_ISSUE(i + W4_RING - 1, v + W4_RING - 1);
-                w4_cp_wait<W4_RING - 1>();
-                __syncwarp();
-                const int left = i + 1 < nst ? 128 : tail;
-#pragma unroll
-                for (int f = 0; f < NF; ++f) {
-                    if (NF == 1 || f * 32 * GS < left) {
-                        // words 0 .. GS-1 of this lane in the group: elements t * 8 GS .. of the rows g + 8 q
-                        uint32_t w[4][GS];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int byte = f * 16 * GS;  // of the group in the row; the lane's at + t * 4 GS
-                            const uint32_t at = rd + v * W4_STAGE + q * 512 +
-                                                ((((byte + t * 4 * GS) >> 4) ^ sw) << 4) + ((t * 4 * GS) & 15);
-                            w4_lds<GS>(w[q], at);
-                        }
-                        float tmp[2][C][4];
-#pragma unroll
-                        for (int j = 0; j < GS; ++j)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                uint32_t A[2][4];
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    A[r][0] = w4_pair(w[2 * r][j], 2 * h);
-                                    A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h);
-                                    A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1);
-                                    A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1);
-                                }
-#pragma unroll
-                                for (int c = 0; c < C; ++c) {
-                                    const uint4 b = xb[c][f * GS + j];
-                                    const uint32_t b0 = h ? b.z : b.x, b1 = h ? b.w : b.y;
-                                    if (j == 0 && h == 0) {
-                                        w4_mma_first(tmp[0][c], A[0], b0, b1);
-                                        w4_mma_first(tmp[1][c], A[1], b0, b1);
-                                    } else {
-                                        w4_mma(tmp[0][c], A[0], b0, b1);
-                                        w4_mma(tmp[1][c], A[1], b0, b1);
-                                    }
-                                }
-                            }
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const float s0 = bf16_bits_to_float(sb[f][2 * r]);
-                            const float s1 = bf16_bits_to_float(sb[f][2 * r + 1]);
-#pragma unroll
-                            for (int c = 0; c < C; ++c) {
-                                acc[r][c][0] = fmaf(s0, tmp[r][c][0], acc[r][c][0]);
-                                acc[r][c][1] = fmaf(s0, tmp[r][c][1], acc[r][c][1]);
-                                acc[r][c][2] = fmaf(s1, tmp[r][c][2], acc[r][c][2]);
-                                acc[r][c][3] = fmaf(s1, tmp[r][c][3], acc[r][c][3]);
-                            }
-                        }
-                    }
-                    // the same registers take the next stage's values
-                    W4_LOAD_X(i + 1, v + 1, f);
-                    W4_LOAD_S(i + 1, v + 1, f);
+            for (int h = 0; h < 2; ++h) {
+                // the codes were c / 64
+                const float v0 = 64.f * acc[0][c][2 * h + e], v1 = 64.f * acc[1][c][2 * h + e];
+                if (SWIGLU) {
+                    put(at + 8 * h, v0 / (1.0f + expf(-v0)) * v1);
+                } else {
+                    if (d.n0 + 8 * h + g < N) put(at + 8 * h, v0);
+                    if (d.n0 + 16 + 8 * h + g < N) put(at + 16 + 8 * h, v1);
                 }
-                __syncwarp();  // the ring slot just read is the next one written
             }
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            wsrc[q] += W4_RING * 64;
-            ssrc[q] += W4_RING * NF;
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) xsrc[c] += W4_RING * 128;
-    }
-    w4_cp_wait<0>();
-#undef W4_ISSUE
-#undef W4_LOAD_X
-#undef W4_LOAD_S
-
-    // partial sums of the group's warps, added in order of their K ranges
-    float* mine = red + (buf * W4_WARPS + warp) * (32 * 8 * C);
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            float* p = mine + (r * 16 + g) * (8 * C) + c * 8 + 2 * t;
-            *reinterpret_cast<float2*>(p) = make_float2(64.f * acc[r][c][0], 64.f * acc[r][c][1]);
-            *reinterpret_cast<float2*>(p + 8 * 8 * C) = make_float2(64.f * acc[r][c][2], 64.f * acc[r][c][3]);
-        }
-    w4_group_sync(group_id, KS);
-    const float* all = red + (buf * W4_WARPS + group_warp0) * (32 * 8 * C);
-    for (int o = ks * 32 + lane; o < TN * u.m; o += KS * 32) {
-        const int f = o % TN, col = o / TN;
-        float v = 0.f, up = 0.f;
-        for (int q = 0; q < KS; ++q) {
-            const float* p = all + q * (32 * 8 * C);
-            v += p[f * (8 * C) + col];
-            if (SWIGLU) up += p[(16 + f) * (8 * C) + col];
-        }
-        if (SWIGLU) v = v / (1.0f + expf(-v)) * up;
-        const int n = u.n0 + f;
-        if (n < N) {
-            const int64_t at = (u.row0 + col) * N + n;
-            if (u.p->out_f32)
-                u.p->out_f32[at] = v;
-            else
-                u.p->out_bf16[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
-        }
-    }
 }
 
 template <bool SWIGLU, int GS, int C>
-__global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_constant__ W4Launch a, int KS) {
+__global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_constant__ W4Launch a) {
+    constexpr int WARPS = w4_warps(C), RING = w4_ring(C);
+    constexpr int TILES = 2 * RING;  // tiles a warp has in hand: the copies run RING - 1 stages ahead
     extern __shared__ __align__(128) uint8_t w4_smem[];
-    __shared__ int32_t s_pre[W4_MAXG];  // units of the routed slots before each slot
-    __shared__ int32_t s_part[W4_WARPS];
-    constexpr int TN = SWIGLU ? 16 : 32;
+    __shared__ int32_t s_pre[W4_MAXG];  // routed tiles before each slot
+    __shared__ int32_t s_part[WARPS];
+    __shared__ W4Tile s_tile[WARPS][TILES];
+    __shared__ int32_t s_x[WARPS][TILES][8 * C];  // activation row of each column, -1: none
+    constexpr int TN = SWIGLU ? 16 : 32;                // outputs of a tile
+    constexpr int NF = 4 / GS;                          // groups in a stage
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t ring = smem_u32(w4_smem) + warp * (W4_RING * W4_STAGE);
-    float* red = reinterpret_cast<float*>(w4_smem + W4_WARPS * W4_RING * W4_STAGE);
-    pdl_wait();
-    pdl_trigger();
+    const int g = lane >> 2, t = lane & 3;
+    // pieces rotate within a row of a stage so that the reads below meet every bank once
+    const int sw = ((g >> 1) & 1) * 2 + (g >> 2);
+    const uint32_t ring = smem_u32(w4_smem) + warp * (RING * W4_STAGE) + g * 64;
+    // part [warp][0: of a tile begun by an earlier warp, 1: of one begun here][4 values][lane]
+    float4* parts = reinterpret_cast<float4*>(w4_smem + WARPS * RING * W4_STAGE);
+    if (!a.early) {
+        pdl_wait();
+        pdl_trigger();
+    }
 
-    const int tiles_sh = a.sh.wq ? (a.sh.N_out + TN - 1) / TN : 0;
+    // the list: the dense problem's tiles, then the routed ones by slot; the row tiles of
+    // one weight tile are neighbours
     const int ct_sh = (int)((a.rows_sh + 8 * C - 1) / (8 * C));
-    const int units_sh = tiles_sh * ct_sh;
-    const int tiles = a.G > 0 ? (a.rt.N_out + TN - 1) / TN : 0;
-    int units = units_sh;
+    const int n_sh = (a.sh.K + 127) / 128, n_rt = (a.rt.K + 127) / 128;  // stages of a tile
+    const int tiles_rt = (a.rt.N_out + TN - 1) / TN;
+    const int64_t list_sh = a.sh.wq ? (int64_t)((a.sh.N_out + TN - 1) / TN) * ct_sh : 0;
+    int64_t list_rt = 0;
     if (a.G > 0) {
-        // exclusive scan of the slots' units, four slots a thread
-        const int s0 = threadIdx.x * (W4_MAXG / W4_THREADS);
-        int n[W4_MAXG / W4_THREADS], sum = 0;
+        constexpr int PER = W4_MAXG / (WARPS * 32);
+        const int s0 = threadIdx.x * PER;
+        int n[PER], sum = 0;
         int64_t lo = s0 <= a.G ? __ldg(a.offsets + s0) : 0;
 #pragma unroll
-        for (int i = 0; i < W4_MAXG / W4_THREADS; ++i) {
+        for (int i = 0; i < PER; ++i) {
             n[i] = 0;
             if (s0 + i < a.G) {
                 const int64_t hi = __ldg(a.offsets + s0 + i + 1);
                 const int64_t m = max((int64_t)0, min(hi, a.rows_cap) - max(lo, (int64_t)0));
-                n[i] = (int)((m + 8 * C - 1) / (8 * C)) * tiles;
+                n[i] = (int)((m + 8 * C - 1) / (8 * C)) * tiles_rt;
                 lo = hi;
             }
             sum += n[i];
@@ -395,57 +274,318 @@ __global__ void __launch_bounds__(W4_THREADS, 2) w4_mma_kernel(const __grid_cons
         __syncthreads();
         int base = inc - sum, total = 0;
 #pragma unroll
-        for (int w = 0; w < W4_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             base += w < warp ? s_part[w] : 0;
             total += s_part[w];
         }
 #pragma unroll
-        for (int i = 0; i < W4_MAXG / W4_THREADS; ++i) {
+        for (int i = 0; i < PER; ++i) {
             if (s0 + i < a.G) s_pre[s0 + i] = base;
             base += n[i];
         }
-        units += total;
+        list_rt = total;
         __syncthreads();
     }
+    // this CTA's tiles: from the first that starts at or after its share of the stages
+    const int64_t stages_sh = list_sh * n_sh, stages = stages_sh + list_rt * n_rt;
+    auto first_tile = [&](int64_t cta) {
+        const int64_t s = stages * cta / gridDim.x;
+        return s <= stages_sh ? (n_sh ? (s + n_sh - 1) / n_sh : 0) : list_sh + (s - stages_sh + n_rt - 1) / n_rt;
+    };
+    auto start_of = [&](int64_t v) { return v <= list_sh ? v * n_sh : stages_sh + (v - list_sh) * n_rt; };
+    const int64_t base = start_of(first_tile(blockIdx.x));
+    const int64_t all = start_of(first_tile(blockIdx.x + 1)) - base;
+    // this warp's stages: cnt from lo; the first one's tile
+    const int64_t lo = base + all * warp / WARPS;
+    const int cnt = (int)(base + all * (warp + 1) / WARPS - lo);
+    const int64_t v0 = lo < stages_sh ? lo / n_sh : list_sh + (n_rt ? (lo - stages_sh) / n_rt : 0);
 
-    const int groups = W4_WARPS / KS;
-    const int grp = warp / KS, ks = warp - grp * KS;
-    int buf = 0;
-    for (int64_t v = (int64_t)grp * gridDim.x + blockIdx.x; v < units; v += (int64_t)groups * gridDim.x, buf ^= 1) {
-        W4Unit u;
-        if (v < units_sh) {
-            const int c = (int)v % ct_sh;
-            u.p = &a.sh;
-            u.wq = a.sh.wq;
-            u.ws = a.sh.ws;
-            u.n0 = ((int)v / ct_sh) * TN;
-            u.row0 = (int64_t)c * 8 * C;
-            u.m = (int)min((int64_t)(8 * C), a.rows_sh - u.row0);
-            u.routed = false;
-        } else {
-            const int w = (int)v - units_sh;
-            int lo = 0, hi = a.G - 1;  // the last slot whose units begin at or before w
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) / 2;
-                if (s_pre[mid] <= w)
-                    lo = mid;
-                else
-                    hi = mid - 1;
+    // Three cursors run over the stages: the copies three ahead, the activations and
+    // scales one ahead, the products.  Tile i from v0 is at s_tile[warp][i % TILES]
+    // from when the copies reach it; ends count from lo.  (The loop is not unrolled over
+    // the ring: four copies of what a tile's end takes overran the instruction cache,
+    // 3 of 8 stalled cycles.)
+    W4Tile* tiles = s_tile[warp];
+    auto end_of = [&](int i) { return (int)(start_of(v0 + i + 1) - lo); };
+    int xs = 0;  // activation row sets so far
+    auto locate = [&](int i) {
+        W4Tile d;
+        const int64_t v = v0 + i;
+        if (i > 0) {
+            d = tiles[(i - 1) % TILES];
+            const W4Problem& p = d.routed ? a.rt : a.sh;
+            if (d.ct == 1 && d.n0 + TN < p.N_out) {  // the same rows, the next weights
+                d.n0 += TN;
+                d.wq += (int64_t)TN * (p.K / 2);
+                d.ws += (int64_t)TN * (p.K / (32 * GS));
+                __syncwarp();
+                if (lane == 0) tiles[i % TILES] = d;
+                __syncwarp();
+                return;
             }
-            const int64_t first = max(0, __ldg(a.offsets + lo));
-            const int64_t end = min((int64_t)__ldg(a.offsets + lo + 1), a.rows_cap);
-            const int ct = (int)((end - first + 8 * C - 1) / (8 * C));
-            const int q = w - s_pre[lo];
-            const int64_t wrows = SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out;
-            u.p = &a.rt;
-            u.wq = a.rt.wq + lo * wrows * (a.rt.K / 2);
-            u.ws = a.rt.ws + lo * wrows * (a.rt.K / (32 * GS));
-            u.n0 = (q / ct) * TN;
-            u.row0 = first + (int64_t)(q % ct) * 8 * C;
-            u.m = (int)min((int64_t)(8 * C), end - u.row0);
-            u.routed = true;
         }
-        w4_run_unit<SWIGLU, GS, C>(a, u, KS, ks, ring, red, grp * KS, grp + 1, buf);
+        int64_t rows, at;  // the slot's end, its first weight row
+        int q;             // tile of the slot
+        if (v < list_sh) {
+            q = (int)v;
+            d.routed = false;
+            d.ct = ct_sh;
+            d.row0 = 0;
+            rows = a.rows_sh;
+            at = 0;
+        } else {
+            const int w = (int)(v - list_sh);
+            int s_lo = 0, s_hi = a.G - 1;  // the last slot whose tiles begin at or before w
+            while (s_lo < s_hi) {
+                const int mid = (s_lo + s_hi + 1) / 2;
+                if (s_pre[mid] <= w)
+                    s_lo = mid;
+                else
+                    s_hi = mid - 1;
+            }
+            d.routed = true;
+            d.row0 = max(0, __ldg(a.offsets + s_lo));
+            rows = min((int64_t)__ldg(a.offsets + s_lo + 1), a.rows_cap);
+            d.ct = (int)((rows - d.row0 + 8 * C - 1) / (8 * C));
+            q = w - s_pre[s_lo];
+            at = s_lo * (SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out);
+        }
+        const W4Problem& p = d.routed ? a.rt : a.sh;
+        d.n0 = q / d.ct * TN;
+        d.row0 += (int64_t)(q % d.ct) * 8 * C;
+        d.m = (int)min((int64_t)(8 * C), rows - d.row0);
+        d.wq = p.wq + (at + d.n0) * (p.K / 2);
+        d.ws = p.ws + (at + d.n0) * (p.K / (32 * GS));
+        d.x = xs++ % TILES;
+        __syncwarp();
+        if (lane == 0) tiles[i % TILES] = d;
+        __syncwarp();
+    };
+    // the activation rows of tile i's columns (FC1 reads the routing table for them)
+    int x_done = -1;
+    auto rows_of = [&](int i) {
+        const W4Tile& d = tiles[i % TILES];
+        if (d.x == x_done) return;
+        x_done = d.x;
+        if (lane < 8 * C) {
+            int32_t r = lane < d.m ? (int32_t)(d.row0 + lane) : -1;
+            if (r >= 0 && d.routed && a.perm_src) {
+                const int32_t p = a.perm_src[r];
+                const bool ok = p >= 0 && (int64_t)p < a.T * a.k;
+                if (!ok) report(a.status, MOE_ERR_DEVICE_BOUNDS);
+                r = ok ? p / a.k : -1;
+            }
+            s_x[warp][d.x][lane] = r;
+        }
+        __syncwarp();
+    };
+    auto row_of = [&](const W4Problem& p, const W4Tile& d, int q) {  // weight row g + 8 q from the tile's first
+        const int r = q * 8 + g;
+        return SWIGLU ? (q < 2 ? r : r - 16 + p.N_out) : min(r, p.N_out - 1 - d.n0);
+    };
+
+    const uint8_t* wsrc[4];
+    int w_tile = -1, w_end = 0, w_lane_end = 0;
+    auto next_w = [&](int j) {  // the copies' next tile, from stage j
+        locate(++w_tile);
+        const W4Tile& d = tiles[w_tile % TILES];
+        const W4Problem& p = d.routed ? a.rt : a.sh;
+        const int n = d.routed ? n_rt : n_sh, end = end_of(w_tile);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            wsrc[q] = d.wq + (int64_t)row_of(p, d, q) * (p.K / 2) + (j + n - end) * 64 + t * 16;
+        w_end = min(end, cnt);
+        // a row may end inside its last stage (at a group's end)
+        const bool cut = GS < 4 && end <= cnt && t * 32 >= p.K - (n - 1) * 128;
+        w_lane_end = w_end - (cut ? 1 : 0);
+    };
+    uint32_t w_slot = ring + ((t ^ sw) << 4), r_slot = ring;  // ring stages written and read next
+    auto turn_slot = [&](uint32_t slot) {
+        const uint32_t first = smem_u32(w4_smem) + warp * (RING * W4_STAGE);
+        return first + ((slot - first + W4_STAGE) & (RING * W4_STAGE - 1));
+    };
+    auto issue = [&](int j) {
+        if (j == w_end && j < cnt) next_w(j);
+        if (j < w_lane_end) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                w4_cp16(w_slot + q * 512, wsrc[q]);
+                wsrc[q] += 64;
+            }
+        }
+        w4_cp_commit();
+        w_slot = turn_slot(w_slot);
+    };
+#pragma unroll 1
+    for (int j = 0; j < RING - 1; ++j) issue(j);
+
+    if (a.early) {  // the tables and the weights do not depend on the previous kernel, the activations do
+        pdl_wait();
+        pdl_trigger();
+    }
+
+    const uint16_t* xsrc[C];
+    const uint16_t* ssrc[4];  // scales of accumulator rows g, g + 8 of both 16-row halves
+    bool x_ok[C];
+    int p_tile = -1, p_end = 0;
+    int p_last = 0, p_cut = 0;  // the stage that ends the tile's rows, and how many elements it holds
+    auto next_p = [&](int j) {  // the activations' and scales' next tile, from stage j
+        rows_of(++p_tile);
+        const W4Tile& d = tiles[p_tile % TILES];
+        const W4Problem& p = d.routed ? a.rt : a.sh;
+        const int n = d.routed ? n_rt : n_sh;
+        p_last = end_of(p_tile) - 1;
+        p_cut = p.K - (n - 1) * 128;
+        p_end = min(p_last + 1, cnt);
+        const int stage = j + n - 1 - p_last;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            ssrc[q] = d.ws + (int64_t)row_of(p, d, q) * (p.K / (32 * GS)) + stage * NF;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int32_t r = s_x[warp][d.x][c * 8 + g];
+            x_ok[c] = r >= 0;
+            xsrc[c] = p.x + (int64_t)max(r, 0) * p.K + stage * 128 + t * 8 * GS;
+        }
+    };
+    uint4 xb[C][4];
+    uint32_t sb[NF][4];
+    auto load = [&](int f, int has) {  // group f of their stage, which holds `has` elements
+        if (f * 32 * GS < has) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (x_ok[c]) {
+#pragma unroll
+                    for (int j = 0; j < GS; ++j)
+                        xb[c][f * GS + j] = *reinterpret_cast<const uint4*>(xsrc[c] + f * 32 * GS + j * 8);
+                }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sb[f][q] = __ldg(ssrc[q] + f);
+        }
+    };
+    auto step = [&] {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ssrc[q] += NF;
+#pragma unroll
+        for (int c = 0; c < C; ++c) xsrc[c] += 128;
+    };
+    float acc[2][C][4];
+    auto clear = [&] {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][c][e] = 0.f;
+    };
+    clear();
+    int left = 0;  // elements of the stage that is multiplied next
+    int tile = 0, m = 0, end = 0;
+    if (cnt > 0) {
+        next_p(0);
+        left = GS < 4 && p_last == 0 ? p_cut : 128;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xb[c][j] = make_uint4(0, 0, 0, 0);  // columns without a row stay zero
+#pragma unroll
+        for (int f = 0; f < NF; ++f) load(f, left);
+        step();
+        m = tiles[0].m;
+        end = min(end_of(0), cnt);
+    }
+    bool begun = lo > start_of(v0);  // the tile in hand was begun by an earlier warp
+    W4Tile head;                     // the tile that an earlier warp began and this one ended, or m = 0
+    int64_t head_start = 0;
+    head.m = 0;
+
+#pragma unroll 1
+    for (int i = 0; i < cnt; ++i) {
+        issue(i + RING - 1);
+        const bool turn = i + 1 == p_end && i + 1 < cnt;  // the next stage is another tile's
+        if (turn) next_p(i + 1);
+        const int next = i + 1 < cnt ? (GS < 4 && i + 1 == p_last ? p_cut : 128) : 0;
+        w4_cp_wait<RING - 1>();
+        __syncwarp();
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            if (NF == 1 || f * 32 * GS < left) {
+                // words 0 .. GS-1 of this lane in the group: elements t * 8 GS .. of the rows g + 8 q
+                uint32_t w[4][GS];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int byte = f * 16 * GS + t * 4 * GS;
+                    w4_lds<GS>(w[q], r_slot + q * 512 + (((byte >> 4) ^ sw) << 4) + (byte & 15));
+                }
+                if (C == 1 || m <= 8)
+                    w4_group<GS, 1, C>(acc, w, &xb[0][f * GS], sb[f]);
+                else if (C == 2 || m <= 16)
+                    w4_group<GS, C < 2 ? C : 2, C>(acc, w, &xb[0][f * GS], sb[f]);
+                else
+                    w4_group<GS, C, C>(acc, w, &xb[0][f * GS], sb[f]);
+            }
+            // the same registers take the next stage's values
+            if (turn) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (!x_ok[c])
+#pragma unroll
+                        for (int j = 0; j < GS; ++j) xb[c][f * GS + j] = make_uint4(0, 0, 0, 0);
+            }
+            load(f, next);
+        }
+        __syncwarp();  // the ring slot just read is the next one written
+        left = next;
+        step();
+        r_slot = turn_slot(r_slot);
+        if (i + 1 == end) {  // the tile's last stage here
+            const W4Tile& d = tiles[tile % TILES];
+            const int tile_end = end_of(tile);
+            if (!begun && tile_end <= cnt) {
+                w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, acc);
+            } else {
+                float4* o = parts + ((warp * 2 + (begun ? 0 : 1)) * 2 * C) * 32 + lane;
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int c = 0; c < C; ++c)
+                        o[(r * C + c) * 32] =
+                            make_float4(acc[r][c][0], acc[r][c][1], acc[r][c][2], acc[r][c][3]);
+                if (begun && tile_end <= cnt) {
+                    head = d;
+                    head_start = start_of(v0 + tile);
+                }
+            }
+            clear();
+            begun = false;
+            if (i + 1 < cnt) {
+                ++tile;
+                m = tiles[tile % TILES].m;
+                end = min(end_of(tile), cnt);
+            }
+        }
+    }
+    w4_cp_wait<0>();
+    __syncthreads();
+
+    // the parts of the tile that this warp ended, in stage order
+    if (head.m > 0) {
+        const int first = (int)((WARPS * (head_start - base + 1) - 1) / all);  // the warp that began it
+        for (int w = first; w <= warp; ++w) {
+            if (all * w / WARPS == all * (w + 1) / WARPS) continue;  // a warp without stages
+            const float4* o = parts + ((w * 2 + (w == first ? 1 : 0)) * 2 * C) * 32 + lane;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const float4 f = o[(r * C + c) * 32];
+                    acc[r][c][0] += f.x;
+                    acc[r][c][1] += f.y;
+                    acc[r][c][2] += f.z;
+                    acc[r][c][3] += f.w;
+                }
+        }
+        w4_store<SWIGLU, C>(head.routed ? a.rt : a.sh, head, acc);
     }
 }
 
@@ -459,8 +599,7 @@ __global__ void __launch_bounds__(W4C_THREADS) w4_combine_kernel(const __grid_co
     __shared__ int32_t s_row[W4C_MAXK];
     __shared__ float s_w[W4C_MAXK];
     __shared__ float s_dot[W4C_THREADS / 32];
-    pdl_wait();
-    pdl_trigger();
+    // the tables, x and the gate were written before FC2's predecessor began; only y waits
     const int64_t t = blockIdx.x;
     if (threadIdx.x < a.k) {
         int32_t r = a.pair_row[t * a.k + threadIdx.x];
@@ -492,6 +631,8 @@ __global__ void __launch_bounds__(W4C_THREADS) w4_combine_kernel(const __grid_co
         for (int w = 0; w < W4C_THREADS / 32; ++w) d += s_dot[w];
         g = 1.0f / (1.0f + expf(-d));
     }
+    pdl_wait();
+    pdl_trigger();
     // 4 outputs a thread, blockIdx.y a range of W4C_THREADS * 4 outputs
     const int n = (blockIdx.y * W4C_THREADS + threadIdx.x) * 4;
     if (n >= a.H) return;
@@ -528,7 +669,7 @@ cudaError_t launch_quantize_w4_rows(const uint16_t* w, int64_t rows, int K, int 
 }
 
 template <bool SWIGLU, int GS, int C>
-static cudaError_t launch_w4_mma(const W4Launch& L, int num_sms, cudaStream_t s) {
+static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t s) {
     // the shared-memory limit is set once per device
     static std::atomic<bool> ready[64];
     int dev = 0;
@@ -537,39 +678,28 @@ static cudaError_t launch_w4_mma(const W4Launch& L, int num_sms, cudaStream_t s)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     const size_t smem = w4_smem_bytes(C);
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(w4_mma_kernel<SWIGLU, GS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    // Warps of a unit split its K among them: more of them shorten a unit, fewer waste
-    // less on its ends.  KS minimises the list-scheduling bound over groups of KS warps,
-    // sum of the units' stages / groups + the longest unit, a unit's ends counted as
-    // three stages.  The routed units are bounded by one row tile per slot with pairs.
-    constexpr int TN = SWIGLU ? 16 : 32;
-    const double u_sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + 8 * C - 1) / (8 * C)) : 0.0;
-    const double u_rt = L.G > 0 ? (double)((L.rt.N_out + TN - 1) / TN) * std::min<int64_t>(L.rows_cap, L.G) : 0.0;
-    const int n_sh = (L.sh.K + 127) / 128, n_rt = (L.rt.K + 127) / 128;
-    int KS = 1;
-    double best = 0.0;
-    for (int ks = 1; ks <= W4_WARPS; ks *= 2) {
-        const double groups = 2.0 * num_sms * W4_WARPS / ks;
-        const double l_sh = (n_sh + ks - 1) / ks + 3, l_rt = (n_rt + ks - 1) / ks + 3;
-        const double cost = (u_sh * l_sh + u_rt * l_rt) / groups + std::max(u_sh > 0 ? l_sh : 0.0, u_rt > 0 ? l_rt : 0.0);
-        if (ks == 1 || cost < best) {
-            best = cost;
-            KS = ks;
-        }
-    }
-    const double want = std::ceil((u_sh + u_rt) * KS / W4_WARPS);
-    const unsigned grid = (unsigned)std::max(1.0, std::min(want, 2.0 * num_sms));
-    return launch_k(L.name, w4_mma_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), smem, s, L, KS);
+    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(num_sms), dim3(w4_warps(C) * 32), smem, s, L);
 }
 
 template <bool SWIGLU, int GS>
 static cudaError_t launch_w4_rows(const W4Launch& L, int num_sms, cudaStream_t s) {
-    // a slot has at most as many rows as there are tokens
-    const int64_t most = std::max<int64_t>(L.sh.wq ? L.rows_sh : 0, L.G > 0 ? std::min(L.T, L.rows_cap) : 0);
-    return most <= 8 ? launch_w4_mma<SWIGLU, GS, 1>(L, num_sms, s) : launch_w4_mma<SWIGLU, GS, 2>(L, num_sms, s);
+    // Passes over the weights that the narrow kernel's 8 columns and the wide one's 32 take,
+    // in weight rows; a slot holds rows_cap / G rows on average.
+    const double sh = L.sh.wq ? (double)L.sh.N_out * L.sh.K : 0.0, rt = L.G > 0 ? (double)L.rt.N_out * L.rt.K : 0.0;
+    const double slots = (double)std::min<int64_t>(L.G, L.rows_cap);
+    const double mean = slots > 0 ? L.rows_cap / slots : 0.0;
+    auto passes = [&](int rows) {
+        return sh * std::ceil((double)L.rows_sh / rows) + rt * slots * std::max(1.0, mean / rows);
+    };
+#ifndef W4_WIDE
+#define W4_WIDE 1.5
+#endif
+    return passes(8) < W4_WIDE * passes(32) ? launch_w4_tiles<SWIGLU, GS, 1>(L, num_sms, s)
+                                            : launch_w4_tiles<SWIGLU, GS, 4>(L, num_sms, s);
 }
 
 template <bool SWIGLU>
