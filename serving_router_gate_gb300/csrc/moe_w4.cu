@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 // ---------------------------------------------------------------------------
 // Products on mma.sync.  The work is a list of tiles, 32 weight rows of one slot
 // (FC1: 16 gate rows and the matching 16 up rows) times up to 8 C activation rows;
-// a tile's K is cut into stages of 128.  One CTA per SM takes a contiguous range of
-// the list, about the same number of stages each, and its 16 warps take equal
+// a tile's K is cut into stages of 128.  Every CTA takes a contiguous range of the
+// list, about the same number of stages each, and its 8 warps take equal
 // contiguous ranges of those stages, whatever tiles they fall into.  A warp streams
 // its stages through a ring of its own without a break at a tile's end; it stores
 // the tiles that are all its own, and leaves its part of the at most two that it
@@ -69,16 +69,17 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 constexpr int W4_STAGE = 2048;  // bytes of a stage: 32 rows of 128 elements
 constexpr int W4_MAXG = 1024;   // slots
 
-// The narrow kernel (C = 1) runs 16 warps: eight columns leave the tensor cores idle and
-// the masks and the multiply-adds that widen the codes bound it, which more warps hide.
-// The wide one (C = 4) keeps four column tiles of sums and activations in the registers
-// of 8 warps.  Both have 128 KB of weights in their rings.
-__host__ __device__ constexpr int w4_warps(int C) { return C == 1 ? 16 : 8; }
-__host__ __device__ constexpr int w4_ring(int C) { return 64 / w4_warps(C); }  // stages in each warp's ring
+// The narrow kernel (C = 1) runs two CTAs an SM: eight columns leave the tensor cores
+// idle and the masks and the multiply-adds that widen the codes bound it, which more
+// warps hide.  The wide one (C = 4) keeps four column tiles of sums and activations in
+// the registers of one CTA.  Both have 128 KB of weights of an SM in their rings.
+constexpr int W4_WARPS = 8;
+__host__ __device__ constexpr int w4_ctas(int C) { return C == 1 ? 2 : 1; }  // on an SM
+__host__ __device__ constexpr int w4_ring(int C) { return 8 / w4_ctas(C); }  // stages in each warp's ring
 
 __host__ __device__ constexpr size_t w4_smem_bytes(int C) {
     // every warp's ring, then its parts of two shared tiles (16 C sums a lane)
-    return (size_t)w4_warps(C) * (w4_ring(C) * W4_STAGE + 2 * 32 * 8 * C * 4);
+    return (size_t)W4_WARPS * (w4_ring(C) * W4_STAGE + 2 * 32 * 8 * C * 4);
 }
 
 struct W4Tile {
@@ -93,6 +94,9 @@ struct W4Tile {
 
 __device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void w4_prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 __device__ __forceinline__ void w4_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -219,8 +223,8 @@ __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Tile& d, co
 }
 
 template <bool SWIGLU, int GS, int C>
-__global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_constant__ W4Launch a) {
-    constexpr int WARPS = w4_warps(C), RING = w4_ring(C);
+__global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __grid_constant__ W4Launch a) {
+    constexpr int WARPS = W4_WARPS, RING = w4_ring(C);
     constexpr int TILES = 2 * RING;  // tiles a warp has in hand: the copies run RING - 1 stages ahead
     extern __shared__ __align__(128) uint8_t w4_smem[];
     __shared__ int32_t s_pre[W4_MAXG];  // routed tiles before each slot
@@ -236,7 +240,9 @@ __global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_co
     const uint32_t ring = smem_u32(w4_smem) + warp * (RING * W4_STAGE) + g * 64;
     // part [warp][0: of a tile begun by an earlier warp, 1: of one begun here][4 values][lane]
     float4* parts = reinterpret_cast<float4*>(w4_smem + WARPS * RING * W4_STAGE);
-    if (!a.early) {
+    // What a previous kernel may still be writing is waited for as late as the call allows:
+    // the tables here, the weights before their first copy, the activations after it.
+    if (!a.early && a.G > 0) {
         pdl_wait();
         pdl_trigger();
     }
@@ -288,9 +294,13 @@ __global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_co
     }
     // this CTA's tiles: from the first that starts at or after its share of the stages
     const int64_t stages_sh = list_sh * n_sh, stages = stages_sh + list_rt * n_rt;
+    const bool small = stages * gridDim.x < (int64_t(1) << 31);  // divisions in 32 bits, a fifth of the 64-bit ones
+    auto over = [small](int64_t x, int y) {
+        return small ? (int64_t)((uint32_t)x / (uint32_t)y) : x / (int64_t)y;
+    };
     auto first_tile = [&](int64_t cta) {
-        const int64_t s = stages * cta / gridDim.x;
-        return s <= stages_sh ? (n_sh ? (s + n_sh - 1) / n_sh : 0) : list_sh + (s - stages_sh + n_rt - 1) / n_rt;
+        const int64_t s = over(stages * cta, (int)gridDim.x);
+        return s <= stages_sh ? (n_sh ? over(s + n_sh - 1, n_sh) : 0) : list_sh + over(s - stages_sh + n_rt - 1, n_rt);
     };
     auto start_of = [&](int64_t v) { return v <= list_sh ? v * n_sh : stages_sh + (v - list_sh) * n_rt; };
     const int64_t base = start_of(first_tile(blockIdx.x));
@@ -298,7 +308,7 @@ __global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_co
     // this warp's stages: cnt from lo; the first one's tile
     const int64_t lo = base + all * warp / WARPS;
     const int cnt = (int)(base + all * (warp + 1) / WARPS - lo);
-    const int64_t v0 = lo < stages_sh ? lo / n_sh : list_sh + (n_rt ? (lo - stages_sh) / n_rt : 0);
+    const int64_t v0 = lo < stages_sh ? over(lo, n_sh) : list_sh + (n_rt ? over(lo - stages_sh, n_rt) : 0);
 
     // Three cursors run over the stages: the copies three ahead, the activations and
     // scales one ahead, the products.  Tile i from v0 is at s_tile[warp][i % TILES]
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_co
         return first + ((slot - first + W4_STAGE) & (RING * W4_STAGE - 1));
     };
     auto issue = [&](int j) {
-        if (j == w_end && j < cnt) next_w(j);
+        if (j >= w_end && j < cnt) next_w(j);
         if (j < w_lane_end) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -416,6 +426,20 @@ __global__ void __launch_bounds__(w4_warps(C) * 32, 1) w4_kernel(const __grid_co
         w4_cp_commit();
         w_slot = turn_slot(w_slot);
     };
+    if (!a.early && a.G == 0) {
+        if (cnt > 0) {
+            // the first stages' lines on their way to L2 meanwhile
+            next_w(0);
+            if (t == 0)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    w4_prefetch_l2(wsrc[q]);
+                    if (w_end > 2) w4_prefetch_l2(wsrc[q] + 128);
+                }
+        }
+        pdl_wait();
+        pdl_trigger();
+    }
 #pragma unroll 1
     for (int j = 0; j < RING - 1; ++j) issue(j);
 
@@ -682,7 +706,16 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(num_sms), dim3(w4_warps(C) * 32), smem, s, L);
+    // No more CTAs than tiles, and no fewer stages to a CTA than its longest tile has
+    // (between one CTA an SM and as many as fit).
+    constexpr int TN = SWIGLU ? 16 : 32;
+    const int n_sh = (L.sh.K + 127) / 128, n_rt = (L.rt.K + 127) / 128;
+    const double sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + 8 * C - 1) / (8 * C)) : 0.0;
+    const double rt = L.G > 0 ? (double)((L.rt.N_out + TN - 1) / TN) * std::min<int64_t>(L.rows_cap, L.G) : 0.0;
+    const double even = (sh * n_sh + rt * n_rt) / std::max(sh > 0 ? n_sh : 1, rt > 0 ? n_rt : 1);
+    const double most = std::min(sh + rt, (double)w4_ctas(C) * num_sms);
+    const unsigned grid = (unsigned)std::max(1.0, std::min(most, std::max(even, (double)num_sms)));
+    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_WARPS * 32), smem, s, L);
 }
 
 template <bool SWIGLU, int GS>
