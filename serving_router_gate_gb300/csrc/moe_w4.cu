@@ -12,7 +12,6 @@
 // activations lie in memory.
 #include <algorithm>
 #include <atomic>
-#include <cmath>
 
 #include "moe_internal.cuh"
 
@@ -57,38 +56,33 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 
 // ---------------------------------------------------------------------------
 // Products on mma.sync.  The work is a list of tiles, 32 weight rows of one slot
-// (FC1: 16 gate rows and the matching 16 up rows) times up to 8 C activation rows;
-// a tile's K is cut into stages of 128.  Every CTA takes a contiguous range of the
-// list, about the same number of stages each, and its 8 warps take equal
-// contiguous ranges of those stages, whatever tiles they fall into.  A warp streams
-// its stages through a ring of its own without a break at a tile's end; it stores
-// the tiles that are all its own, and leaves its part of the at most two that it
-// shares with its neighbours in shared memory, where the warp that ends a tile adds
-// the parts in stage order.
+// (FC1: 16 gate rows and the matching 16 up rows) times up to 8 activation rows; a
+// tile's K is cut into stages of 128.  Every CTA takes a contiguous range of the list,
+// about the same number of stages each, and its 8 warps take equal contiguous ranges
+// of those stages, whatever tiles they fall into.  A warp streams its stages through
+// a ring of its own without a break at a tile's end; it stores the tiles that are all
+// its own, and leaves its part of the at most two that it shares with its neighbours
+// in shared memory, where the warp that ends a tile adds the parts in stage order.
 // ---------------------------------------------------------------------------
-constexpr int W4_STAGE = 2048;  // bytes of a stage: 32 rows of 128 elements
-constexpr int W4_MAXG = 1024;   // slots
-
-// The narrow kernel (C = 1) runs two CTAs an SM: eight columns leave the tensor cores
-// idle and the masks and the multiply-adds that widen the codes bound it, which more
-// warps hide.  The wide one (C = 4) keeps four column tiles of sums and activations in
-// the registers of one CTA.  Both have 128 KB of weights of an SM in their rings.
 constexpr int W4_WARPS = 8;
-__host__ __device__ constexpr int w4_ctas(int C) { return C == 1 ? 2 : 1; }  // on an SM
-__host__ __device__ constexpr int w4_ring(int C) { return 8 / w4_ctas(C); }  // stages in each warp's ring
+constexpr int W4_THREADS = W4_WARPS * 32;
+constexpr int W4_CTAS = 2;       // on an SM
+constexpr int W4_RING = 4;       // stages in each warp's ring
+constexpr int W4_STAGE = 2048;   // bytes of a stage: 32 rows of 128 elements
+constexpr int W4_ROWS = 8;       // activation rows of a tile
+constexpr int W4_MAXG = 1024;    // slots
+constexpr int W4_RUNS = 8;       // runs a warp has in hand: the copies are three stages ahead
+// every warp's ring, then its parts of two shared tiles (8 sums a lane)
+constexpr size_t W4_SMEM = (size_t)W4_WARPS * (W4_RING * W4_STAGE + 2 * 32 * 8 * 4);
 
-__host__ __device__ constexpr size_t w4_smem_bytes(int C) {
-    // every warp's ring, then its parts of two shared tiles (16 C sums a lane)
-    return (size_t)W4_WARPS * (w4_ring(C) * W4_STAGE + 2 * 32 * 8 * C * 4);
-}
-
-struct W4Tile {
-    const uint8_t* wq;   // packed weights and scales of its first row
+// Neighbouring tiles of the list with the same activation rows, from the first that a
+// warp has a stage of.
+struct W4Run {
+    const uint8_t* wq;   // packed weights and scales of the first tile's first row
     const uint16_t* ws;
     int64_t row0;        // first output row
-    int n0, m;           // first output, rows
-    int ct;              // row tiles of its slot
-    int x;               // where its activation rows stand
+    int n0, m;           // first output of the first tile, rows
+    int tiles;
     bool routed;
 };
 
@@ -116,21 +110,14 @@ __device__ __forceinline__ void w4_lds(uint32_t (&v)[n], uint32_t addr) {
     else
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
 }
-
-// D += A B (first: D = A B), A 16 x 16 (row), B 16 x 8 (column), bf16 inputs, fp32 sums
-__device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// D = A B + C, A 16 x 16 (row), B 16 x 8 (column), bf16 inputs, fp32 sums
+__device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                       const float (&c)[4]) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void w4_mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %10, %10, %10};"
+        "{%10, %11, %12, %13};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-
 // Elements 2j and 2j + 1 of a packed word as bf16 c / 64.  With a nibble n = c + 8 at
 // bits 0-3 or 4-7 of a half, the half read as bf16 is n 2^-133 or n 2^-129: exponent
 // fields 0 and 1 are one linear range (the lower one subnormal).  One fused
@@ -145,101 +132,84 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j) {
     return v;
 }
 
-// One group of a stage: acc += scales * (codes x activations), C8 of the C column tiles
-// of eight.  w: the lane's words of rows g + 8 q, xb: its activations, [column tile][4].
-template <int GS, int C8, int C>
-__device__ __forceinline__ void w4_group(float (&acc)[2][C][4], const uint32_t (&w)[4][GS], const uint4* xb,
-                                         const uint32_t (&sb)[4]) {
-    float tmp[2][C8][4];
+// One group of a stage: acc += scales * (codes x activations).  w: the lane's words of
+// rows g + 8 q; xb: its activations; s: the scales of those rows.  Accumulators
+// [half][row g, g + 8][column 2t, 2t + 1], in units of 1/64.
+template <int GS>
+__device__ __forceinline__ void w4_group(float (&acc)[2][2][2], const uint32_t (&w)[4][GS], const uint32_t* xb,
+                                         const float (&s)[4]) {
+    float tmp[2][4] = {};
 #pragma unroll
     for (int j = 0; j < GS; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t A[2][4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                A[r][0] = w4_pair(w[2 * r][j], 2 * h);
-                A[r][1] = w4_pair(w[2 * r + 1][j], 2 * h);
-                A[r][2] = w4_pair(w[2 * r][j], 2 * h + 1);
-                A[r][3] = w4_pair(w[2 * r + 1][j], 2 * h + 1);
+                const uint32_t A[4] = {w4_pair(w[2 * r][j], 2 * h), w4_pair(w[2 * r + 1][j], 2 * h),
+                                       w4_pair(w[2 * r][j], 2 * h + 1), w4_pair(w[2 * r + 1][j], 2 * h + 1)};
+                w4_mma(tmp[r], A, xb[4 * j + 2 * h], xb[4 * j + 2 * h + 1], tmp[r]);
             }
 #pragma unroll
-            for (int c = 0; c < C8; ++c) {
-                const uint4 b = xb[c * 4 + j];
-                const uint32_t b0 = h ? b.z : b.x, b1 = h ? b.w : b.y;
-                if (j == 0 && h == 0) {
-                    w4_mma_first(tmp[0][c], A[0], b0, b1);
-                    w4_mma_first(tmp[1][c], A[1], b0, b1);
-                } else {
-                    w4_mma(tmp[0][c], A[0], b0, b1);
-                    w4_mma(tmp[1][c], A[1], b0, b1);
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][i / 2][i % 2] = fmaf(s[2 * r + i / 2], tmp[r][i], acc[r][i / 2][i % 2]);
+}
+
+// The outputs of the tile at n0 from its accumulators.  xrow: the activation row of each
+// column, -1 for one that the tables got wrong (its outputs are zero).
+template <bool SWIGLU>
+__device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int n0, const int32_t* xrow,
+                                         const float (&acc)[2][2][2]) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const int64_t N = p.N_out;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int col = 2 * t + c;
+        if (col >= d.m) continue;
+        const float unit = xrow[col] < 0 ? 0.f : 64.f;
+        const int64_t at = (d.row0 + col) * N + n0 + g;
+        float v[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v[r][h] = acc[r][h][c] * unit;
+        if (SWIGLU) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float o = __fdividef(v[0][h], 1.0f + expf(-v[0][h])) * v[1][h];
+                p.out_bf16[at + 8 * h] = (uint16_t)(pack_bf16x2(o, 0.f) & 0xFFFFu);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (n0 + 16 * r + 8 * h + g >= N) continue;
+                    if (p.out_f32)
+                        p.out_f32[at + 16 * r + 8 * h] = v[r][h];
+                    else
+                        p.out_bf16[at + 16 * r + 8 * h] = (uint16_t)(pack_bf16x2(v[r][h], 0.f) & 0xFFFFu);
                 }
-            }
-        }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const float s0 = bf16_bits_to_float(sb[2 * r]), s1 = bf16_bits_to_float(sb[2 * r + 1]);
-#pragma unroll
-        for (int c = 0; c < C8; ++c) {
-            acc[r][c][0] = fmaf(s0, tmp[r][c][0], acc[r][c][0]);
-            acc[r][c][1] = fmaf(s0, tmp[r][c][1], acc[r][c][1]);
-            acc[r][c][2] = fmaf(s1, tmp[r][c][2], acc[r][c][2]);
-            acc[r][c][3] = fmaf(s1, tmp[r][c][3], acc[r][c][3]);
         }
     }
 }
 
-// The outputs of a tile from its accumulators: this lane has rows g, g + 8 of both
-// 16-row halves and columns 2t, 2t + 1 of every eight.
-template <bool SWIGLU, int C>
-__device__ __forceinline__ void w4_store(const W4Problem& p, const W4Tile& d, const float (&acc)[2][C][4]) {
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-    const int64_t N = p.N_out;
-    auto put = [&](int64_t at, float v) {
-        if (p.out_f32)
-            p.out_f32[at] = v;
-        else
-            p.out_bf16[at] = (uint16_t)(pack_bf16x2(v, 0.f) & 0xFFFFu);
-    };
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int col = c * 8 + 2 * t + e;
-            if (col >= d.m) continue;
-            const int64_t at = (d.row0 + col) * N + d.n0 + g;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // the codes were c / 64
-                const float v0 = 64.f * acc[0][c][2 * h + e], v1 = 64.f * acc[1][c][2 * h + e];
-                if (SWIGLU) {
-                    put(at + 8 * h, v0 / (1.0f + expf(-v0)) * v1);
-                } else {
-                    if (d.n0 + 8 * h + g < N) put(at + 8 * h, v0);
-                    if (d.n0 + 16 + 8 * h + g < N) put(at + 16 + 8 * h, v1);
-                }
-            }
-        }
-}
-
-template <bool SWIGLU, int GS, int C>
-__global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __grid_constant__ W4Launch a) {
-    constexpr int WARPS = W4_WARPS, RING = w4_ring(C);
-    constexpr int TILES = 2 * RING;  // tiles a warp has in hand: the copies run RING - 1 stages ahead
+template <bool SWIGLU, int GS>
+__global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_constant__ W4Launch a) {
     extern __shared__ __align__(128) uint8_t w4_smem[];
     __shared__ int32_t s_pre[W4_MAXG];  // routed tiles before each slot
-    __shared__ int32_t s_part[WARPS];
-    __shared__ W4Tile s_tile[WARPS][TILES];
-    __shared__ int32_t s_x[WARPS][TILES][8 * C];  // activation row of each column, -1: none
-    constexpr int TN = SWIGLU ? 16 : 32;                // outputs of a tile
-    constexpr int NF = 4 / GS;                          // groups in a stage
+    __shared__ int32_t s_part[W4_WARPS];
+    __shared__ W4Run s_run[W4_WARPS][W4_RUNS + 1];            // in the last place, that of a tile
+    __shared__ int32_t s_x[W4_WARPS][W4_RUNS + 1][W4_ROWS];  // begun by an earlier warp; columns' activation rows
+    constexpr int TN = SWIGLU ? 16 : 32;  // outputs of a tile
+    constexpr int NF = 4 / GS;            // groups in a stage
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     // pieces rotate within a row of a stage so that the reads below meet every bank once
     const int sw = ((g >> 1) & 1) * 2 + (g >> 2);
-    const uint32_t ring = smem_u32(w4_smem) + warp * (RING * W4_STAGE) + g * 64;
+    const uint32_t ring0 = smem_u32(w4_smem) + warp * (W4_RING * W4_STAGE);
     // part [warp][0: of a tile begun by an earlier warp, 1: of one begun here][4 values][lane]
-    float4* parts = reinterpret_cast<float4*>(w4_smem + WARPS * RING * W4_STAGE);
+    float4* parts = reinterpret_cast<float4*>(w4_smem + W4_WARPS * W4_RING * W4_STAGE);
     // What a previous kernel may still be writing is waited for as late as the call allows:
     // the tables here, the weights before their first copy, the activations after it.
     if (!a.early && a.G > 0) {
@@ -249,13 +219,13 @@ __global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __g
 
     // the list: the dense problem's tiles, then the routed ones by slot; the row tiles of
     // one weight tile are neighbours
-    const int ct_sh = (int)((a.rows_sh + 8 * C - 1) / (8 * C));
+    const int ct_sh = (int)((a.rows_sh + W4_ROWS - 1) / W4_ROWS);
     const int n_sh = (a.sh.K + 127) / 128, n_rt = (a.rt.K + 127) / 128;  // stages of a tile
     const int tiles_rt = (a.rt.N_out + TN - 1) / TN;
     const int64_t list_sh = a.sh.wq ? (int64_t)((a.sh.N_out + TN - 1) / TN) * ct_sh : 0;
     int64_t list_rt = 0;
     if (a.G > 0) {
-        constexpr int PER = W4_MAXG / (WARPS * 32);
+        constexpr int PER = W4_MAXG / W4_THREADS;
         const int s0 = threadIdx.x * PER;
         int n[PER], sum = 0;
         int64_t lo = s0 <= a.G ? __ldg(a.offsets + s0) : 0;
@@ -265,7 +235,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __g
             if (s0 + i < a.G) {
                 const int64_t hi = __ldg(a.offsets + s0 + i + 1);
                 const int64_t m = max((int64_t)0, min(hi, a.rows_cap) - max(lo, (int64_t)0));
-                n[i] = (int)((m + 8 * C - 1) / (8 * C)) * tiles_rt;
+                n[i] = (int)((m + W4_ROWS - 1) / W4_ROWS) * tiles_rt;
                 lo = hi;
             }
             sum += n[i];
@@ -280,7 +250,7 @@ __global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __g
         __syncthreads();
         int base = inc - sum, total = 0;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < W4_WARPS; ++w) {
             base += w < warp ? s_part[w] : 0;
             total += s_part[w];
         }
@@ -306,45 +276,31 @@ __global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __g
     const int64_t base = start_of(first_tile(blockIdx.x));
     const int64_t all = start_of(first_tile(blockIdx.x + 1)) - base;
     // this warp's stages: cnt from lo; the first one's tile
-    const int64_t lo = base + all * warp / WARPS;
-    const int cnt = (int)(base + all * (warp + 1) / WARPS - lo);
+    const int64_t lo = base + all * warp / W4_WARPS;
+    const int cnt = (int)(base + all * (warp + 1) / W4_WARPS - lo);
     const int64_t v0 = lo < stages_sh ? over(lo, n_sh) : list_sh + (n_rt ? over(lo - stages_sh, n_rt) : 0);
 
     // Three cursors run over the stages: the copies three ahead, the activations and
-    // scales one ahead, the products.  Tile i from v0 is at s_tile[warp][i % TILES]
-    // from when the copies reach it; ends count from lo.  (The loop is not unrolled over
-    // the ring: four copies of what a tile's end takes overran the instruction cache,
-    // 3 of 8 stalled cycles.)
-    W4Tile* tiles = s_tile[warp];
-    auto end_of = [&](int i) { return (int)(start_of(v0 + i + 1) - lo); };
-    int xs = 0;  // activation row sets so far
+    // scales one ahead, the products.  Each steps from tile to tile of a run by constants
+    // and finds run i of the warp, when it gets there, at s_run[warp][i % W4_RUNS].  Stage
+    // numbers count from lo.  (The loop is not unrolled over the ring: four copies of what
+    // a tile's end takes overran the instruction cache, 3 of 8 stalled cycles.)
+    W4Run* runs = s_run[warp];
+    const int first = (int)(start_of(v0) - lo);  // where the first tile starts (<= 0)
+    int64_t next_v = v0;                         // the first tile past the runs so far
     auto locate = [&](int i) {
-        W4Tile d;
-        const int64_t v = v0 + i;
-        if (i > 0) {
-            d = tiles[(i - 1) % TILES];
-            const W4Problem& p = d.routed ? a.rt : a.sh;
-            if (d.ct == 1 && d.n0 + TN < p.N_out) {  // the same rows, the next weights
-                d.n0 += TN;
-                d.wq += (int64_t)TN * (p.K / 2);
-                d.ws += (int64_t)TN * (p.K / (32 * GS));
-                __syncwarp();
-                if (lane == 0) tiles[i % TILES] = d;
-                __syncwarp();
-                return;
-            }
-        }
+        W4Run d;
         int64_t rows, at;  // the slot's end, its first weight row
-        int q;             // tile of the slot
-        if (v < list_sh) {
-            q = (int)v;
+        int q, ct;         // tile of the slot, its row tiles
+        if (next_v < list_sh) {
+            q = (int)next_v;
             d.routed = false;
-            d.ct = ct_sh;
+            ct = ct_sh;
             d.row0 = 0;
             rows = a.rows_sh;
             at = 0;
         } else {
-            const int w = (int)(v - list_sh);
+            const int w = (int)(next_v - list_sh);
             int s_lo = 0, s_hi = a.G - 1;  // the last slot whose tiles begin at or before w
             while (s_lo < s_hi) {
                 const int mid = (s_lo + s_hi + 1) / 2;
@@ -356,80 +312,72 @@ __global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __g
             d.routed = true;
             d.row0 = max(0, __ldg(a.offsets + s_lo));
             rows = min((int64_t)__ldg(a.offsets + s_lo + 1), a.rows_cap);
-            d.ct = (int)((rows - d.row0 + 8 * C - 1) / (8 * C));
+            ct = (int)((rows - d.row0 + W4_ROWS - 1) / W4_ROWS);
             q = w - s_pre[s_lo];
             at = s_lo * (SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out);
         }
         const W4Problem& p = d.routed ? a.rt : a.sh;
-        d.n0 = q / d.ct * TN;
-        d.row0 += (int64_t)(q % d.ct) * 8 * C;
-        d.m = (int)min((int64_t)(8 * C), rows - d.row0);
+        const int tile = q / ct;
+        d.n0 = tile * TN;
+        d.row0 += (int64_t)(q - tile * ct) * W4_ROWS;
+        d.m = (int)min((int64_t)W4_ROWS, rows - d.row0);
         d.wq = p.wq + (at + d.n0) * (p.K / 2);
         d.ws = p.ws + (at + d.n0) * (p.K / (32 * GS));
-        d.x = xs++ % TILES;
+        // a last tile with fewer outputs stands alone: some of its rows repeat
+        d.tiles = ct == 1 ? max(1, p.N_out / TN - tile) : 1;
+        next_v += d.tiles;
         __syncwarp();
-        if (lane == 0) tiles[i % TILES] = d;
-        __syncwarp();
-    };
-    // the activation rows of tile i's columns (FC1 reads the routing table for them)
-    int x_done = -1;
-    auto rows_of = [&](int i) {
-        const W4Tile& d = tiles[i % TILES];
-        if (d.x == x_done) return;
-        x_done = d.x;
-        if (lane < 8 * C) {
-            int32_t r = lane < d.m ? (int32_t)(d.row0 + lane) : -1;
-            if (r >= 0 && d.routed && a.perm_src) {
-                const int32_t p = a.perm_src[r];
-                const bool ok = p >= 0 && (int64_t)p < a.T * a.k;
-                if (!ok) report(a.status, MOE_ERR_DEVICE_BOUNDS);
-                r = ok ? p / a.k : -1;
-            }
-            s_x[warp][d.x][lane] = r;
-        }
+        if (lane == 0) runs[i % W4_RUNS] = d;
         __syncwarp();
     };
-    auto row_of = [&](const W4Problem& p, const W4Tile& d, int q) {  // weight row g + 8 q from the tile's first
+    auto row_of = [&](const W4Problem& p, const W4Run& d, int q) {  // weight row g + 8 q from the run's first
         const int r = q * 8 + g;
         return SWIGLU ? (q < 2 ? r : r - 16 + p.N_out) : min(r, p.N_out - 1 - d.n0);
     };
 
     const uint8_t* wsrc[4];
-    int w_tile = -1, w_end = 0, w_lane_end = 0;
-    auto next_w = [&](int j) {  // the copies' next tile, from stage j
-        locate(++w_tile);
-        const W4Tile& d = tiles[w_tile % TILES];
-        const W4Problem& p = d.routed ? a.rt : a.sh;
-        const int n = d.routed ? n_rt : n_sh, end = end_of(w_tile);
+    int w_run = -1, w_tiles = 1, w_end = first, w_n = 0, w_step = 0;
+    bool w_cut = false;             // the lane's piece lies past the end of a row's last stage
+    auto next_w = [&](int j) {  // the copies' next tile
+        if (--w_tiles > 0) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            wsrc[q] = d.wq + (int64_t)row_of(p, d, q) * (p.K / 2) + (j + n - end) * 64 + t * 16;
-        w_end = min(end, cnt);
-        // a row may end inside its last stage (at a group's end)
-        const bool cut = GS < 4 && end <= cnt && t * 32 >= p.K - (n - 1) * 128;
-        w_lane_end = w_end - (cut ? 1 : 0);
+            for (int q = 0; q < 4; ++q) wsrc[q] += w_step;
+        } else {
+            locate(++w_run);
+            const W4Run& d = runs[w_run % W4_RUNS];
+            const W4Problem& p = d.routed ? a.rt : a.sh;
+            w_n = d.routed ? n_rt : n_sh;
+            w_tiles = d.tiles;
+            w_step = TN * (p.K / 2) - w_n * 64;
+            w_cut = GS < 4 && t * 32 >= p.K - (w_n - 1) * 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                wsrc[q] = d.wq + (int64_t)row_of(p, d, q) * (p.K / 2) + (j - w_end) * 64 + t * 16;
+        }
+        w_end += w_n;
     };
-    uint32_t w_slot = ring + ((t ^ sw) << 4), r_slot = ring;  // ring stages written and read next
-    auto turn_slot = [&](uint32_t slot) {
-        const uint32_t first = smem_u32(w4_smem) + warp * (RING * W4_STAGE);
-        return first + ((slot - first + W4_STAGE) & (RING * W4_STAGE - 1));
-    };
+    uint32_t w_off = 0, r_off = 0;  // ring stages written and read next
+    const uint32_t w_slot = ring0 + g * 64 + ((t ^ sw) << 4), r_slot = ring0 + g * 64;
+    bool w_open = false;  // the first tile's addresses stand
     auto issue = [&](int j) {
-        if (j >= w_end && j < cnt) next_w(j);
-        if (j < w_lane_end) {
+        if (j < cnt) {
+            if (j == w_end || !w_open) next_w(j);
+            w_open = true;
+            if (GS == 4 || !(w_cut && j + 1 == w_end)) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                w4_cp16(w_slot + q * 512, wsrc[q]);
-                wsrc[q] += 64;
+                for (int q = 0; q < 4; ++q) w4_cp16(w_slot + w_off + q * 512, wsrc[q]);
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) wsrc[q] += 64;
         }
         w4_cp_commit();
-        w_slot = turn_slot(w_slot);
+        w_off = (w_off + W4_STAGE) & (W4_RING * W4_STAGE - 1);
     };
     if (!a.early && a.G == 0) {
         if (cnt > 0) {
             // the first stages' lines on their way to L2 meanwhile
             next_w(0);
+            w_open = true;
             if (t == 0)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -441,175 +389,156 @@ __global__ void __launch_bounds__(W4_WARPS * 32, w4_ctas(C)) w4_kernel(const __g
         pdl_trigger();
     }
 #pragma unroll 1
-    for (int j = 0; j < RING - 1; ++j) issue(j);
+    for (int j = 0; j < W4_RING - 1; ++j) issue(j);
 
     if (a.early) {  // the tables and the weights do not depend on the previous kernel, the activations do
         pdl_wait();
         pdl_trigger();
     }
 
-    const uint16_t* xsrc[C];
-    const uint16_t* ssrc[4];  // scales of accumulator rows g, g + 8 of both 16-row halves
-    bool x_ok[C];
-    int p_tile = -1, p_end = 0;
-    int p_last = 0, p_cut = 0;  // the stage that ends the tile's rows, and how many elements it holds
-    auto next_p = [&](int j) {  // the activations' and scales' next tile, from stage j
-        rows_of(++p_tile);
-        const W4Tile& d = tiles[p_tile % TILES];
-        const W4Problem& p = d.routed ? a.rt : a.sh;
-        const int n = d.routed ? n_rt : n_sh;
-        p_last = end_of(p_tile) - 1;
-        p_cut = p.K - (n - 1) * 128;
-        p_end = min(p_last + 1, cnt);
-        const int stage = j + n - 1 - p_last;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            ssrc[q] = d.ws + (int64_t)row_of(p, d, q) * (p.K / (32 * GS)) + stage * NF;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int32_t r = s_x[warp][d.x][c * 8 + g];
-            x_ok[c] = r >= 0;
-            xsrc[c] = p.x + (int64_t)max(r, 0) * p.K + stage * 128 + t * 8 * GS;
+    const uint16_t* xsrc = nullptr;  // the lane's activations, of column g (past the tile's rows: its last one)
+    const uint16_t* ssrc = nullptr;  // the scales of weight row g + 8 t
+    int p_run = -1, p_tiles = 1, p_end = first, p_n = 0, p_step = 0;
+    int p_cut = 0;  // elements of a row's last stage
+    auto next_p = [&](int j) {  // the activations' and scales' next tile
+        if (--p_tiles > 0) {
+            ssrc += p_step;
+            xsrc -= p_n * 128;
+        } else {
+            const W4Run& d = runs[++p_run % W4_RUNS];
+            const W4Problem& p = d.routed ? a.rt : a.sh;
+            if (lane < W4_ROWS) {  // FC1 reads the routing table for the rows
+                int32_t r = (int32_t)(d.row0 + min(lane, d.m - 1));
+                if (d.routed && a.perm_src) {
+                    const int32_t q = a.perm_src[r];
+                    const bool ok = q >= 0 && (int64_t)q < a.T * a.k;
+                    if (!ok) report(a.status, MOE_ERR_DEVICE_BOUNDS);
+                    r = ok ? q / a.k : -1;
+                }
+                s_x[warp][p_run % W4_RUNS][lane] = r;
+            }
+            __syncwarp();
+            p_n = d.routed ? n_rt : n_sh;
+            p_tiles = d.tiles;
+            p_step = TN * (p.K / (32 * GS)) - p_n * NF;
+            p_cut = p.K - (p_n - 1) * 128;
+            ssrc = d.ws + (int64_t)row_of(p, d, t) * (p.K / (32 * GS)) + (j - p_end) * NF;
+            xsrc = p.x + (int64_t)max(s_x[warp][p_run % W4_RUNS][g], 0) * p.K + (j - p_end) * 128 + t * 8 * GS;
         }
+        p_end += p_n;
     };
-    uint4 xb[C][4];
-    uint32_t sb[NF][4];
+    uint32_t xb[16], sb[NF];
     auto load = [&](int f, int has) {  // group f of their stage, which holds `has` elements
         if (f * 32 * GS < has) {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (x_ok[c]) {
-#pragma unroll
-                    for (int j = 0; j < GS; ++j)
-                        xb[c][f * GS + j] = *reinterpret_cast<const uint4*>(xsrc[c] + f * 32 * GS + j * 8);
-                }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sb[f][q] = __ldg(ssrc[q] + f);
+            for (int j = 0; j < GS; ++j) {
+                const uint4 u = *reinterpret_cast<const uint4*>(xsrc + f * 32 * GS + j * 8);
+                uint32_t* o = xb + 4 * (f * GS + j);
+                o[0] = u.x;
+                o[1] = u.y;
+                o[2] = u.z;
+                o[3] = u.w;
+            }
+            sb[f] = __ldg(ssrc + f);
         }
     };
     auto step = [&] {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ssrc[q] += NF;
-#pragma unroll
-        for (int c = 0; c < C; ++c) xsrc[c] += 128;
+        ssrc += NF;
+        xsrc += 128;
     };
-    float acc[2][C][4];
-    auto clear = [&] {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[r][c][e] = 0.f;
-    };
-    clear();
+    float acc[2][2][2] = {};
     int left = 0;  // elements of the stage that is multiplied next
-    int tile = 0, m = 0, end = 0;
+    int run = 0, tiles = 0, n0 = 0, end = 0, n = 0;
     if (cnt > 0) {
         next_p(0);
-        left = GS < 4 && p_last == 0 ? p_cut : 128;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) xb[c][j] = make_uint4(0, 0, 0, 0);  // columns without a row stay zero
+        left = GS < 4 && p_end == 1 ? p_cut : 128;
 #pragma unroll
         for (int f = 0; f < NF; ++f) load(f, left);
         step();
-        m = tiles[0].m;
-        end = min(end_of(0), cnt);
+        tiles = runs[0].tiles;
+        n0 = runs[0].n0;
+        n = runs[0].routed ? n_rt : n_sh;
+        end = first + n;
     }
-    bool begun = lo > start_of(v0);  // the tile in hand was begun by an earlier warp
-    W4Tile head;                     // the tile that an earlier warp began and this one ended, or m = 0
-    int64_t head_start = 0;
-    head.m = 0;
+    bool begun = first < 0;  // the tile in hand was begun by an earlier warp
+    bool ended = false;      // and this one ended it
 
 #pragma unroll 1
     for (int i = 0; i < cnt; ++i) {
-        issue(i + RING - 1);
-        const bool turn = i + 1 == p_end && i + 1 < cnt;  // the next stage is another tile's
-        if (turn) next_p(i + 1);
-        const int next = i + 1 < cnt ? (GS < 4 && i + 1 == p_last ? p_cut : 128) : 0;
-        w4_cp_wait<RING - 1>();
+        issue(i + W4_RING - 1);
+        if (i + 1 == p_end && i + 1 < cnt) next_p(i + 1);
+        const int next = i + 1 < cnt ? (GS < 4 && i + 2 == p_end ? p_cut : 128) : 0;
+        w4_cp_wait<W4_RING - 1>();
         __syncwarp();
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
             if (NF == 1 || f * 32 * GS < left) {
                 // words 0 .. GS-1 of this lane in the group: elements t * 8 GS .. of the rows g + 8 q
                 uint32_t w[4][GS];
+                float s[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int byte = f * 16 * GS + t * 4 * GS;
-                    w4_lds<GS>(w[q], r_slot + q * 512 + (((byte >> 4) ^ sw) << 4) + (byte & 15));
+                    w4_lds<GS>(w[q], r_slot + r_off + q * 512 + (((byte >> 4) ^ sw) << 4) + (byte & 15));
+                    s[q] = bf16_bits_to_float(__shfl_sync(0xffffffffu, sb[f], (lane & 28) | q));
                 }
-                if (C == 1 || m <= 8)
-                    w4_group<GS, 1, C>(acc, w, &xb[0][f * GS], sb[f]);
-                else if (C == 2 || m <= 16)
-                    w4_group<GS, C < 2 ? C : 2, C>(acc, w, &xb[0][f * GS], sb[f]);
-                else
-                    w4_group<GS, C, C>(acc, w, &xb[0][f * GS], sb[f]);
+                w4_group<GS>(acc, w, xb + 4 * f * GS, s);
             }
-            // the same registers take the next stage's values
-            if (turn) {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (!x_ok[c])
-#pragma unroll
-                        for (int j = 0; j < GS; ++j) xb[c][f * GS + j] = make_uint4(0, 0, 0, 0);
-            }
-            load(f, next);
+            load(f, next);  // the same registers take the next stage's values
         }
         __syncwarp();  // the ring slot just read is the next one written
         left = next;
         step();
-        r_slot = turn_slot(r_slot);
-        if (i + 1 == end) {  // the tile's last stage here
-            const W4Tile& d = tiles[tile % TILES];
-            const int tile_end = end_of(tile);
-            if (!begun && tile_end <= cnt) {
-                w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, acc);
+        r_off = (r_off + W4_STAGE) & (W4_RING * W4_STAGE - 1);
+        if (i + 1 == end || i + 1 == cnt) {  // the tile's last stage here
+            const W4Run& d = runs[run % W4_RUNS];
+            if (!begun && i + 1 == end) {
+                w4_store<SWIGLU>(d.routed ? a.rt : a.sh, d, n0, s_x[warp][run % W4_RUNS], acc);
             } else {
-                float4* o = parts + ((warp * 2 + (begun ? 0 : 1)) * 2 * C) * 32 + lane;
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        o[(r * C + c) * 32] =
-                            make_float4(acc[r][c][0], acc[r][c][1], acc[r][c][2], acc[r][c][3]);
-                if (begun && tile_end <= cnt) {
-                    head = d;
-                    head_start = start_of(v0 + tile);
+                float4* o = parts + (warp * 2 + (begun ? 0 : 1)) * 64 + lane;
+                o[0] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][1][0], acc[0][1][1]);
+                o[32] = make_float4(acc[1][0][0], acc[1][0][1], acc[1][1][0], acc[1][1][1]);
+                if (begun && i + 1 == end) {
+                    ended = true;
+                    if (lane == 0) runs[W4_RUNS] = d;
+                    if (lane < W4_ROWS) s_x[warp][W4_RUNS][lane] = s_x[warp][run % W4_RUNS][lane];
                 }
             }
-            clear();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e >> 2][(e >> 1) & 1][e & 1] = 0.f;
             begun = false;
-            if (i + 1 < cnt) {
-                ++tile;
-                m = tiles[tile % TILES].m;
-                end = min(end_of(tile), cnt);
+            if (--tiles > 0) {
+                n0 += TN;
+            } else if (i + 1 < cnt) {
+                const W4Run& next_d = runs[++run % W4_RUNS];
+                tiles = next_d.tiles;
+                n0 = next_d.n0;
+                n = next_d.routed ? n_rt : n_sh;
             }
+            end += n;
         }
     }
     w4_cp_wait<0>();
     __syncthreads();
 
     // the parts of the tile that this warp ended, in stage order
-    if (head.m > 0) {
-        const int first = (int)((WARPS * (head_start - base + 1) - 1) / all);  // the warp that began it
-        for (int w = first; w <= warp; ++w) {
-            if (all * w / WARPS == all * (w + 1) / WARPS) continue;  // a warp without stages
-            const float4* o = parts + ((w * 2 + (w == first ? 1 : 0)) * 2 * C) * 32 + lane;
+    if (ended) {
+        const int64_t start = lo + first - base;                            // of the tile among the CTA's stages
+        const int w0 = (int)((W4_WARPS * (start + 1) - 1) / all);           // the warp that began it
+        for (int w = w0; w <= warp; ++w) {
+            if (all * w / W4_WARPS == all * (w + 1) / W4_WARPS) continue;  // a warp without stages
+            const float4* o = parts + (w * 2 + (w == w0 ? 1 : 0)) * 64 + lane;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const float4 f = o[(r * C + c) * 32];
-                    acc[r][c][0] += f.x;
-                    acc[r][c][1] += f.y;
-                    acc[r][c][2] += f.z;
-                    acc[r][c][3] += f.w;
-                }
+            for (int r = 0; r < 2; ++r) {
+                const float4 f = o[32 * r];
+                acc[r][0][0] += f.x;
+                acc[r][0][1] += f.y;
+                acc[r][1][0] += f.z;
+                acc[r][1][1] += f.w;
+            }
         }
-        w4_store<SWIGLU, C>(head.routed ? a.rt : a.sh, head, acc);
+        const W4Run& d = runs[W4_RUNS];
+        w4_store<SWIGLU>(d.routed ? a.rt : a.sh, d, d.n0, s_x[warp][W4_RUNS], acc);
     }
 }
 
@@ -692,7 +621,7 @@ cudaError_t launch_quantize_w4_rows(const uint16_t* w, int64_t rows, int K, int 
                     group / 8, reinterpret_cast<uint32_t*>(q), scale);
 }
 
-template <bool SWIGLU, int GS, int C>
+template <bool SWIGLU, int GS>
 static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t s) {
     // the shared-memory limit is set once per device
     static std::atomic<bool> ready[64];
@@ -700,9 +629,8 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const size_t smem = w4_smem_bytes(C);
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W4_SMEM);
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
@@ -710,36 +638,19 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     // (between one CTA an SM and as many as fit).
     constexpr int TN = SWIGLU ? 16 : 32;
     const int n_sh = (L.sh.K + 127) / 128, n_rt = (L.rt.K + 127) / 128;
-    const double sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + 8 * C - 1) / (8 * C)) : 0.0;
+    const double sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + W4_ROWS - 1) / W4_ROWS) : 0.0;
     const double rt = L.G > 0 ? (double)((L.rt.N_out + TN - 1) / TN) * std::min<int64_t>(L.rows_cap, L.G) : 0.0;
     const double even = (sh * n_sh + rt * n_rt) / std::max(sh > 0 ? n_sh : 1, rt > 0 ? n_rt : 1);
-    const double most = std::min(sh + rt, (double)w4_ctas(C) * num_sms);
+    const double most = std::min(sh + rt, (double)W4_CTAS * num_sms);
     const unsigned grid = (unsigned)std::max(1.0, std::min(most, std::max(even, (double)num_sms)));
-    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_WARPS * 32), smem, s, L);
-}
-
-template <bool SWIGLU, int GS>
-static cudaError_t launch_w4_rows(const W4Launch& L, int num_sms, cudaStream_t s) {
-    // Passes over the weights that the narrow kernel's 8 columns and the wide one's 32 take,
-    // in weight rows; a slot holds rows_cap / G rows on average.
-    const double sh = L.sh.wq ? (double)L.sh.N_out * L.sh.K : 0.0, rt = L.G > 0 ? (double)L.rt.N_out * L.rt.K : 0.0;
-    const double slots = (double)std::min<int64_t>(L.G, L.rows_cap);
-    const double mean = slots > 0 ? L.rows_cap / slots : 0.0;
-    auto passes = [&](int rows) {
-        return sh * std::ceil((double)L.rows_sh / rows) + rt * slots * std::max(1.0, mean / rows);
-    };
-#ifndef W4_WIDE
-#define W4_WIDE 1.5
-#endif
-    return passes(8) < W4_WIDE * passes(32) ? launch_w4_tiles<SWIGLU, GS, 1>(L, num_sms, s)
-                                            : launch_w4_tiles<SWIGLU, GS, 4>(L, num_sms, s);
+    return launch_k(L.name, w4_kernel<SWIGLU, GS>, dim3(grid), dim3(W4_THREADS), W4_SMEM, s, L);
 }
 
 template <bool SWIGLU>
 static cudaError_t launch_w4_group(const W4Launch& L, int num_sms, cudaStream_t s) {
-    if (L.group == 32) return launch_w4_rows<SWIGLU, 1>(L, num_sms, s);
-    if (L.group == 64) return launch_w4_rows<SWIGLU, 2>(L, num_sms, s);
-    return launch_w4_rows<SWIGLU, 4>(L, num_sms, s);
+    if (L.group == 32) return launch_w4_tiles<SWIGLU, 1>(L, num_sms, s);
+    if (L.group == 64) return launch_w4_tiles<SWIGLU, 2>(L, num_sms, s);
+    return launch_w4_tiles<SWIGLU, 4>(L, num_sms, s);
 }
 
 cudaError_t launch_w4_gemm(const W4Launch& L, int num_sms, cudaStream_t s) {
