@@ -466,9 +466,9 @@ MOE_API moe_status_t moe_quantize_w4_rows(const moe_bf16_t *w, int64_t rows, int
                                    moe_bf16_t *scale, moe_stream_t stream);
 
 /* moe_matvec_w4 -- y [M, N] bf16 = x [M, K] bf16 times W^T, W [N, K] in the format
- * above: products with a few rows (made for M up to 32; beyond, the weights are
- * read again, from L2 where they fit it, for every 32 rows).  Sums in
- * fp32, one rounding at the end; for M up to 8 a row's result does not depend on M.  x and q
+ * above: products with a few rows (made for M up to 16; beyond, the weights are
+ * read again, from L2 where they are still there, for every 16 rows).  Sums in
+ * fp32, one rounding at the end; for M up to 16 a row's result does not depend on M.  x and q
  * 16-byte, scale and y 2-byte aligned; M, N < 2^31.  No workspace. */
 MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const moe_bf16_t *scale, int64_t M, int N,
                                    int K, int group, moe_bf16_t *y, moe_stream_t stream);
@@ -489,9 +489,9 @@ MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const 
  *   ws       at least moe_workspace_size_w4 bytes
  * H, I and I_shared_total multiples of 64 and of group.  Entries of perm_src
  * outside [0, T*k) and of pair_row outside [-1, P_cap) are dropped and flagged.
- * Meant for decode batches (up to about 32 rows per slot); larger batches are
- * right, but a slot's weights are read again, from L2, for every 8 or 32 rows.  The
- * other arguments and errors as moe_forward. */
+ * Meant for decode batches (up to about 16 rows per slot); larger batches are
+ * right, but a slot's weights are read again, from L2, for every 16 rows.  The other
+ * arguments and errors as moe_forward. */
 MOE_API moe_status_t moe_forward_w4(const moe_bf16_t *x, const int32_t *offsets, int S_local, int64_t P_cap,
                                    const int32_t *perm_src, const uint8_t *W1q, const moe_bf16_t *W1_scale,
                                    const uint8_t *W2q, const moe_bf16_t *W2_scale, int H, int I, int group,

@@ -12,6 +12,8 @@
 // activations lie in memory.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
+#include <type_traits>
 
 #include "moe_internal.cuh"
 
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 
 // ---------------------------------------------------------------------------
 // Products on mma.sync.  The work is a list of tiles, 32 weight rows of one slot
-// (FC1: 16 gate rows and the matching 16 up rows) times up to 8 activation rows; a
+// (FC1: 16 gate rows and the matching 16 up rows) times up to 8 C activation rows; a
 // tile's K is cut into stages of 128.  Every CTA takes a contiguous range of the list,
 // about the same number of stages each, and its 8 warps take equal contiguous ranges
 // of those stages, whatever tiles they fall into.  A warp streams its stages through
@@ -69,11 +71,10 @@ constexpr int W4_THREADS = W4_WARPS * 32;
 constexpr int W4_CTAS = 2;       // on an SM
 constexpr int W4_RING = 4;       // stages in each warp's ring
 constexpr int W4_STAGE = 2048;   // bytes of a stage: 32 rows of 128 elements
-constexpr int W4_ROWS = 8;       // activation rows of a tile
 constexpr int W4_MAXG = 1024;    // slots
 constexpr int W4_RUNS = 8;       // runs a warp has in hand: the copies are three stages ahead
-// every warp's ring, then its parts of two shared tiles (8 sums a lane)
-constexpr size_t W4_SMEM = (size_t)W4_WARPS * (W4_RING * W4_STAGE + 2 * 32 * 8 * 4);
+// every warp's ring, then its parts of two shared tiles (8 C sums a lane)
+constexpr size_t w4_smem_bytes(int C) { return (size_t)W4_WARPS * (W4_RING * W4_STAGE + 2 * 32 * 8 * C * 4); }
 
 // Neighbouring tiles of the list with the same activation rows, from the first that a
 // warp has a stage of.
@@ -97,19 +98,15 @@ template <int N>
 __device__ __forceinline__ void w4_cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// n consecutive words of shared memory
-template <int n>
-__device__ __forceinline__ void w4_lds(uint32_t (&v)[n], uint32_t addr) {
-    if constexpr (n == 4)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                     : "r"(addr)
-                     : "memory");
-    else if constexpr (n == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr) : "memory");
+__device__ __forceinline__ uint32_t w4_lds32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
+__device__ __forceinline__ void w4_lds64(uint32_t (&v)[2], uint32_t addr) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr) : "memory");
+}
+
 // D = A B + C, A 16 x 16 (row), B 16 x 8 (column), bf16 inputs, fp32 sums
 __device__ __forceinline__ void w4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                        const float (&c)[4]) {
@@ -132,39 +129,35 @@ __device__ __forceinline__ uint32_t w4_pair(uint32_t word, int j) {
     return v;
 }
 
-// One group of a stage: acc += scales * (codes x activations).  w: the lane's words of
-// rows g + 8 q; xb: its activations; s: the scales of those rows.  Accumulators
-// [half][row g, g + 8][column 2t, 2t + 1], in units of 1/64.
-template <int GS>
-__device__ __forceinline__ void w4_group(float (&acc)[2][2][2], const uint32_t (&w)[4][GS], const uint32_t* xb,
-                                         const float (&s)[4]) {
-    float tmp[2][4] = {};
+// 32 elements of a stage: sum[column tile][half] += codes x activations.  u, v: the lane's
+// words of rows g and g + 8 of both 16-row halves; x: its activations of each column tile.
+template <int C8, int C>
+__device__ __forceinline__ void w4_step(float (&sum)[C][2][4], const uint32_t (&u)[2], const uint32_t (&v)[2],
+                                        const uint4 (&x)[C]) {
 #pragma unroll
-    for (int j = 0; j < GS; ++j)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t A[4] = {w4_pair(u[r], 2 * h), w4_pair(v[r], 2 * h), w4_pair(u[r], 2 * h + 1),
+                                   w4_pair(v[r], 2 * h + 1)};
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint32_t A[4] = {w4_pair(w[2 * r][j], 2 * h), w4_pair(w[2 * r + 1][j], 2 * h),
-                                       w4_pair(w[2 * r][j], 2 * h + 1), w4_pair(w[2 * r + 1][j], 2 * h + 1)};
-                w4_mma(tmp[r], A, xb[4 * j + 2 * h], xb[4 * j + 2 * h + 1], tmp[r]);
-            }
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][i / 2][i % 2] = fmaf(s[2 * r + i / 2], tmp[r][i], acc[r][i / 2][i % 2]);
+            for (int c = 0; c < C8; ++c)
+                w4_mma(sum[c][r], A, h ? x[c].z : x[c].x, h ? x[c].w : x[c].y, sum[c][r]);
+        }
 }
 
-// The outputs of the tile at n0 from its accumulators.  xrow: the activation row of each
+// The outputs of the tile at n0 from its accumulators [column tile][half][4], in units
+// of 1/64: row g or g + 8 and column 2t or 2t + 1 as the product leaves them.  xrow: the activation row of each
 // column, -1 for one that the tables got wrong (its outputs are zero).
-template <bool SWIGLU>
+template <bool SWIGLU, int C>
 __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int n0, const int32_t* xrow,
-                                         const float (&acc)[2][2][2]) {
+                                         const float (&acc)[C][2][4]) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
     const int64_t N = p.N_out;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int col = 2 * t + c;
+    for (int c = 0; c < 2 * C; ++c) {
+        if (c == 2 && d.m <= 8) break;
+        const int col = 8 * (c / 2) + 2 * t + c % 2;
         if (col >= d.m) continue;
         const float unit = xrow[col] < 0 ? 0.f : 64.f;
         const int64_t at = (d.row0 + col) * N + n0 + g;
@@ -172,7 +165,7 @@ __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) v[r][h] = acc[r][h][c] * unit;
+            for (int h = 0; h < 2; ++h) v[r][h] = acc[c / 2][r][2 * h + c % 2] * unit;
         if (SWIGLU) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -194,21 +187,23 @@ __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int
     }
 }
 
-template <bool SWIGLU, int GS>
+template <bool SWIGLU, int GS, int C>
 __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_constant__ W4Launch a) {
+    constexpr int ROWS = 8 * C;  // activation rows of a tile
     extern __shared__ __align__(128) uint8_t w4_smem[];
     __shared__ int32_t s_pre[W4_MAXG];  // routed tiles before each slot
     __shared__ int32_t s_part[W4_WARPS];
     __shared__ W4Run s_run[W4_WARPS][W4_RUNS + 1];            // in the last place, that of a tile
-    __shared__ int32_t s_x[W4_WARPS][W4_RUNS + 1][W4_ROWS];  // begun by an earlier warp; columns' activation rows
-    constexpr int TN = SWIGLU ? 16 : 32;  // outputs of a tile
-    constexpr int NF = 4 / GS;            // groups in a stage
+    __shared__ int32_t s_x[W4_WARPS][W4_RUNS + 1][ROWS];  // begun by an earlier warp; columns' activation rows
+    constexpr int TN = SWIGLU ? 16 : 32;   // outputs of a tile
+    constexpr int NF = 4 / GS;             // groups in a stage
+    constexpr int WORDS = GS < 2 ? 1 : 2;  // consecutive words of a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     // pieces rotate within a row of a stage so that the reads below meet every bank once
     const int sw = ((g >> 1) & 1) * 2 + (g >> 2);
     const uint32_t ring0 = smem_u32(w4_smem) + warp * (W4_RING * W4_STAGE);
-    // part [warp][0: of a tile begun by an earlier warp, 1: of one begun here][4 values][lane]
+    // part [warp][0: of a tile begun by an earlier warp, 1: of one begun here][2 C x 4 values][lane]
     float4* parts = reinterpret_cast<float4*>(w4_smem + W4_WARPS * W4_RING * W4_STAGE);
     // What a previous kernel may still be writing is waited for as late as the call allows:
     // the tables here, the weights before their first copy, the activations after it.
@@ -219,7 +214,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
 
     // the list: the dense problem's tiles, then the routed ones by slot; the row tiles of
     // one weight tile are neighbours
-    const int ct_sh = (int)((a.rows_sh + W4_ROWS - 1) / W4_ROWS);
+    const int ct_sh = (int)((a.rows_sh + ROWS - 1) / ROWS);
     const int n_sh = (a.sh.K + 127) / 128, n_rt = (a.rt.K + 127) / 128;  // stages of a tile
     const int tiles_rt = (a.rt.N_out + TN - 1) / TN;
     const int64_t list_sh = a.sh.wq ? (int64_t)((a.sh.N_out + TN - 1) / TN) * ct_sh : 0;
@@ -235,7 +230,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             if (s0 + i < a.G) {
                 const int64_t hi = __ldg(a.offsets + s0 + i + 1);
                 const int64_t m = max((int64_t)0, min(hi, a.rows_cap) - max(lo, (int64_t)0));
-                n[i] = (int)((m + W4_ROWS - 1) / W4_ROWS) * tiles_rt;
+                n[i] = (int)((m + ROWS - 1) / ROWS) * tiles_rt;
                 lo = hi;
             }
             sum += n[i];
@@ -312,15 +307,15 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             d.routed = true;
             d.row0 = max(0, __ldg(a.offsets + s_lo));
             rows = min((int64_t)__ldg(a.offsets + s_lo + 1), a.rows_cap);
-            ct = (int)((rows - d.row0 + W4_ROWS - 1) / W4_ROWS);
+            ct = (int)((rows - d.row0 + ROWS - 1) / ROWS);
             q = w - s_pre[s_lo];
             at = s_lo * (SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out);
         }
         const W4Problem& p = d.routed ? a.rt : a.sh;
         const int tile = q / ct;
         d.n0 = tile * TN;
-        d.row0 += (int64_t)(q - tile * ct) * W4_ROWS;
-        d.m = (int)min((int64_t)W4_ROWS, rows - d.row0);
+        d.row0 += (int64_t)(q - tile * ct) * ROWS;
+        d.m = (int)min((int64_t)ROWS, rows - d.row0);
         d.wq = p.wq + (at + d.n0) * (p.K / 2);
         d.ws = p.ws + (at + d.n0) * (p.K / (32 * GS));
         // a last tile with fewer outputs stands alone: some of its rows repeat
@@ -396,18 +391,19 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         pdl_trigger();
     }
 
-    const uint16_t* xsrc = nullptr;  // the lane's activations, of column g (past the tile's rows: its last one)
+    const uint16_t* xsrc[C] = {};    // the lane's activations, of column g of each eight (past the rows: the last)
     const uint16_t* ssrc = nullptr;  // the scales of weight row g + 8 t
-    int p_run = -1, p_tiles = 1, p_end = first, p_n = 0, p_step = 0;
+    int p_run = -1, p_tiles = 1, p_end = first, p_n = 0, p_step = 0, p_m = 0;
     int p_cut = 0;  // elements of a row's last stage
     auto next_p = [&](int j) {  // the activations' and scales' next tile
-        if (--p_tiles > 0) {
+        if (--p_tiles > 0) {  // (called with the pointers at the tile's last stage)
             ssrc += p_step;
-            xsrc -= p_n * 128;
+#pragma unroll
+            for (int c = 0; c < C; ++c) xsrc[c] -= (p_n - 1) * 128;
         } else {
             const W4Run& d = runs[++p_run % W4_RUNS];
             const W4Problem& p = d.routed ? a.rt : a.sh;
-            if (lane < W4_ROWS) {  // FC1 reads the routing table for the rows
+            if (lane < ROWS) {  // FC1 reads the routing table for the rows
                 int32_t r = (int32_t)(d.row0 + min(lane, d.m - 1));
                 if (d.routed && a.perm_src) {
                     const int32_t q = a.perm_src[r];
@@ -420,92 +416,150 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             __syncwarp();
             p_n = d.routed ? n_rt : n_sh;
             p_tiles = d.tiles;
-            p_step = TN * (p.K / (32 * GS)) - p_n * NF;
+            p_m = d.m;
+            p_step = TN * (p.K / (32 * GS)) - (p_n - 1) * NF;
             p_cut = p.K - (p_n - 1) * 128;
             ssrc = d.ws + (int64_t)row_of(p, d, t) * (p.K / (32 * GS)) + (j - p_end) * NF;
-            xsrc = p.x + (int64_t)max(s_x[warp][p_run % W4_RUNS][g], 0) * p.K + (j - p_end) * 128 + t * 8 * GS;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                xsrc[c] = p.x + (int64_t)max(s_x[warp][p_run % W4_RUNS][8 * c + g], 0) * p.K + (j - p_end) * 128 +
+                          t * 8 * WORDS;
         }
         p_end += p_n;
     };
-    uint32_t xb[16], sb[NF];
-    auto load = [&](int f, int has) {  // group f of their stage, which holds `has` elements
-        if (f * 32 * GS < has) {
+    // A stage is two halves of two steps of 32 elements; the lane's word of a step is its word
+    // of the half's t-th pair of words, or (groups of 32) the t-th word of the step.  Scales
+    // are fetched a stage ahead, activations as far as registers allow: a stage, or with
+    // sixteen columns half of one.
+    constexpr int AHEAD = C == 1 ? 4 : 2;  // steps
+    uint4 xb[AHEAD][C];
+    uint32_t sb[NF];
+    auto load_x = [&](int step, int has) {  // of the stage at xsrc, which holds `has` elements
+        const int at = step / 2 * 64 + step % 2 * (GS < 2 ? 32 : 8);
+        if (GS == 4 || step / GS * 32 * GS < has) {
 #pragma unroll
-            for (int j = 0; j < GS; ++j) {
-                const uint4 u = *reinterpret_cast<const uint4*>(xsrc + f * 32 * GS + j * 8);
-                uint32_t* o = xb + 4 * (f * GS + j);
-                o[0] = u.x;
-                o[1] = u.y;
-                o[2] = u.z;
-                o[3] = u.w;
-            }
-            sb[f] = __ldg(ssrc + f);
+            for (int c = 0; c < C; ++c)
+                if (c == 0 || p_m > 8) xb[step % AHEAD][c] = *reinterpret_cast<const uint4*>(xsrc[c] + at);
         }
     };
-    auto step = [&] {
-        ssrc += NF;
-        xsrc += 128;
+    auto load_s = [&](int f, int has) {
+        if (f * 32 * GS < has) sb[f] = __ldg(ssrc + f);
     };
-    float acc[2][2][2] = {};
+    float acc[C][2][4] = {};
     int left = 0;  // elements of the stage that is multiplied next
-    int run = 0, tiles = 0, n0 = 0, end = 0, n = 0;
+    int run = 0, tiles = 0, n0 = 0, end = 0, n = 0, m = 0;
     if (cnt > 0) {
         next_p(0);
         left = GS < 4 && p_end == 1 ? p_cut : 128;
 #pragma unroll
-        for (int f = 0; f < NF; ++f) load(f, left);
-        step();
+        for (int f = 0; f < NF; ++f) load_s(f, left);
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) load_x(j, left);
         tiles = runs[0].tiles;
         n0 = runs[0].n0;
+        m = runs[0].m;
         n = runs[0].routed ? n_rt : n_sh;
         end = first + n;
     }
     bool begun = first < 0;  // the tile in hand was begun by an earlier warp
     bool ended = false;      // and this one ended it
 
+    // the products of stage i, in column tiles of a tile's rows
+    auto multiply = [&](int i, auto columns) {
+        constexpr int C8 = decltype(columns)::value;
+        const uint32_t slot = r_slot + r_off;
+        float sum[C][2][4];
+        int next = 0;  // elements of the next stage
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half == 2 - AHEAD / 2) {  // from here on the next stage's activations and scales are fetched
+                if (i + 1 == p_end && i + 1 < cnt) {
+                    next_p(i + 1);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) xsrc[c] += 128;
+                    ssrc += NF;
+                }
+                next = i + 1 < cnt ? (GS < 4 && i + 2 == p_end ? p_cut : 128) : 0;
+            }
+            uint32_t w[4][2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (GS < 2) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        w[q][j] = w4_lds32(slot + q * 512 + (((half * 2 + j) ^ sw) << 4) + t * 4);
+                } else {
+                    w4_lds64(w[q], slot + q * 512 + (((half * 2 + (t >> 1)) ^ sw) << 4) + (t & 1) * 8);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int step = 2 * half + j, f = step / GS;
+                if (step % GS == 0) {
+#pragma unroll
+                    for (int e = 0; e < 8 * C8; ++e) sum[e >> 3][(e >> 2) & 1][e & 3] = 0.f;
+                }
+                if (GS == 4 || f * 32 * GS < left) {
+                    const uint32_t u[2] = {w[0][j], w[2][j]}, v[2] = {w[1][j], w[3][j]};
+                    w4_step<C8, C>(sum, u, v, xb[step % AHEAD]);
+                    if (step % GS == GS - 1) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float sc = bf16_bits_to_float(__shfl_sync(0xffffffffu, sb[f], (lane & 28) | q));
+                            const int r = q >> 1, h = 2 * (q & 1);
+#pragma unroll
+                            for (int c = 0; c < C8; ++c) {
+                                acc[c][r][h] = fmaf(sc, sum[c][r][h], acc[c][r][h]);
+                                acc[c][r][h + 1] = fmaf(sc, sum[c][r][h + 1], acc[c][r][h + 1]);
+                            }
+                        }
+                    }
+                }
+                // the registers take the values of AHEAD steps on
+                if (step + AHEAD >= 4)
+                    load_x((step + AHEAD) % 4, next);
+                else
+                    load_x(step + AHEAD, left);
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f) load_s(f, next);
+        left = next;
+    };
+
 #pragma unroll 1
     for (int i = 0; i < cnt; ++i) {
         issue(i + W4_RING - 1);
-        if (i + 1 == p_end && i + 1 < cnt) next_p(i + 1);
-        const int next = i + 1 < cnt ? (GS < 4 && i + 2 == p_end ? p_cut : 128) : 0;
         w4_cp_wait<W4_RING - 1>();
         __syncwarp();
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            if (NF == 1 || f * 32 * GS < left) {
-                // words 0 .. GS-1 of this lane in the group: elements t * 8 GS .. of the rows g + 8 q
-                uint32_t w[4][GS];
-                float s[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int byte = f * 16 * GS + t * 4 * GS;
-                    w4_lds<GS>(w[q], r_slot + r_off + q * 512 + (((byte >> 4) ^ sw) << 4) + (byte & 15));
-                    s[q] = bf16_bits_to_float(__shfl_sync(0xffffffffu, sb[f], (lane & 28) | q));
-                }
-                w4_group<GS>(acc, w, xb + 4 * f * GS, s);
-            }
-            load(f, next);  // the same registers take the next stage's values
-        }
+        if (C == 1 || m <= 8)
+            multiply(i, std::integral_constant<int, 1>());
+        else
+            multiply(i, std::integral_constant<int, C>());
         __syncwarp();  // the ring slot just read is the next one written
-        left = next;
-        step();
         r_off = (r_off + W4_STAGE) & (W4_RING * W4_STAGE - 1);
         if (i + 1 == end || i + 1 == cnt) {  // the tile's last stage here
             const W4Run& d = runs[run % W4_RUNS];
             if (!begun && i + 1 == end) {
-                w4_store<SWIGLU>(d.routed ? a.rt : a.sh, d, n0, s_x[warp][run % W4_RUNS], acc);
+                w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, n0, s_x[warp][run % W4_RUNS], acc);
             } else {
-                float4* o = parts + (warp * 2 + (begun ? 0 : 1)) * 64 + lane;
-                o[0] = make_float4(acc[0][0][0], acc[0][0][1], acc[0][1][0], acc[0][1][1]);
-                o[32] = make_float4(acc[1][0][0], acc[1][0][1], acc[1][1][0], acc[1][1][1]);
+                float4* o = parts + (warp * 2 + (begun ? 0 : 1)) * (64 * C) + lane;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    if (c && d.m <= 8) break;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        o[(2 * c + r) * 32] = make_float4(acc[c][r][0], acc[c][r][1], acc[c][r][2], acc[c][r][3]);
+                }
                 if (begun && i + 1 == end) {
                     ended = true;
                     if (lane == 0) runs[W4_RUNS] = d;
-                    if (lane < W4_ROWS) s_x[warp][W4_RUNS][lane] = s_x[warp][run % W4_RUNS][lane];
+                    if (lane < ROWS) s_x[warp][W4_RUNS][lane] = s_x[warp][run % W4_RUNS][lane];
                 }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e >> 2][(e >> 1) & 1][e & 1] = 0.f;
+            for (int e = 0; e < 8 * C; ++e) acc[e >> 3][(e >> 2) & 1][e & 3] = 0.f;
             begun = false;
             if (--tiles > 0) {
                 n0 += TN;
@@ -513,6 +567,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
                 const W4Run& next_d = runs[++run % W4_RUNS];
                 tiles = next_d.tiles;
                 n0 = next_d.n0;
+                m = next_d.m;
                 n = next_d.routed ? n_rt : n_sh;
             }
             end += n;
@@ -527,18 +582,22 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         const int w0 = (int)((W4_WARPS * (start + 1) - 1) / all);           // the warp that began it
         for (int w = w0; w <= warp; ++w) {
             if (all * w / W4_WARPS == all * (w + 1) / W4_WARPS) continue;  // a warp without stages
-            const float4* o = parts + (w * 2 + (w == w0 ? 1 : 0)) * 64 + lane;
+            const float4* o = parts + (w * 2 + (w == w0 ? 1 : 0)) * (64 * C) + lane;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float4 f = o[32 * r];
-                acc[r][0][0] += f.x;
-                acc[r][0][1] += f.y;
-                acc[r][1][0] += f.z;
-                acc[r][1][1] += f.w;
+            for (int c = 0; c < C; ++c) {
+                if (c && runs[W4_RUNS].m <= 8) break;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float4 f = o[(2 * c + r) * 32];
+                    acc[c][r][0] += f.x;
+                    acc[c][r][1] += f.y;
+                    acc[c][r][2] += f.z;
+                    acc[c][r][3] += f.w;
+                }
             }
         }
         const W4Run& d = runs[W4_RUNS];
-        w4_store<SWIGLU>(d.routed ? a.rt : a.sh, d, d.n0, s_x[warp][W4_RUNS], acc);
+        w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, d.n0, s_x[warp][W4_RUNS], acc);
     }
 }
 
@@ -621,7 +680,7 @@ cudaError_t launch_quantize_w4_rows(const uint16_t* w, int64_t rows, int K, int 
                     group / 8, reinterpret_cast<uint32_t*>(q), scale);
 }
 
-template <bool SWIGLU, int GS>
+template <bool SWIGLU, int GS, int C>
 static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t s) {
     // the shared-memory limit is set once per device
     static std::atomic<bool> ready[64];
@@ -630,7 +689,7 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)W4_SMEM);
+        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem_bytes(C));
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
@@ -638,19 +697,31 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     // (between one CTA an SM and as many as fit).
     constexpr int TN = SWIGLU ? 16 : 32;
     const int n_sh = (L.sh.K + 127) / 128, n_rt = (L.rt.K + 127) / 128;
-    const double sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + W4_ROWS - 1) / W4_ROWS) : 0.0;
+    const double sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + 8 * C - 1) / (8 * C)) : 0.0;
     const double rt = L.G > 0 ? (double)((L.rt.N_out + TN - 1) / TN) * std::min<int64_t>(L.rows_cap, L.G) : 0.0;
     const double even = (sh * n_sh + rt * n_rt) / std::max(sh > 0 ? n_sh : 1, rt > 0 ? n_rt : 1);
     const double most = std::min(sh + rt, (double)W4_CTAS * num_sms);
     const unsigned grid = (unsigned)std::max(1.0, std::min(most, std::max(even, (double)num_sms)));
-    return launch_k(L.name, w4_kernel<SWIGLU, GS>, dim3(grid), dim3(W4_THREADS), W4_SMEM, s, L);
+    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), w4_smem_bytes(C), s, L);
+}
+
+template <bool SWIGLU, int GS>
+static cudaError_t launch_w4_rows(const W4Launch& L, int num_sms, cudaStream_t s) {
+    // Passes over the weights in pieces of 8 and of 16 rows (a slot holds rows_cap / G rows on
+    // average): one of 16 takes 1.6 times as long as one of 8 (65536 x 7168: 77 and 49 us).
+    const double sh = L.sh.wq ? (double)L.sh.N_out * L.sh.K : 0.0;
+    const double slots = (double)std::min<int64_t>(L.G, L.rows_cap);
+    const double rt = slots * L.rt.N_out * L.rt.K, mean = slots > 0 ? L.rows_cap / slots : 0.0;
+    auto passes = [&](double rows) { return sh * std::ceil(L.rows_sh / rows) + rt * std::max(1.0, mean / rows); };
+    return passes(8) <= 1.6 * passes(16) ? launch_w4_tiles<SWIGLU, GS, 1>(L, num_sms, s)
+                                         : launch_w4_tiles<SWIGLU, GS, 2>(L, num_sms, s);
 }
 
 template <bool SWIGLU>
 static cudaError_t launch_w4_group(const W4Launch& L, int num_sms, cudaStream_t s) {
-    if (L.group == 32) return launch_w4_tiles<SWIGLU, 1>(L, num_sms, s);
-    if (L.group == 64) return launch_w4_tiles<SWIGLU, 2>(L, num_sms, s);
-    return launch_w4_tiles<SWIGLU, 4>(L, num_sms, s);
+    if (L.group == 32) return launch_w4_rows<SWIGLU, 1>(L, num_sms, s);
+    if (L.group == 64) return launch_w4_rows<SWIGLU, 2>(L, num_sms, s);
+    return launch_w4_rows<SWIGLU, 4>(L, num_sms, s);
 }
 
 cudaError_t launch_w4_gemm(const W4Launch& L, int num_sms, cudaStream_t s) {

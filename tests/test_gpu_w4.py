@@ -128,8 +128,8 @@ def test_matvec_nonfinite_values_stay_in_their_row():
 
 @pytest.mark.parametrize("N,K,group", [(64, 2048, 128), (4096, 512, 64), (513, 1408, 32)])
 def test_matvec_rows_do_not_depend_on_the_batch(N, K, group):
-    x, q, s, y = _matvec(8, N, K, group, seed=7)
-    for m in (0, 3, 7):
+    x, q, s, y = _matvec(16, N, K, group, seed=7)
+    for m in (0, 7, 8, 15):
         one = torch.empty(1, N, dtype=torch.bfloat16, device="cuda")
         moe.moe_matvec_w4(x[m:m + 1], q, s, one)
         assert torch.equal(one[0], y[m])
