@@ -17,15 +17,14 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
-#include <mutex>
 
 #include "moe_internal.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int NM_THREADS = 256;
-constexpr int NM_WARPS = NM_THREADS / 32;
+constexpr int NM_WARPS = 8;      // rows of a CTA whose warps take one each
+constexpr int NM_CTAS = 64;      // CTAs an SM before they loop over rows
 
 __device__ __forceinline__ void nm_load8(const uint16_t* p, float f[8]) {
     unpack8(*reinterpret_cast<const uint4*>(p), f);
@@ -61,23 +60,28 @@ __device__ __forceinline__ uint32_t nm_e4m3x4(const float* f, float inv) {
     return lo | (hi << 16);
 }
 
-// One CTA per row at a time (grid-stride): each thread owns VPT vectors of 8 values.
-template <int VPT, bool F32>
-__global__ void __launch_bounds__(NM_THREADS) add_rmsnorm_kernel(const __grid_constant__ NormLaunch a) {
-    __shared__ float red_sum[2][NM_WARPS];
-    __shared__ uint32_t red_max[2][NM_WARPS];
+// THREADS threads per row at a time, each with VPT vectors of 8 values (grid-stride over
+// rows): a CTA, or (THREADS = 32) each of its NM_WARPS warps by itself.
+template <int VPT, int THREADS, bool F32>
+__global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rmsnorm_kernel(const __grid_constant__ NormLaunch a) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ float red_sum[2][WARPS];
+    __shared__ uint32_t red_max[2][WARPS];
+    constexpr bool ALONE = THREADS == 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = ALONE ? lane : threadIdx.x;
     const int vec = a.H / 8;
     pdl_wait();
     pdl_trigger();
     int it = 0;
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, it ^= 1) {
+    const int64_t rows = (int64_t)gridDim.x * (ALONE ? NM_WARPS : 1);
+    for (int64_t row = ALONE ? (int64_t)blockIdx.x * NM_WARPS + warp : blockIdx.x; row < a.T; row += rows, it ^= 1) {
         const int64_t base = row * a.H;
         float f[VPT][8];
         float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * NM_THREADS;
+            const int v = first + j * THREADS;
             if (v >= vec) continue;
             nm_load8(a.x + base + 8 * v, f[j]);
             if (a.residual) {
@@ -91,16 +95,25 @@ __global__ void __launch_bounds__(NM_THREADS) add_rmsnorm_kernel(const __grid_co
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        if (lane == 0) red_sum[it][warp] = ss;
-        __syncthreads();
-        float tot = 0.f;
+        float tot = ss;
+        if (!ALONE) {
+            if (lane == 0) red_sum[it][warp] = ss;
+            __syncthreads();
+            tot = 0.f;
 #pragma unroll
-        for (int w = 0; w < NM_WARPS; ++w) tot += red_sum[it][w];
-        const float rstd = __frsqrt_rn(tot / (float)a.H + a.eps);
+            for (int w = 0; w < WARPS; ++w) tot += red_sum[it][w];
+        }
+        // rstd to twice binary32's precision: its rounding would move a whole row of y by up
+        // to 2^-24 and with it every E4M3 code that sits on a boundary
+        const float ms = tot / (float)a.H + a.eps;
+        const float hi = __frsqrt_rn(ms);
+        const float sq = ms * hi, err = fmaf(-sq, hi, 1.f) - fmaf(ms, hi, -sq) * hi;
+        float lo = 0.5f * hi * err;
+        if (!(fabsf(lo) < hi)) lo = 0.f;  // not finite: an infinite or zero mean square
         uint32_t mx = 0u;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * NM_THREADS;
+            const int v = first + j * THREADS;
             if (v >= vec) continue;
             if (a.residual_out) {
                 if (F32) {
@@ -115,23 +128,25 @@ __global__ void __launch_bounds__(NM_THREADS) add_rmsnorm_kernel(const __grid_co
             nm_load8(a.weight + 8 * v, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                f[j][i] = (f[j][i] * rstd) * w[i];
+                f[j][i] = fmaf(f[j][i], hi, f[j][i] * lo) * w[i];
                 mx = max(mx, __float_as_uint(f[j][i]) & 0x7FFFFFFFu);
             }
             if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = nm_pack8(f[j]);
         }
         if (!a.q) continue;
         mx = __reduce_max_sync(0xffffffffu, mx);
-        if (lane == 0) red_max[it][warp] = mx;
-        __syncthreads();
+        if (!ALONE) {
+            if (lane == 0) red_max[it][warp] = mx;
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < NM_WARPS; ++w) mx = max(mx, red_max[it][w]);
+            for (int w = 0; w < WARPS; ++w) mx = max(mx, red_max[it][w]);
+        }
         const int e = nm_exponent(__uint_as_float(mx));
         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-        if (threadIdx.x == 0) a.scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (first == 0) a.scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = threadIdx.x + j * NM_THREADS;
+            const int v = first + j * THREADS;
             if (v < vec)
                 *reinterpret_cast<uint2*>(a.q + base + 8 * v) =
                     make_uint2(nm_e4m3x4(f[j], inv), nm_e4m3x4(f[j] + 4, inv));
@@ -139,21 +154,34 @@ __global__ void __launch_bounds__(NM_THREADS) add_rmsnorm_kernel(const __grid_co
     }
 }
 
-template <int VPT>
-cudaError_t launch_norm_vpt(const NormLaunch& L, unsigned grid, cudaStream_t s) {
-    if (L.f32) return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, true>, dim3(grid), dim3(NM_THREADS), 0, s, L);
-    return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, false>, dim3(grid), dim3(NM_THREADS), 0, s, L);
+template <int VPT, int THREADS, bool F32>
+cudaError_t launch_norm_size(const NormLaunch& L, int num_sms, cudaStream_t s) {
+    constexpr int ROWS = THREADS == 32 ? NM_WARPS : 1;
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T + ROWS - 1) / ROWS, (int64_t)num_sms * NM_CTAS);
+    return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, THREADS, F32>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
+}
+
+template <bool F32>
+cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
+    // A warp to a row while its lanes hold it in two vectors each, then one vector a thread
+    // to 2048 values, and a CTA of 224 or 256 threads with four: at 7168 values (16384 rows
+    // with E4M3 rows) four of 224 threads take 164 us, two of 448 take 201, one of 896 197
+    // and four of 256 (an eighth of them idle) 175.
+    const int vec = L.H / 8;
+    if (vec <= 32) return launch_norm_size<1, 32, F32>(L, num_sms, s);
+    if (vec <= 64) return launch_norm_size<2, 32, F32>(L, num_sms, s);
+    if (vec <= 128) return launch_norm_size<1, 128, F32>(L, num_sms, s);
+    if (vec <= 256) return launch_norm_size<1, 256, F32>(L, num_sms, s);
+    if (vec <= 512) return launch_norm_size<2, 256, F32>(L, num_sms, s);
+    if (vec <= 896) return launch_norm_size<4, 224, F32>(L, num_sms, s);
+    if (vec <= 1024) return launch_norm_size<4, 256, F32>(L, num_sms, s);
+    return launch_norm_size<4, 512, F32>(L, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const NormLaunch& L, int num_sms, cudaStream_t s) {
-    const int vpt = (L.H / 8 + NM_THREADS - 1) / NM_THREADS;
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(L.T, (int64_t)num_sms * 8));
-    if (vpt <= 1) return launch_norm_vpt<1>(L, grid, s);
-    if (vpt <= 2) return launch_norm_vpt<2>(L, grid, s);
-    if (vpt <= 4) return launch_norm_vpt<4>(L, grid, s);
-    return launch_norm_vpt<8>(L, grid, s);
+    return L.f32 ? launch_norm_type<true>(L, num_sms, s) : launch_norm_type<false>(L, num_sms, s);
 }
 
 }  // namespace moe
