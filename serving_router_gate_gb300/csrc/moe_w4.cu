@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     uint32_t sb[NF];
     auto load_x = [&](int step, int has) {  // of the stage at xsrc, which holds `has` elements
         const int at = step / 2 * 64 + step % 2 * (GS < 2 ? 32 : 8);
-        if (GS == 4 || step / GS * 32 * GS < has) {
+        if (step / GS * 32 * GS < has) {  // (has = 0: there is no such stage, and xsrc may lie past x)
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 if (c == 0 || p_m > 8) xb[step % AHEAD][c] = *reinterpret_cast<const uint4*>(xsrc[c] + at);

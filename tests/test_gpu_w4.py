@@ -143,6 +143,25 @@ def test_matvec_writes_only_its_outputs():
     _check_matvec(x, q, s, buf[1:4])
 
 
+def _at_the_end(t):
+    """A copy of t whose last byte is the last of its allocation (whole pages of 2 MiB, a segment of its own)."""
+    n = t.numel() * t.element_size()
+    buf = torch.empty(-(-n // (2 << 20)) * (2 << 20) + (32 << 20), dtype=torch.uint8, device="cuda")
+    out = buf[buf.numel() - n:].view(t.dtype).view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("M,N,K,group", [(1, 64, 512, 128), (8, 64, 1024, 128), (16, 96, 512, 128), (5, 32, 256, 64),
+                                         (9, 32, 96, 32)])
+def test_matvec_operands_that_end_with_their_allocations(M, N, K, group):
+    # no read goes past the last row's end, whatever the fetches ahead ask for
+    x, q, s, want = _matvec(M, N, K, group, seed=9)
+    y = _at_the_end(torch.zeros_like(want))
+    moe.moe_matvec_w4(_at_the_end(x), _at_the_end(q), _at_the_end(s), y)
+    assert torch.equal(y, want)
+
+
 def test_matvec_empty_batch():
     q, s = _weights((8,), 64, 64, 1)
     n = moe.moe_get_launch_count()
