@@ -87,6 +87,9 @@ struct W4Run {
     bool routed;
 };
 
+// a value that every lane of the warp has, said so
+__device__ __forceinline__ int w4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 __device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     constexpr int TN = SWIGLU ? 16 : 32;   // outputs of a tile
     constexpr int NF = 4 / GS;             // groups in a stage
     constexpr int WORDS = GS < 2 ? 1 : 2;  // consecutive words of a lane
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = w4_uniform(threadIdx.x >> 5);
     const int g = lane >> 2, t = lane & 3;
     // pieces rotate within a row of a stage so that the reads below meet every bank once
     const int sw = ((g >> 1) & 1) * 2 + (g >> 2);
@@ -341,8 +344,8 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             locate(++w_run);
             const W4Run& d = runs[w_run % W4_RUNS];
             const W4Problem& p = d.routed ? a.rt : a.sh;
-            w_n = d.routed ? n_rt : n_sh;
-            w_tiles = d.tiles;
+            w_n = w4_uniform(d.routed) ? n_rt : n_sh;
+            w_tiles = w4_uniform(d.tiles);
             w_step = TN * (p.K / 2) - w_n * 64;
             w_cut = GS < 4 && t * 32 >= p.K - (w_n - 1) * 128;
 #pragma unroll
@@ -414,9 +417,9 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
                 s_x[warp][p_run % W4_RUNS][lane] = r;
             }
             __syncwarp();
-            p_n = d.routed ? n_rt : n_sh;
-            p_tiles = d.tiles;
-            p_m = d.m;
+            p_n = w4_uniform(d.routed) ? n_rt : n_sh;
+            p_tiles = w4_uniform(d.tiles);
+            p_m = w4_uniform(d.m);
             p_step = TN * (p.K / (32 * GS)) - (p_n - 1) * NF;
             p_cut = p.K - (p_n - 1) * 128;
             ssrc = d.ws + (int64_t)row_of(p, d, t) * (p.K / (32 * GS)) + (j - p_end) * NF;
@@ -455,10 +458,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         for (int f = 0; f < NF; ++f) load_s(f, left);
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) load_x(j, left);
-        tiles = runs[0].tiles;
+        tiles = w4_uniform(runs[0].tiles);
         n0 = runs[0].n0;
-        m = runs[0].m;
-        n = runs[0].routed ? n_rt : n_sh;
+        m = w4_uniform(runs[0].m);
+        n = w4_uniform(runs[0].routed) ? n_rt : n_sh;
         end = first + n;
     }
     bool begun = first < 0;  // the tile in hand was begun by an earlier warp
@@ -565,10 +568,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
                 n0 += TN;
             } else if (i + 1 < cnt) {
                 const W4Run& next_d = runs[++run % W4_RUNS];
-                tiles = next_d.tiles;
+                tiles = w4_uniform(next_d.tiles);
                 n0 = next_d.n0;
-                m = next_d.m;
-                n = next_d.routed ? n_rt : n_sh;
+                m = w4_uniform(next_d.m);
+                n = w4_uniform(next_d.routed) ? n_rt : n_sh;
             }
             end += n;
         }
