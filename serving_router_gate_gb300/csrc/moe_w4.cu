@@ -89,6 +89,11 @@ struct W4Run {
 
 // a value that every lane of the warp has, said so
 __device__ __forceinline__ int w4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ const uint8_t* w4_uniform(const uint8_t* p) {
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = w4_uniform((int)(uint32_t)v), hi = w4_uniform((int)(v >> 32));
+    return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
+}
 
 __device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -333,24 +338,32 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         return SWIGLU ? (q < 2 ? r : r - 16 + p.N_out) : min(r, p.N_out - 1 - d.n0);
     };
 
-    const uint8_t* wsrc[4];
+    // rows g, g + 8 from the first base, g + 16, g + 24 (FC1: the up rows g, g + 8) from the second
+    const uint8_t *w_base0 = nullptr, *w_base1 = nullptr;
+    uint32_t woff[4];
     int w_run = -1, w_tiles = 1, w_end = first, w_n = 0, w_step = 0;
     bool w_cut = false;             // the lane's piece lies past the end of a row's last stage
     auto next_w = [&](int j) {  // the copies' next tile
         if (--w_tiles > 0) {
+            w_base0 += w_step;
+            w_base1 += w_step;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) wsrc[q] += w_step;
+            for (int q = 0; q < 4; ++q) woff[q] -= w_n * 64;
         } else {
             locate(++w_run);
             const W4Run& d = runs[w_run % W4_RUNS];
             const W4Problem& p = d.routed ? a.rt : a.sh;
             w_n = w4_uniform(d.routed) ? n_rt : n_sh;
             w_tiles = w4_uniform(d.tiles);
-            w_step = TN * (p.K / 2) - w_n * 64;
+            w_step = TN * (p.K / 2);
             w_cut = GS < 4 && t * 32 >= p.K - (w_n - 1) * 128;
+            w_base0 = w4_uniform(d.wq);
+            w_base1 = w_base0 + (SWIGLU ? (int64_t)p.N_out * (p.K / 2) : 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                wsrc[q] = d.wq + (int64_t)row_of(p, d, q) * (p.K / 2) + (j - w_end) * 64 + t * 16;
+            for (int q = 0; q < 4; ++q) {
+                const int row = SWIGLU ? q % 2 * 8 + g : min(q * 8 + g, p.N_out - 1 - d.n0);
+                woff[q] = row * (p.K / 2) + (j - w_end) * 64 + t * 16;
+            }
         }
         w_end += w_n;
     };
@@ -363,10 +376,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             w_open = true;
             if (GS == 4 || !(w_cut && j + 1 == w_end)) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) w4_cp16(w_slot + w_off + q * 512, wsrc[q]);
+                for (int q = 0; q < 4; ++q) w4_cp16(w_slot + w_off + q * 512, (q < 2 ? w_base0 : w_base1) + woff[q]);
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) wsrc[q] += 64;
+            for (int q = 0; q < 4; ++q) woff[q] += 64;
         }
         w4_cp_commit();
         w_off = (w_off + W4_STAGE) & (W4_RING * W4_STAGE - 1);
@@ -379,8 +392,9 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             if (t == 0)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    w4_prefetch_l2(wsrc[q]);
-                    if (w_end > 2) w4_prefetch_l2(wsrc[q] + 128);
+                    const uint8_t* p = (q < 2 ? w_base0 : w_base1) + woff[q];
+                    w4_prefetch_l2(p);
+                    if (w_end > 2) w4_prefetch_l2(p + 128);
                 }
         }
         pdl_wait();
@@ -507,9 +521,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
                     const uint32_t u[2] = {w[0][j], w[2][j]}, v[2] = {w[1][j], w[3][j]};
                     w4_step<C8, C>(sum, u, v, xb[step % AHEAD]);
                     if (step % GS == GS - 1) {
+                        const float mine = bf16_bits_to_float(sb[f]);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const float sc = bf16_bits_to_float(__shfl_sync(0xffffffffu, sb[f], (lane & 28) | q));
+                            const float sc = __shfl_sync(0xffffffffu, mine, (lane & 28) | q);
                             const int r = q >> 1, h = 2 * (q & 1);
 #pragma unroll
                             for (int c = 0; c < C8; ++c) {
