@@ -630,6 +630,11 @@ struct W4Problem {
     uint16_t* out_bf16 = nullptr;  // [., N_out]
     float* out_f32 = nullptr;      // or this
 };
+struct W4Div {  // a divisor and its multiplier, see w4_over
+    int d;
+    uint32_t m;
+    int shift;
+};
 struct W4Launch {
     const char* name;
     bool swiglu;
@@ -650,6 +655,8 @@ struct W4Launch {
     // only the A rows wait for it
     bool early = false;
     int32_t* status = nullptr;
+    // the grid, stages of a tile of either problem, k (filled in by launch_w4_gemm)
+    W4Div by_grid = {}, by_sh = {}, by_rt = {}, by_k = {};
 };
 cudaError_t launch_w4_gemm(const W4Launch& L, int num_sms, cudaStream_t s);
 struct W4CombineLaunch {

@@ -81,11 +81,18 @@ constexpr size_t w4_smem_bytes(int C) { return (size_t)W4_WARPS * (W4_RING * W4_
 struct W4Run {
     const uint8_t* wq;   // packed weights and scales of the first tile's first row
     const uint16_t* ws;
-    int64_t row0;        // first output row
+    int row0;            // first output row
     int n0, m;           // first output of the first tile, rows
     int tiles;
     bool routed;
 };
+
+// x / d for 0 <= x < 2^31 by the multiplier that the host made for d (w4_div: at most
+// 2^(31 + shift) / d + 1, exact for 31-bit x by Granlund and Montgomery's bound); the
+// divisions in front of a warp's first copy took a microsecond as such.
+__device__ __forceinline__ int w4_over(int x, const W4Div& d) {
+    return (int)(__umulhi(2 * (uint32_t)x, d.m) >> d.shift);
+}
 
 // a value that every lane of the warp has, said so
 __device__ __forceinline__ int w4_uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
@@ -168,7 +175,7 @@ __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int
         const int col = 8 * (c / 2) + 2 * t + c % 2;
         if (col >= d.m) continue;
         const float unit = xrow[col] < 0 ? 0.f : 64.f;
-        const int64_t at = (d.row0 + col) * N + n0 + g;
+        const int64_t at = (int64_t)(d.row0 + col) * N + n0 + g;
         float v[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
@@ -200,6 +207,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     constexpr int ROWS = 8 * C;  // activation rows of a tile
     extern __shared__ __align__(128) uint8_t w4_smem[];
     __shared__ int32_t s_pre[W4_MAXG];  // routed tiles before each slot
+    __shared__ int32_t s_off[W4_MAXG + 1];  // the slots' rows
     __shared__ int32_t s_part[W4_WARPS];
     __shared__ W4Run s_run[W4_WARPS][W4_RUNS + 1];            // in the last place, that of a tile
     __shared__ int32_t s_x[W4_WARPS][W4_RUNS + 1][ROWS];  // begun by an earlier warp; columns' activation rows
@@ -222,24 +230,27 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
 
     // the list: the dense problem's tiles, then the routed ones by slot; the row tiles of
     // one weight tile are neighbours
-    const int ct_sh = (int)((a.rows_sh + ROWS - 1) / ROWS);
+    const int rows_sh = (int)a.rows_sh, rows_cap = (int)a.rows_cap;
+    const int ct_sh = (rows_sh + ROWS - 1) / ROWS;
     const int n_sh = (a.sh.K + 127) / 128, n_rt = (a.rt.K + 127) / 128;  // stages of a tile
     const int tiles_rt = (a.rt.N_out + TN - 1) / TN;
-    const int64_t list_sh = a.sh.wq ? (int64_t)((a.sh.N_out + TN - 1) / TN) * ct_sh : 0;
-    int64_t list_rt = 0;
+    const int list_sh = a.sh.wq ? (a.sh.N_out + TN - 1) / TN * ct_sh : 0;
+    int list_rt = 0;
     if (a.G > 0) {
         constexpr int PER = W4_MAXG / W4_THREADS;
         const int s0 = threadIdx.x * PER;
         int n[PER], sum = 0;
-        int64_t lo = s0 <= a.G ? __ldg(a.offsets + s0) : 0;
+        int lo = s0 <= a.G ? __ldg(a.offsets + s0) : 0;
+        if (s0 <= a.G) s_off[s0] = lo;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             n[i] = 0;
             if (s0 + i < a.G) {
-                const int64_t hi = __ldg(a.offsets + s0 + i + 1);
-                const int64_t m = max((int64_t)0, min(hi, a.rows_cap) - max(lo, (int64_t)0));
-                n[i] = (int)((m + ROWS - 1) / ROWS) * tiles_rt;
+                const int hi = __ldg(a.offsets + s0 + i + 1);
+                const int m = max(0, min(hi, rows_cap) - max(lo, 0));
+                n[i] = (int)((uint32_t)(m + ROWS - 1) / ROWS) * tiles_rt;
                 lo = hi;
+                if (i + 1 < PER || s0 + PER == a.G) s_off[s0 + i + 1] = hi;
             }
             sum += n[i];
         }
@@ -266,22 +277,19 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         __syncthreads();
     }
     // this CTA's tiles: from the first that starts at or after its share of the stages
-    const int64_t stages_sh = list_sh * n_sh, stages = stages_sh + list_rt * n_rt;
-    const bool small = stages * gridDim.x < (int64_t(1) << 31);  // divisions in 32 bits, a fifth of the 64-bit ones
-    auto over = [small](int64_t x, int y) {
-        return small ? (int64_t)((uint32_t)x / (uint32_t)y) : x / (int64_t)y;
+    const int stages_sh = list_sh * n_sh, stages = stages_sh + list_rt * n_rt;
+    const int share = w4_over(stages, a.by_grid), more = stages - share * (int)gridDim.x;  // (`more` CTAs: one more)
+    auto first_tile = [&](int cta) {
+        const int s = share * cta + min(cta, more);
+        return s <= stages_sh ? w4_over(s + n_sh - 1, a.by_sh) : list_sh + w4_over(s - stages_sh + n_rt - 1, a.by_rt);
     };
-    auto first_tile = [&](int64_t cta) {
-        const int64_t s = over(stages * cta, (int)gridDim.x);
-        return s <= stages_sh ? (n_sh ? over(s + n_sh - 1, n_sh) : 0) : list_sh + over(s - stages_sh + n_rt - 1, n_rt);
-    };
-    auto start_of = [&](int64_t v) { return v <= list_sh ? v * n_sh : stages_sh + (v - list_sh) * n_rt; };
-    const int64_t base = start_of(first_tile(blockIdx.x));
-    const int64_t all = start_of(first_tile(blockIdx.x + 1)) - base;
+    auto start_of = [&](int v) { return v <= list_sh ? v * n_sh : stages_sh + (v - list_sh) * n_rt; };
+    const int base = start_of(first_tile(blockIdx.x));
+    const int all = start_of(first_tile(blockIdx.x + 1)) - base;
     // this warp's stages: cnt from lo; the first one's tile
-    const int64_t lo = base + all * warp / W4_WARPS;
-    const int cnt = (int)(base + all * (warp + 1) / W4_WARPS - lo);
-    const int64_t v0 = lo < stages_sh ? over(lo, n_sh) : list_sh + (n_rt ? over(lo - stages_sh, n_rt) : 0);
+    const int lo = base + all * warp / W4_WARPS;
+    const int cnt = base + all * (warp + 1) / W4_WARPS - lo;
+    const int v0 = lo < stages_sh ? w4_over(lo, a.by_sh) : list_sh + w4_over(lo - stages_sh, a.by_rt);
 
     // Three cursors run over the stages: the copies three ahead, the activations and
     // scales one ahead, the products.  Each steps from tile to tile of a run by constants
@@ -289,46 +297,48 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     // numbers count from lo.  (The loop is not unrolled over the ring: four copies of what
     // a tile's end takes overran the instruction cache, 3 of 8 stalled cycles.)
     W4Run* runs = s_run[warp];
-    const int first = (int)(start_of(v0) - lo);  // where the first tile starts (<= 0)
-    int64_t next_v = v0;                         // the first tile past the runs so far
+    const int first = start_of(v0) - lo;  // where the first tile starts (<= 0)
+    int next_v = v0;                      // the first tile past the runs so far
+    int32_t xrow = 0;                     // the activation row (FC1: pair) of the run's column `lane`
     auto locate = [&](int i) {
         W4Run d;
-        int64_t rows, at;  // the slot's end, its first weight row
-        int q, ct;         // tile of the slot, its row tiles
+        int64_t at = 0;  // the slot's first weight row
+        int rows;        // its end
+        int q, ct;       // tile of the slot, its row tiles
         if (next_v < list_sh) {
-            q = (int)next_v;
+            q = next_v;
             d.routed = false;
             ct = ct_sh;
             d.row0 = 0;
-            rows = a.rows_sh;
-            at = 0;
+            rows = rows_sh;
         } else {
-            const int w = (int)(next_v - list_sh);
-            int s_lo = 0, s_hi = a.G - 1;  // the last slot whose tiles begin at or before w
-            while (s_lo < s_hi) {
-                const int mid = (s_lo + s_hi + 1) / 2;
-                if (s_pre[mid] <= w)
-                    s_lo = mid;
-                else
-                    s_hi = mid - 1;
-            }
+            const int w = next_v - list_sh;
+            // the last slot whose tiles begin at or before w: its 32, then itself
+            int s_lo = 32 * lane;
+            s_lo = 32 * (__popc(__ballot_sync(0xffffffffu, s_lo < a.G && s_pre[s_lo] <= w)) - 1);
+            const int s_at = s_lo + lane;
+            s_lo += __popc(__ballot_sync(0xffffffffu, s_at < a.G && s_pre[s_at] <= w)) - 1;
             d.routed = true;
-            d.row0 = max(0, __ldg(a.offsets + s_lo));
-            rows = min((int64_t)__ldg(a.offsets + s_lo + 1), a.rows_cap);
-            ct = (int)((rows - d.row0 + ROWS - 1) / ROWS);
+            d.row0 = max(0, s_off[s_lo]);
+            rows = min(s_off[s_lo + 1], rows_cap);
+            ct = (int)((uint32_t)(rows - d.row0 + ROWS - 1) / ROWS);
             q = w - s_pre[s_lo];
             at = s_lo * (SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out);
         }
         const W4Problem& p = d.routed ? a.rt : a.sh;
-        const int tile = q / ct;
+        const int tile = ct == 1 ? q : q / ct;
         d.n0 = tile * TN;
-        d.row0 += (int64_t)(q - tile * ct) * ROWS;
-        d.m = (int)min((int64_t)ROWS, rows - d.row0);
+        d.row0 += (q - tile * ct) * ROWS;
+        d.m = min(ROWS, rows - d.row0);
         d.wq = p.wq + (at + d.n0) * (p.K / 2);
         d.ws = p.ws + (at + d.n0) * (p.K / (32 * GS));
         // a last tile with fewer outputs stands alone: some of its rows repeat
         d.tiles = ct == 1 ? max(1, p.N_out / TN - tile) : 1;
         next_v += d.tiles;
+        if (lane < ROWS) {  // (kept when the first copies are on their way)
+            xrow = d.row0 + min(lane, d.m - 1);
+            if (d.routed && a.perm_src) xrow = a.perm_src[xrow];
+        }
         __syncwarp();
         if (lane == 0) runs[i % W4_RUNS] = d;
         __syncwarp();
@@ -367,11 +377,23 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         }
         w_end += w_n;
     };
+    auto keep_rows = [&] {
+        if (lane < ROWS) {
+            int32_t r = xrow;
+            if (runs[w_run % W4_RUNS].routed && a.perm_src) {  // FC1 reads the routing table for the rows
+                const bool ok = r >= 0 && r < (int)(a.T * a.k);
+                if (!ok) report(a.status, MOE_ERR_DEVICE_BOUNDS);
+                r = ok ? w4_over(r, a.by_k) : -1;
+            }
+            s_x[warp][w_run % W4_RUNS][lane] = r;
+        }
+    };
     uint32_t w_off = 0, r_off = 0;  // ring stages written and read next
     const uint32_t w_slot = ring0 + g * 64 + ((t ^ sw) << 4), r_slot = ring0 + g * 64;
     bool w_open = false;  // the first tile's addresses stand
     auto issue = [&](int j) {
         if (j < cnt) {
+            const int r = w_run;
             if (j == w_end || !w_open) next_w(j);
             w_open = true;
             if (GS == 4 || !(w_cut && j + 1 == w_end)) {
@@ -380,6 +402,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) woff[q] += 64;
+            if (r != w_run || j == 0) keep_rows();
         }
         w4_cp_commit();
         w_off = (w_off + W4_STAGE) & (W4_RING * W4_STAGE - 1);
@@ -420,16 +443,6 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         } else {
             const W4Run& d = runs[++p_run % W4_RUNS];
             const W4Problem& p = d.routed ? a.rt : a.sh;
-            if (lane < ROWS) {  // FC1 reads the routing table for the rows
-                int32_t r = (int32_t)(d.row0 + min(lane, d.m - 1));
-                if (d.routed && a.perm_src) {
-                    const int32_t q = a.perm_src[r];
-                    const bool ok = q >= 0 && (int64_t)q < a.T * a.k;
-                    if (!ok) report(a.status, MOE_ERR_DEVICE_BOUNDS);
-                    r = ok ? q / a.k : -1;
-                }
-                s_x[warp][p_run % W4_RUNS][lane] = r;
-            }
             __syncwarp();
             p_n = w4_uniform(d.routed) ? n_rt : n_sh;
             p_tiles = w4_uniform(d.tiles);
@@ -596,8 +609,8 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
 
     // the parts of the tile that this warp ended, in stage order
     if (ended) {
-        const int64_t start = lo + first - base;                            // of the tile among the CTA's stages
-        const int w0 = (int)((W4_WARPS * (start + 1) - 1) / all);           // the warp that began it
+        const int start = lo + first - base;                     // of the tile among the CTA's stages
+        const int w0 = (W4_WARPS * (start + 1) - 1) / all;       // the warp that began it
         for (int w = w0; w <= warp; ++w) {
             if (all * w / W4_WARPS == all * (w + 1) / W4_WARPS) continue;  // a warp without stages
             const float4* o = parts + (w * 2 + (w == w0 ? 1 : 0)) * (64 * C) + lane;
@@ -698,6 +711,14 @@ cudaError_t launch_quantize_w4_rows(const uint16_t* w, int64_t rows, int K, int 
                     group / 8, reinterpret_cast<uint32_t*>(q), scale);
 }
 
+static W4Div w4_div(int d) {
+    W4Div r = {d, 0, 0};
+    if (d <= 0) return r;
+    while ((int64_t(1) << r.shift) < d) ++r.shift;
+    r.m = (uint32_t)((uint64_t(1) << (31 + r.shift)) / (uint64_t)d + 1);
+    return r;
+}
+
 template <bool SWIGLU, int GS, int C>
 static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t s) {
     // the shared-memory limit is set once per device
@@ -720,7 +741,12 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     const double even = (sh * n_sh + rt * n_rt) / std::max(sh > 0 ? n_sh : 1, rt > 0 ? n_rt : 1);
     const double most = std::min(sh + rt, (double)W4_CTAS * num_sms);
     const unsigned grid = (unsigned)std::max(1.0, std::min(most, std::max(even, (double)num_sms)));
-    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), w4_smem_bytes(C), s, L);
+    W4Launch K = L;
+    K.by_grid = w4_div((int)grid);
+    K.by_sh = w4_div(n_sh);
+    K.by_rt = w4_div(n_rt);
+    K.by_k = w4_div(L.k);
+    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), w4_smem_bytes(C), s, K);
 }
 
 template <bool SWIGLU, int GS>
