@@ -436,9 +436,10 @@ MOE_API moe_status_t moe_forward_w8a8_rows(const uint8_t *xq, const float *x_sca
  * residual_out may be residual and y may be x (in place); no other overlap.  At
  * least one output is given.  H: a multiple of 8, at most 16384
  * (MOE_ERR_UNSUPPORTED otherwise).  Every pointer 16-byte aligned, q 8-byte, scale
- * 4-byte.  A row of zeros gives y = 0, q = 0, scale 2^-126; a row holding an
- * infinity or a NaN gives what these formulas give in binary32 (E4M3 NaN codes for
- * NaN values).  No workspace; asynchronous on `stream`; one launch. */
+ * 4-byte.  With eps > 0 a row of zeros gives y = 0, q = 0, scale 2^-126.  A row
+ * holding an infinity or a NaN, one whose sum of squares passes binary32 (values
+ * about 10^19 and more: y = 0), and zeros with eps = 0 (NaN) give what these formulas
+ * give in binary32 (E4M3 NaN codes for NaN values).  No workspace; asynchronous on `stream`; one launch. */
 MOE_API moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const void *residual, int residual_f32,
                                    const moe_bf16_t *weight, float eps, int64_t T, int H, void *residual_out,
                                    moe_bf16_t *y, uint8_t *q, float *scale, moe_stream_t stream);
@@ -459,7 +460,8 @@ MOE_API moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const void *residual, 
 /* Quantise a bf16 matrix w [rows, K]: per group scale = bf16(amax / 7) and
  * c = w / scale rounded to the nearest integer (ties to even) and clamped to
  * -8 .. 7, both divisions in IEEE binary32; a group of zeros gets scale 0 and
- * c = 0.  w must be 16-byte, q 4-byte and scale 2-byte aligned.  group other than
+ * c = 0.  Weights are finite: the codes of a group with a NaN or an infinity mean
+ * nothing.  w must be 16-byte, q 4-byte and scale 2-byte aligned.  group other than
  * 32, 64, 128 or K not a multiple of it -> MOE_ERR_UNSUPPORTED.  Asynchronous on
  * `stream`; allocates nothing. */
 MOE_API moe_status_t moe_quantize_w4_rows(const moe_bf16_t *w, int64_t rows, int K, int group, uint8_t *q,
@@ -467,9 +469,12 @@ MOE_API moe_status_t moe_quantize_w4_rows(const moe_bf16_t *w, int64_t rows, int
 
 /* moe_matvec_w4 -- y [M, N] bf16 = x [M, K] bf16 times W^T, W [N, K] in the format
  * above: products with a few rows (made for M up to 16; beyond, the weights are
- * read again, from L2 where they are still there, for every 16 rows).  Sums in
- * fp32, one rounding at the end; for M up to 16 a row's result does not depend on M.  x and q
- * 16-byte, scale and y 2-byte aligned; M, N < 2^31.  No workspace. */
+ * read again, from L2 where they are still there, for every 8 or 16 rows).  Sums in
+ * fp32, one rounding at the end; for M up to 16 a row's result does not depend on M.
+ * A NaN or an infinity in a row of x stays in that row of y.  x and q 16-byte, scale
+ * and y 2-byte aligned, y apart from the inputs.  M < 2^31, K <= 2^20 and
+ * ceil(M/8) ceil(N/32) ceil(K/128) < 2^31 - 2^20, else MOE_ERR_UNSUPPORTED.  No
+ * workspace; asynchronous on `stream`. */
 MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const moe_bf16_t *scale, int64_t M, int N,
                                    int K, int group, moe_bf16_t *y, moe_stream_t stream);
 
@@ -490,7 +495,9 @@ MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const 
  * H, I and I_shared_total multiples of 64 and of group.  Entries of perm_src
  * outside [0, T*k) and of pair_row outside [-1, P_cap) are dropped and flagged.
  * Meant for decode batches (up to about 16 rows per slot); larger batches are
- * right, but a slot's weights are read again, from L2, for every 16 rows.  The other
+ * right, but a slot's weights are read again, from L2, for every 8 or 16 rows.
+ * MOE_ERR_UNSUPPORTED where (ceil(P_cap/8) + S_local - 1) ceil(I/16) ceil(H/128), or
+ * the shared experts' part with T and I_shared_total, passes 2^31 - 2^20.  The other
  * arguments and errors as moe_forward. */
 MOE_API moe_status_t moe_forward_w4(const moe_bf16_t *x, const int32_t *offsets, int S_local, int64_t P_cap,
                                    const int32_t *perm_src, const uint8_t *W1q, const moe_bf16_t *W1_scale,

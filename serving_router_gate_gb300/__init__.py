@@ -461,7 +461,7 @@ def moe_forward_nvfp4(x_perm, offsets, W1q, W1sf, s1, W2q, W2sf, s2, pair_row, t
 def moe_quantize_fp8_rows(w, q, scale, stream=None):
     """Row-wise E4M3 quantisation of a bf16 tensor [..., K] into q (uint8, same shape) and scale ([...] fp32)."""
     K = w.shape[-1]
-    rows = w.numel() // K
+    rows = w.numel() // max(1, K)
     st = _lib.moe_quantize_fp8_rows(_ptr(w, "w", _bf16), rows, K, _ptr(q, "q", torch.uint8, tuple(w.shape)),
                                     _ptr(scale, "scale", _f32, tuple(w.shape[:-1])), _stream(stream))
     _check("moe_quantize_fp8_rows", st)
@@ -555,7 +555,7 @@ def moe_quantize_w4_rows(w, q, scale, stream=None):
     """4-bit quantisation of a bf16 tensor [..., K] with one bf16 scale per group: q [..., K/2] uint8, scale
     [..., K/group] bf16; the group (32, 64 or 128) is read off scale's shape."""
     K = w.shape[-1]
-    rows = w.numel() // K
+    rows = w.numel() // max(1, K)
     lead = tuple(w.shape[:-1])
     group = max(1, K // max(1, scale.shape[-1]))
     st = _lib.moe_quantize_w4_rows(_ptr(w, "w", _bf16), rows, K, group,

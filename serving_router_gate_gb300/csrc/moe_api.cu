@@ -763,7 +763,7 @@ namespace {
 constexpr int64_t kW4MaxStages = (int64_t(1) << 31) - (1 << 20);
 int64_t w4_stages(int64_t rows, int64_t slots, int64_t N, int64_t K) {
     const __int128 n = (__int128)((rows + 7) / 8 + slots - 1) * ((N + 31) / 32) * ((K + 127) / 128);
-    return n > kW4MaxStages ? kW4MaxStages + 1 : (int64_t)n;
+    return n > kW4MaxStages ? kW4MaxStages : (int64_t)n;
 }
 }  // namespace
 
@@ -772,7 +772,7 @@ moe_status_t moe_matvec_w4(const moe_bf16_t* x, const uint8_t* q, const moe_bf16
     MOE_NVTX("moe_matvec_w4");
     if (M < 0 || N <= 0 || K <= 0 || group <= 0) return MOE_ERR_INVALID_ARG;
     if (!w4_group_ok(K, group) || K > (1 << 20) || M >= (int64_t(1) << 31) ||
-        w4_stages(M, 1, N, K) > kW4MaxStages)
+        w4_stages(M, 1, N, K) >= kW4MaxStages)
         return MOE_ERR_UNSUPPORTED;
     if (M == 0) return MOE_OK;
     if (!x || !q || !scale || !y || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 2) || !aligned(y, 2))
@@ -831,8 +831,8 @@ moe_status_t moe_forward_w4(const moe_bf16_t* x, const int32_t* offsets, int S_l
         return MOE_ERR_UNSUPPORTED;
     // (FC1's gate and up rows are 2 I weight rows)
     const int64_t I_sh = I_shared_total;
-    if (w4_stages(P_cap, S_local, 2 * (int64_t)I, H) + w4_stages(T, 1, 2 * I_sh, H) > kW4MaxStages ||
-        w4_stages(P_cap, S_local, H, I) + w4_stages(T, 1, H, I_sh) > kW4MaxStages)
+    if (w4_stages(P_cap, S_local, 2 * (int64_t)I, H) + w4_stages(T, 1, 2 * I_sh, H) >= kW4MaxStages ||
+        w4_stages(P_cap, S_local, H, I) + w4_stages(T, 1, H, I_sh) >= kW4MaxStages)
         return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !offsets || !perm_src || !W1q || !W1_scale || !W2q || !W2_scale || !pair_row || !out)

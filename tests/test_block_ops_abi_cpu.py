@@ -44,6 +44,15 @@ def test_matvec_refusals(kw, want):
     assert _matvec(**kw) == want
 
 
+def test_matvec_work_that_its_kernel_could_not_count():
+    # ceil(M / 8) ceil(N / 32) ceil(K / 128) pieces of work, below 2^31 - 2^20
+    assert _matvec(M=1 << 30, N=1 << 30, K=1 << 20, group=128) == UNSUPPORTED
+    assert _matvec(M=8 * 2048, N=32 * 1024, K=128 * 1024) == UNSUPPORTED      # 2^31
+    assert _matvec(M=8 * 2047, N=32 * 1024, K=128 * 1024) == UNSUPPORTED      # 2^31 - 2^20
+    assert _matvec(M=8 * 2047, N=32 * 1024, K=128 * 1024, y=None) == UNSUPPORTED
+    assert _matvec(M=8 * 2046, N=32 * 1024, K=128 * 1024, y=None) == INVALID  # counted; refused for y
+
+
 def _quant(w=FAKE, rows=2, K=256, group=64, q=FAKE, s=FAKE):
     return moe._lib.moe_quantize_w4_rows(w, rows, K, group, q, s, None)
 
@@ -76,6 +85,13 @@ def _forward(x=FAKE, off=FAKE, S=8, P=8, src=FAKE, w1=FAKE, s1=FAKE, w2=FAKE, s2
     (dict(ws=None), WORKSPACE), (dict(wsb=300), WORKSPACE), (dict(T=0, x=None, off=None), OK)])
 def test_forward_w4_refusals(kw, want):
     assert _forward(**kw) == want
+
+
+def test_forward_w4_work_that_its_kernels_could_not_count():
+    big = dict(H=16384, I=8192, group=128)
+    assert _forward(T=1 << 20, k=1, P=1 << 20, **big) == UNSUPPORTED
+    assert _forward(T=1 << 20, k=1, P=8, I_sh=16384, sh=(FAKE,) * 4, **big) == UNSUPPORTED
+    assert _forward(T=1 << 10, k=1, P=1 << 10, wsb=300, **big) == WORKSPACE   # counted; the workspace is too small
 
 
 def test_forward_w4_workspace():

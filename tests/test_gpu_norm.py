@@ -141,6 +141,30 @@ def test_norm_rows_do_not_depend_on_the_batch():
             assert torch.equal(a[0], b[t])
 
 
+def test_norm_rows_past_2_31_elements():
+    T, H = 140001, 16384
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(9))
+    r = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(10))
+    w = _inputs(1, H, False)[2].cuda()
+    rows = torch.tensor([0, 1, 65535, 65536, 131071, 131072, 131073, T - 2, T - 1])
+    xs, rs = x[rows].cpu(), r[rows].cpu()
+    q, sc = torch.empty(T, H, dtype=torch.uint8, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_add_rmsnorm(x, r, w, EPS, r, x, q, sc)
+    _check(xs, rs, w.cpu(), [t[rows].cpu() for t in (r, x, q, sc)])
+
+
+def test_norm_binding_refuses_what_it_would_misread():
+    x, r, w = (t.cuda() for t in _inputs(4, 64, False))
+    y, q, sc = torch.empty_like(x), torch.empty(4, 64, dtype=torch.uint8, device="cuda"), torch.empty(4, device="cuda")
+    good = dict(x=x, r=r, w=w, ro=r, y=y, q=q, sc=sc)
+    for bad in (dict(x=x.t().contiguous().t()), dict(x=x.float()), dict(r=r.half()), dict(r=r[:3]), dict(w=w[:32]),
+                dict(w=w.float()), dict(ro=r.float()), dict(y=y.t().contiguous().t()), dict(q=q.view(torch.int8)),
+                dict(sc=sc[:3])):
+        a = {**good, **bad}
+        with pytest.raises(ValueError):
+            moe.moe_add_rmsnorm(a["x"], a["r"], a["w"], EPS, a["ro"], a["y"], a["q"], a["sc"])
+
+
 def test_norm_empty_batch():
     x = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")

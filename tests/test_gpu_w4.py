@@ -170,6 +170,68 @@ def test_matvec_empty_batch():
     assert moe.moe_get_launch_count() == n
 
 
+def test_matvec_codes_past_4_gib():
+    # 530001 rows of 8 KiB: the last ones lie past 2^32 bytes and 2^33 codes
+    N, K = 530001, 16384
+    q, s = torch.empty(N, K // 2, dtype=torch.uint8, device="cuda"), torch.empty(N, K // 128, device="cuda")
+    q.random_(0, 256, generator=_gen(11))
+    s = s.uniform_(-0.01, 0.01, generator=_gen(12)).to(torch.bfloat16)
+    x = torch.randn(2, K, generator=_gen(13), device="cuda").to(torch.bfloat16)
+    y = torch.full((2, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    moe.moe_matvec_w4(x, q, s, y)
+    rows = torch.tensor([0, 1, 31, 32, 262143, 262144, 262145, 524287, 524288, 524289, N - 33, N - 2, N - 1], device="cuda")
+    _check_matvec(x, q[rows], s[rows], y[:, rows])
+    assert torch.isfinite(y.float()).all()
+
+
+def test_matvec_on_another_stream_and_in_a_graph():
+    x, q, s, want = _matvec(3, 200, 512, 64, seed=14)
+    y, stream = torch.empty_like(want), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    moe.moe_matvec_w4(x, q, s, y, stream=stream)
+    stream.synchronize()
+    assert torch.equal(y, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_matvec_w4(x, q, s, y)
+        moe.moe_matvec_w4(x, q, s, y)
+    y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_matvec_of_weights_written_just_before():
+    # the product's kernel may start while the quantiser finishes; it reads nothing of the weights before that
+    g = _gen(15)
+    x = torch.randn(4, 4096, generator=g, device="cuda").to(torch.bfloat16)
+    q, s = torch.zeros(4096, 2048, dtype=torch.uint8, device="cuda"), torch.zeros(4096, 32, device="cuda").to(torch.bfloat16)
+    y = torch.empty(4, 4096, dtype=torch.bfloat16, device="cuda")
+    for i in range(5):
+        w = torch.randn(4096, 4096, generator=g, device="cuda").to(torch.bfloat16)
+        torch.cuda.synchronize()
+        moe.moe_quantize_w4_rows(w, q, s)
+        moe.moe_matvec_w4(x, q, s, y)
+        _check_matvec(x, q, s, y)
+
+
+def test_binding_refuses_what_it_would_misread():
+    x, q, s, y = _matvec(4, 64, 256, 64, seed=16)
+    for bad in (dict(x=x.t().contiguous().t()), dict(x=x.float()), dict(q=q[:, ::2]), dict(q=q.view(torch.int8)),
+                dict(s=s[:-1]), dict(s=s.float()), dict(y=y.t().contiguous().t()), dict(y=y[:3]), dict(y=y.float())):
+        a = {**dict(x=x, q=q, s=s, y=y), **bad}
+        with pytest.raises(ValueError):
+            moe.moe_matvec_w4(a["x"], a["q"], a["s"], a["y"])
+    with pytest.raises(ValueError):
+        moe.moe_quantize_w4_rows(torch.empty(8, 128, device="cuda"), q, s)
+    with pytest.raises(moe.MoEError):
+        moe.moe_matvec_w4(x.reshape(-1)[1:1 + 2 * 256].view(2, 256), q, s, y[:2])  # not 16-byte aligned
+    with pytest.raises(moe.MoEError):
+        moe.moe_quantize_w4_rows(torch.empty(8, 0, dtype=torch.bfloat16, device="cuda"),
+                                 torch.empty(8, 0, dtype=torch.uint8, device="cuda"),
+                                 torch.empty(8, 0, dtype=torch.bfloat16, device="cuda"))
+
+
 # ---------------------------------------------------------------------------------------------- experts
 
 def _tables(T, E, k, S, seed, hot=None):
@@ -328,3 +390,18 @@ def test_layer_with_4bit_experts_and_its_graph():
         MoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, cfg.renorm, 16, w4=64, fp8=True)
     with pytest.raises(ValueError):
         MoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, cfg.renorm, 16, w4=64, on_input=True)
+
+
+def test_layer_with_4bit_experts_on_another_stream():
+    cfg = mi.MoEConfig("w4", T=5, H=256, I=128, E=8, k=2, renorm=True, n_shared=1, I_shared=128, shared_gate=True)
+    inp = mi.make_inputs(cfg)
+    d = {n: (v.cuda() if isinstance(v, torch.Tensor) else v) for n, v in inp.items()}
+    W1s, W2s = mi.shared_concat(d["W1s"], d["W2s"])
+    layer = MoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, cfg.renorm, 8, W1s=W1s, W2s=W2s, shared_gate_w=d["w_s"], w4=32)
+    want = layer.forward(d["x"]).clone()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for _ in range(20):  # calls in a row share the workspace
+        layer.forward(d["x"], stream=stream)
+    stream.synchronize()
+    assert torch.equal(layer.out[:5], want)
