@@ -61,6 +61,28 @@ def test_quantise_w4_rows(group, rows, K):
     assert (err <= 0.51 * s.double().abs().unsqueeze(-1)).all()
 
 
+@pytest.mark.parametrize("group", [32, 128])
+def test_quantise_every_quotient(group):
+    # every pair of eight-bit significands, f / s from 1/8 to 8, ties among them; scales from subnormal to the largest
+    m = torch.arange(128, 256, device="cuda", dtype=torch.float64)
+    for e in (-133, -130, -126, -100, -64, -63, -1, 0, 60, 117):
+        amax = m * 2.0 ** e                                          # a group's largest element, 128 of them
+        f = (m.repeat_interleave(2) * torch.tensor([1.0, -1.0], device="cuda").repeat(128)).repeat(128, 1)
+        f = f[:, None, :] * 2.0 ** (e - torch.arange(0, 6, device="cuda", dtype=torch.float64))[:, None]
+        f = torch.where(f.abs() <= amax[:, None, None], f, f / 2).reshape(128, -1, group)
+        f[:, :, 0] = amax[:, None]
+        w = f.to(torch.bfloat16).reshape(128, -1)
+        q = torch.empty(128, w.shape[1] // 2, dtype=torch.uint8, device="cuda")
+        s = torch.empty(128, w.shape[1] // group, dtype=torch.bfloat16, device="cuda")
+        moe.moe_quantize_w4_rows(w, q, s)
+        wf = w.float().reshape(128, -1, group)
+        ref_s = (wf.abs().amax(-1) / torch.full((), 7.0, device="cuda")).to(torch.bfloat16)
+        assert torch.equal(s, ref_s)
+        ratio = wf.double() / ref_s.double().unsqueeze(-1)           # (a tie is exact in 64 bits, the rest far from one)
+        codes = torch.where(ref_s.unsqueeze(-1) == 0, torch.zeros_like(ratio), torch.round(ratio).clamp(-8, 7))
+        assert torch.equal(q, pack_w4(codes.reshape(128, -1)))
+
+
 def _check_matvec(x, q, s, y):
     c, sc = unpack_w4(q, s)
     ref = x.double() @ (c * sc).t()
