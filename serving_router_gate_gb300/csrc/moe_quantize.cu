@@ -324,7 +324,9 @@ cudaError_t launch_quantize_act_rows(const ActQuantSeg* seg, int nseg, int num_s
 namespace {
 
 // Rows that are E4M3 already, copied to their pairs' rows (each read once): one warp
-// per token row at a time, 16-byte pieces.
+// per token row at a time, 16-byte pieces.  No arithmetic: what is bound is the (k + 1)
+// T H bytes and, for a decode batch, the launch.  The copy stands where
+// quantize_act_rows_kernel would read twice the bytes to make the same codes.
 __global__ void __launch_bounds__(QZ_WARPS * 32) place_rows_kernel(const __grid_constant__ PlaceRowsLaunch a) {
     pdl_wait();
     pdl_trigger();

@@ -79,14 +79,40 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 }
 
 // ---------------------------------------------------------------------------
-// Products on mma.sync.  The work is a list of tiles, 32 weight rows of one slot
-// (FC1: 16 gate rows and the matching 16 up rows) times up to 8 C activation rows; a
-// tile's K is cut into stages of 128.  Every CTA takes a contiguous range of the list,
-// about the same number of stages each, and its 8 warps take equal contiguous ranges
-// of those stages, whatever tiles they fall into.  A warp streams its stages through
-// a ring of its own without a break at a tile's end; it stores the tiles that are all
-// its own, and leaves its part of the at most two that it shares with its neighbours
-// in shared memory, where the warp that ends a tile adds the parts in stage order.
+// Products.  For one group of a weight row n and an activation row m
+//
+//   y[m][n] += s * sum_k c[n][k] x[m][k]
+//
+// the inner sum is an mma.sync chain in fp32 over the codes widened to bf16 (c / 64, exact)
+// and the bf16 activations as they are (every product exact), the outer one an fp32 fused
+// multiply-add per group; y is rounded once.
+//
+// The work is a list of tiles, 32 weight rows of one slot (FC1: 16 gate rows and the
+// matching 16 up rows) times up to 8 C activation rows; a tile's K is cut into stages of
+// 128.  Every CTA takes a contiguous range of the list, about the same number of stages
+// each, and its 8 warps take equal contiguous ranges of those stages, whatever tiles they
+// fall into.  A warp streams its stages through a ring of its own without a break at a
+// tile's end; it stores the tiles that are all its own, and leaves its part of the at most
+// two that it shares with its neighbours in shared memory, where the warp that ends a tile
+// adds the parts in stage order (no atomics: the order is fixed by the sizes).
+//
+// Bound: HBM for the weights when they are many, else instruction issue.  A stage (2 KB of
+// codes) takes a warp 262 instructions, 144 of them to widen (nine per word of eight codes),
+// so the SMs together could take in 9 TB/s; at 16 warps an SM they issue in 0.6 of all
+// cycles (the rest: the ALU's and the tensor pipe's turns, and latency).  tcgen05 would
+// want the widened codes stored to shared memory and at least 128 rows a tile; registers
+// feed mma.sync as they are, and a tile of 32 rows splits evenly at one row of activations.
+// What else was measured for 65536 x 7168 by one row when it took 48 us: 24 warps an SM on
+// 80 registers 59 us, 16 warps in one CTA no faster, the ring's loop unrolled by four
+// slower (the instruction cache), codes as E4M3 pieces 70 us (emulated on this part), codes
+// left as subnormals with activations scaled by a kernel in front 50 us.
+//
+// Measured (weights not in L2): 65536 x 7168, groups of 128, one row 43.3 .. 45.3 us (two
+// boxes), 242 MB at 5.6 .. 5.3 TB/s; eight rows 49 us, sixteen 76 us.  Eight tokens, 8 of 256
+// experts of 7168 x 2048: 218 .. 234 us for FC1, FC2 and the combine, 1.30 GB at 6.0 .. 5.6
+// TB/s.  32 tokens, 6 of 64 experts of 2048 x 1408 and a shared one of 5632: 68 us (291 MB,
+// 4.3 TB/s); one token of it 19.3 us (45 MB): three kernels of about 6, 6 and 1.3 us
+// behind prologues of 3 us and 1.5 us from each one's end to the next one's start.
 // ---------------------------------------------------------------------------
 constexpr int W4_WARPS = 8;
 constexpr int W4_THREADS = W4_WARPS * 32;
@@ -655,7 +681,14 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------
-// Combine: out[t] = bf16( sum_j w[t][j] y[row] + g_t shared[t] ), fixed j order
+// Combine: out[t] = bf16( sum_j w[t][j] y[row] + g_t shared[t] ), fixed j order,
+// g_t = 1 / (1 + exp(-x[t] gate_w)) or 1.
+//
+// Bound: latency.  k + 1 fp32 rows are read per token, from L2 where FC2 has just left
+// them; the tables and the gate are read and summed before FC2 is waited for.  From FC2's
+// end to its own 2.8 us at one token, 3.2 us at 32 (H = 2048, k = 6: 1.8 MB), of which 1.5 us
+// is the kernels' handover.  y is fp32: rounding it to bf16 here would add an error of the
+// size of the output's own rounding for every expert.
 // ---------------------------------------------------------------------------
 constexpr int W4C_THREADS = 256;
 constexpr int W4C_MAXK = 32;
