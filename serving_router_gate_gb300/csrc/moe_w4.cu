@@ -404,23 +404,21 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     auto next_w = [&](int j) {  // the copies' next tile
         if (--w_tiles > 0) {
             w_base0 += w_step;
-            w_base1 += w_step;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) woff[q] -= w_n * 64;
+            if (SWIGLU) w_base1 += w_step;
         } else {
             locate(++w_run);
             const W4Run& d = runs[w_run % W4_RUNS];
             const W4Problem& p = d.routed ? a.rt : a.sh;
             w_n = w4_uniform(d.routed) ? n_rt : n_sh;
             w_tiles = w4_uniform(d.tiles);
-            w_step = TN * (p.K / 2);
+            w_step = TN * (p.K / 2) - w_n * 64;
             w_cut = GS < 4 && t * 32 >= p.K - (w_n - 1) * 128;
-            w_base0 = w4_uniform(d.wq);
+            w_base0 = w4_uniform(d.wq) + (j - w_end) * 64;
             w_base1 = w_base0 + (SWIGLU ? (int64_t)p.N_out * (p.K / 2) : 0);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int row = SWIGLU ? q % 2 * 8 + g : min(q * 8 + g, p.N_out - 1 - d.n0);
-                woff[q] = row * (p.K / 2) + (j - w_end) * 64 + t * 16;
+                woff[q] = row * (p.K / 2) + t * 16;
             }
         }
         w_end += w_n;
@@ -446,10 +444,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             w_open = true;
             if (GS == 4 || !(w_cut && j + 1 == w_end)) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) w4_cp16(w_slot + w_off + q * 512, (q < 2 ? w_base0 : w_base1) + woff[q]);
+                for (int q = 0; q < 4; ++q) w4_cp16(w_slot + w_off + q * 512, (SWIGLU && q >= 2 ? w_base1 : w_base0) + woff[q]);
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) woff[q] += 64;
+            w_base0 += 64;
+            if (SWIGLU) w_base1 += 64;
             if (r != w_run || j == 0) keep_rows();
         }
         w4_cp_commit();
@@ -463,7 +461,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             if (t == 0)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const uint8_t* p = (q < 2 ? w_base0 : w_base1) + woff[q];
+                    const uint8_t* p = (SWIGLU && q >= 2 ? w_base1 : w_base0) + woff[q];
                     w4_prefetch_l2(p);
                     if (w_end > 2) w4_prefetch_l2(p + 128);
                 }
