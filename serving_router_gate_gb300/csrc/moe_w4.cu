@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 // adds the parts in stage order (no atomics: the order is fixed by the sizes).
 //
 // Bound: HBM for the weights when they are many, else instruction issue.  A stage (2 KB of
-// codes) takes a warp 262 instructions, 144 of them to widen (nine per word of eight codes),
+// codes) takes a warp about 265 instructions, 144 of them to widen (nine per word of eight codes),
 // so the SMs together could take in 9 TB/s; at 16 warps an SM they issue in 0.6 of all
 // cycles (the rest: the ALU's and the tensor pipe's turns, and latency).  tcgen05 would
 // want the widened codes stored to shared memory and at least 128 rows a tile; registers
