@@ -85,7 +85,9 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 //
 // the inner sum is an mma.sync chain in fp32 over the codes widened to bf16 (c / 64, exact)
 // and the bf16 activations as they are (every product exact), the outer one an fp32 fused
-// multiply-add per group; y is rounded once.
+// multiply-add per group; the matvec's y is rounded once, to bf16, the experts' y not at
+// all.  FC1's h is rounded to bf16, the type that FC2's products take: carried in two bf16
+// words it would double them for an error that is the size of the output's own rounding.
 //
 // The work is a list of tiles, 32 weight rows of one slot (FC1: 16 gate rows and the
 // matching 16 up rows) times up to 8 C activation rows; a tile's K is cut into stages of
