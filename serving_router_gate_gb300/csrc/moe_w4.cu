@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 // left as subnormals with activations scaled by a kernel in front 50 us.
 //
 // Measured (weights not in L2): 65536 x 7168, groups of 128, one row 43.3 .. 45.3 us (two
-// boxes), 242 MB at 5.6 .. 5.3 TB/s; eight rows 49 us, sixteen 76 us.  Eight tokens, 8 of 256
+// boxes), 242 MB at 5.6 .. 5.3 TB/s; eight rows 47 us, sixteen 67 us.  Eight tokens, 8 of 256
 // experts of 7168 x 2048: 218 .. 234 us for FC1, FC2 and the combine, 1.30 GB at 6.0 .. 5.6
 // TB/s.  32 tokens, 6 of 64 experts of 2048 x 1408 and a shared one of 5632: 68 us (291 MB,
 // 4.3 TB/s); one token of it 19.3 us (45 MB): three kernels of about 6, 6 and 1.3 us
@@ -157,6 +157,18 @@ __device__ __forceinline__ void w4_cp16(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void w4_prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+// 32 consecutive bytes; WIDE: p is a multiple of 32
+template <bool WIDE>
+__device__ __forceinline__ void w4_ld32(uint4& u, uint4& v, const void* p) {
+    if (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w), "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+    } else {
+        u = static_cast<const uint4*>(p)[0];
+        v = static_cast<const uint4*>(p)[1];
+    }
 }
 __device__ __forceinline__ void w4_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -252,7 +264,8 @@ __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int
     }
 }
 
-template <bool SWIGLU, int GS, int C>
+// WIDE: an activation row's 32-byte pieces lie on 32 bytes and are fetched by one load each.
+template <bool SWIGLU, int GS, int C, bool WIDE>
 __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_constant__ W4Launch a) {
     constexpr int ROWS = 8 * C;  // activation rows of a tile
     extern __shared__ __align__(128) uint8_t w4_smem[];
@@ -513,11 +526,16 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     uint4 xb[AHEAD][C];
     uint32_t sb[NF];
     auto load_x = [&](int step, int has) {  // of the stage at xsrc, which holds `has` elements
-        const int at = step / 2 * 64 + step % 2 * (GS < 2 ? 32 : 8);
         if (step / GS * 32 * GS < has) {  // (has = 0: there is no such stage, and xsrc may lie past x)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                if (c == 0 || p_m > 8) xb[step % AHEAD][c] = *reinterpret_cast<const uint4*>(xsrc[c] + at);
+            for (int c = 0; c < C; ++c) {
+                if (c && p_m <= 8) continue;
+                if (GS < 2) {
+                    xb[step % AHEAD][c] = *reinterpret_cast<const uint4*>(xsrc[c] + step * 32);
+                } else if (step % 2) {  // both steps of a half: a lane's 32 consecutive bytes
+                    w4_ld32<WIDE>(xb[step % AHEAD - 1][c], xb[step % AHEAD][c], xsrc[c] + step / 2 * 64);
+                }
+            }
         }
     };
     auto load_s = [&](int f, int has) {
@@ -774,7 +792,7 @@ static W4Div w4_div(int d) {
     return r;
 }
 
-template <bool SWIGLU, int GS, int C>
+template <bool SWIGLU, int GS, int C, bool WIDE>
 static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t s) {
     // the shared-memory limit is set once per device
     static std::atomic<bool> ready[64];
@@ -783,7 +801,7 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem_bytes(C));
+        e = cudaFuncSetAttribute(w4_kernel<SWIGLU, GS, C, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)w4_smem_bytes(C));
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
@@ -801,19 +819,27 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
     K.by_sh = w4_div(n_sh);
     K.by_rt = w4_div(n_rt);
     K.by_k = w4_div(L.k);
-    return launch_k(L.name, w4_kernel<SWIGLU, GS, C>, dim3(grid), dim3(W4_THREADS), w4_smem_bytes(C), s, K);
+    return launch_k(L.name, w4_kernel<SWIGLU, GS, C, WIDE>, dim3(grid), dim3(W4_THREADS), w4_smem_bytes(C), s, K);
 }
 
 template <bool SWIGLU, int GS>
 static cudaError_t launch_w4_rows(const W4Launch& L, int num_sms, cudaStream_t s) {
     // Passes over the weights in pieces of 8 and of 16 rows (a slot holds rows_cap / G rows on
-    // average): one of 16 takes 1.6 times as long as one of 8 (65536 x 7168: 77 and 49 us).
+    // average): one of 16 takes 1.44 times as long as one of 8 (65536 x 7168: 67 and 47 us; 24 rows
+    // as two of 16 117 us, as three of 8 133; 32 tokens over 64 experts, 3 rows to a slot and
+    // 32 for the shared one, in pieces of 8 68 us, of 16 84).
     const double sh = L.sh.wq ? (double)L.sh.N_out * L.sh.K : 0.0;
     const double slots = (double)std::min<int64_t>(L.G, L.rows_cap);
     const double rt = slots * L.rt.N_out * L.rt.K, mean = slots > 0 ? L.rows_cap / slots : 0.0;
     auto passes = [&](double rows) { return sh * std::ceil(L.rows_sh / rows) + rt * std::max(1.0, mean / rows); };
-    return passes(8) <= 1.6 * passes(16) ? launch_w4_tiles<SWIGLU, GS, 1>(L, num_sms, s)
-                                         : launch_w4_tiles<SWIGLU, GS, 2>(L, num_sms, s);
+    const bool narrow = passes(8) <= 1.44 * passes(16);
+    // 32-byte loads of x where it allows them (half the requests: 65536 x 7168 by 16 rows 66 us,
+    // by 16-byte loads 70); groups of 32 take 16 bytes of a row at a time
+    if (GS > 1 && (((uintptr_t)L.sh.x | (uintptr_t)L.rt.x) & 31) == 0)
+        return narrow ? launch_w4_tiles<SWIGLU, GS, 1, (GS > 1)>(L, num_sms, s)
+                      : launch_w4_tiles<SWIGLU, GS, 2, (GS > 1)>(L, num_sms, s);
+    return narrow ? launch_w4_tiles<SWIGLU, GS, 1, false>(L, num_sms, s)
+                  : launch_w4_tiles<SWIGLU, GS, 2, false>(L, num_sms, s);
 }
 
 template <bool SWIGLU>

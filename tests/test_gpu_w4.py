@@ -184,6 +184,20 @@ def test_matvec_operands_that_end_with_their_allocations(M, N, K, group):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M", [3, 13])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_matvec_rows_on_16_bytes(M, group):
+    # rows that start on 16 but not on 32 bytes take two loads where the others take one: the same results
+    x, q, s, want = _matvec(M, 96, 384, group, seed=17)
+    buf = torch.empty(M * 384 + 8, dtype=torch.bfloat16, device="cuda")
+    odd = buf[8:].view(M, 384)
+    odd.copy_(x)
+    assert odd.data_ptr() % 32 == 16
+    y = torch.empty_like(want)
+    moe.moe_matvec_w4(odd, q, s, y)
+    assert torch.equal(y, want)
+
+
 def test_matvec_empty_batch():
     q, s = _weights((8,), 64, 64, 1)
     n = moe.moe_get_launch_count()
