@@ -138,8 +138,8 @@ struct W4Run {
 };
 
 // x / d for 0 <= x < 2^31 by the multiplier that the host made for d (w4_div: at most
-// 2^(31 + shift) / d + 1, exact for 31-bit x by Granlund and Montgomery's bound); the
-// divisions in front of a warp's first copy took a microsecond as such.
+// 2^(31 + shift) / d + 1, exact for 31-bit x by Granlund and Montgomery's bound): in 64 bits
+// and as divisions, a warp's share of the work took it 1.0 us to find, so 0.5.
 __device__ __forceinline__ int w4_over(int x, const W4Div& d) {
     return (int)(__umulhi(2 * (uint32_t)x, d.m) >> d.shift);
 }
