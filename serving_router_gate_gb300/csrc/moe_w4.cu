@@ -236,13 +236,13 @@ __device__ __forceinline__ void w4_store(const W4Problem& p, const W4Run& d, int
         if (c == 2 && d.m <= 8) break;
         const int col = 8 * (c / 2) + 2 * t + c % 2;
         if (col >= d.m) continue;
-        const float unit = xrow[col] < 0 ? 0.f : 64.f;
+        const bool ok = xrow[col] >= 0;  // (else the sums are of some other row, whose values may be NaN)
         const int64_t at = (int64_t)(d.row0 + col) * N + n0 + g;
         float v[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) v[r][h] = acc[c / 2][r][2 * h + c % 2] * unit;
+            for (int h = 0; h < 2; ++h) v[r][h] = ok ? acc[c / 2][r][2 * h + c % 2] * 64.f : 0.f;
         if (SWIGLU) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
