@@ -493,7 +493,9 @@ MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const 
  *   W1sq [2*I_shared_total, H/2], W1s_scale; W2sq [H, I_shared_total/2], W2s_scale (or NULL)
  *   ws       at least moe_workspace_size_w4 bytes
  * H, I and I_shared_total multiples of 64 and of group.  Entries of perm_src
- * outside [0, T*k) and of pair_row outside [-1, P_cap) are dropped and flagged.
+ * outside [0, T*k) and of pair_row outside [-1, P_cap) are dropped and flagged;
+ * offsets that descend or leave [0, P_cap] are flagged and no routed row is
+ * computed (out then holds whatever the workspace held for the routed pairs).
  * Meant for decode batches (up to about 16 rows per slot); larger batches are
  * right, but a slot's weights are read again, from L2, for every 8 or 16 rows.
  * MOE_ERR_UNSUPPORTED where (ceil(P_cap/8) + S_local - 1) ceil(I/16) ceil(H/128), or

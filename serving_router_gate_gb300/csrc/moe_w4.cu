@@ -304,14 +304,15 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         const int s0 = threadIdx.x * PER;
         int n[PER], sum = 0;
         int lo = s0 <= a.G ? __ldg(a.offsets + s0) : 0;
+        int ok = lo >= 0;  // ascending from 0 or more to rows_cap or less
         if (s0 <= a.G) s_off[s0] = lo;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             n[i] = 0;
             if (s0 + i < a.G) {
                 const int hi = __ldg(a.offsets + s0 + i + 1);
-                const int m = max(0, min(hi, rows_cap) - max(lo, 0));
-                n[i] = (int)((uint32_t)(m + ROWS - 1) / ROWS) * tiles_rt;
+                ok &= (hi >= lo) & (hi <= rows_cap);
+                n[i] = (int)(((uint32_t)hi - (uint32_t)lo + ROWS - 1) / ROWS) * tiles_rt;
                 lo = hi;
                 if (i + 1 < PER || s0 + PER == a.G) s_off[s0 + i + 1] = hi;
             }
@@ -323,21 +324,25 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             const int v = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += v;
         }
-        if (lane == 31) s_part[warp] = inc;
+        // (offsets that descend or leave the rows would outgrow the list's count: no routed tile then)
+        ok = __all_sync(0xffffffffu, ok);
+        if (lane == 31) s_part[warp] = ok ? inc : -1;
         __syncthreads();
-        int base = inc - sum, total = 0;
+        int base = inc - sum, total = 0, bad = 0;
 #pragma unroll
         for (int w = 0; w < W4_WARPS; ++w) {
             base += w < warp ? s_part[w] : 0;
             total += s_part[w];
+            bad |= s_part[w];
         }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             if (s0 + i < a.G) s_pre[s0 + i] = base;
             base += n[i];
         }
-        list_rt = total;
+        list_rt = bad < 0 ? 0 : total;
         __syncthreads();
+        if (bad < 0 && threadIdx.x == 0) report(a.status, MOE_ERR_DEVICE_BOUNDS);
     }
     // this CTA's tiles: from the first that starts at or after its share of the stages
     const int stages_sh = list_sh * n_sh, stages = stages_sh + list_rt * n_rt;
@@ -382,8 +387,8 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             const int s_at = s_lo + lane;
             s_lo += __popc(__ballot_sync(0xffffffffu, s_at < a.G && s_pre[s_at] <= w)) - 1;
             d.routed = true;
-            d.row0 = max(0, s_off[s_lo]);
-            rows = min(s_off[s_lo + 1], rows_cap);
+            d.row0 = s_off[s_lo];
+            rows = s_off[s_lo + 1];
             ct = (int)((uint32_t)(rows - d.row0 + ROWS - 1) / ROWS);
             q = w - s_pre[s_lo];
             at = s_lo * (SWIGLU ? 2 * (int64_t)a.rt.N_out : a.rt.N_out);

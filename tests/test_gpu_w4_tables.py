@@ -63,3 +63,29 @@ def test_bad_pair_row_entries_leave_the_other_pairs():
     got, status = _run(args)
     assert status == moe.MOE_ERR_DEVICE_BOUNDS
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("make", [
+    lambda off, cap: [0, cap] * (len(off) // 2) + [cap],            # slots that overlap, over and over
+    lambda off, cap: [-1] + off[1:],
+    lambda off, cap: [-2 ** 31] + off[1:],
+    lambda off, cap: off[:-1] + [cap + 1],
+    lambda off, cap: off[:-1] + [2 ** 31 - 1],
+    lambda off, cap: off[:3] + [off[2] - 1] + off[4:],
+    lambda off, cap: [cap] + [0] * (len(off) - 1),
+    lambda off, cap: [2 ** 31 - 1] + [-2 ** 31] * (len(off) - 1)])
+@pytest.mark.parametrize("E", [8, 500, 1024])
+def test_bad_offsets_are_flagged_and_no_routed_row_is_computed(E, make):
+    args = list(_experts(6, 128, 64, E, 4, 64, I_sh=64, gated=True, seed=22))
+    args[WS][moe.MOE_WS_HEADER_BYTES:] = 0               # routed outputs that nothing writes read as zeros
+    alone = list(args)
+    alone[PAIR_ROW] = torch.full_like(args[PAIR_ROW], -1)
+    want, status = _run(alone)                            # the shared expert alone
+    assert status == 0
+    args[WS][moe.MOE_WS_HEADER_BYTES:] = 0
+    off = make(args[OFFSETS].tolist(), 24)
+    assert len(off) == E + 1
+    args[OFFSETS] = torch.tensor(off, dtype=torch.int64).to(torch.int32).cuda()
+    got, status = _run(args)
+    assert status == moe.MOE_ERR_DEVICE_BOUNDS
+    assert torch.equal(got, want)
