@@ -17,7 +17,7 @@ Method (vLLM EP-aware FusedMoE override, ep_fused_moe_patch.py):
 Readings taken here: slot ranges split S as evenly as contiguous ranges allow
 (rank r owns [r S / N, (r + 1) S / N)), which is E / N when N divides S; the
 shared experts' intermediate is split the same way in units of 64 (the
-library's row granularity); the reduction runs in fp32 (the pages do not fix
+library's row granularity; whole groups of 4-bit weights); the reduction runs in fp32 (the pages do not fix
 its precision) and the result is rounded to bf16 once.
 
 Every rank calls the same three library calls as a one-GPU layer (moe_route,
@@ -60,13 +60,14 @@ def ep_shared_range(I_shared: int, world: int, rank: int, unit: int = 64) -> Tup
     return lo * unit, (hi - lo) * unit
 
 
-def ep_shared_shard(W1s: torch.Tensor, W2s: torch.Tensor, world: int, rank: int):
+def ep_shared_shard(W1s: torch.Tensor, W2s: torch.Tensor, world: int, rank: int, unit: int = 64):
     """The row-parallel shard of the shared experts (as one concatenated MLP:
     W1s [2 I_sh, H] gate rows then up rows, W2s [H, I_sh]) that rank `rank` holds:
-    gate rows [a, a + w), up rows [I_sh + a, I_sh + a + w), W2s columns [a, a + w).
+    gate rows [a, a + w), up rows [I_sh + a, I_sh + a + w), W2s columns [a, a + w),
+    a and w multiples of unit.
     Returns (W1 shard [2 w, H], W2 shard [H, w]) or (None, None) for w = 0."""
     I_sh = W2s.shape[1]
-    a, w = ep_shared_range(I_sh, world, rank)
+    a, w = ep_shared_range(I_sh, world, rank, unit)
     if w == 0:
         return None, None
     W1 = torch.cat([W1s[a:a + w], W1s[I_sh + a:I_sh + a + w]], 0).contiguous()
@@ -220,7 +221,8 @@ class EPMoELayer:
         W1sh = W2sh = None
         gate = None
         if W1s is not None:
-            W1sh, W2sh = ep_shared_shard(W1s, W2s, world, rank)
+            # (a group of 4-bit weights, up to 128 columns of W2s, stays on one rank)
+            W1sh, W2sh = ep_shared_shard(W1s, W2s, world, rank, max(64, int(layer_options.get("w4", 0))))
             gate = shared_gate_w if W1sh is not None else None
         self.layer = MoELayer(Wg, W1l, W2l, k, renorm, max_T, logit_bias=logit_bias, rep_offset=rep_offset,
                               rep_slots=rep_slots, S=S, local_start=self.start, local_count=self.count,
