@@ -204,8 +204,9 @@ class EPMoELayer:
     Wg [E, H] (replicated), W1 [S, 2I, H], W2 [S, H, I] (all slots; only this
     rank's range is kept), optional shared experts W1s [2 I_sh, H], W2s [H, I_sh]
     (concatenated; only this rank's shard is kept) and their gate vector; further
-    keyword options (routing variant, weight format) go to MoELayer as they are.
-    forward(x) returns the full layer output [T, H] after the reduction."""
+    keyword options (routing variant, weight format, norm) go to MoELayer as they are.
+    forward(x) returns the full layer output [T, H] after the reduction; block(x, residual)
+    that of the norm of the residual stream, which every rank holds."""
 
     def __init__(self, Wg, W1, W2, k, renorm, max_T, world: int, rank: int, logit_bias=None, rep_offset=None,
                  rep_slots=None, W1s=None, W2s=None, shared_gate_w=None, group=None,
@@ -244,6 +245,23 @@ class EPMoELayer:
         """Peer reduction, first half: this rank's partial into its slot, then its flag."""
         self.layer.forward(x, stream, out=self.peer.begin(x.shape[0]))
         self.peer.signal(stream)
+
+    def write_block_partial(self, x: torch.Tensor, residual: torch.Tensor, stream=None) -> None:
+        """write_partial with the norm in front (block())."""
+        self.layer.check_block()
+        self.layer.block(x, residual, stream, out=self.peer.begin(x.shape[0]))
+        self.peer.signal(stream)
+
+    def block(self, x: torch.Tensor, residual: torch.Tensor, stream=None) -> torch.Tensor:
+        """MoELayer.block over the ranks: every rank adds x to its copy of residual [T, H] in place, and the
+        reduction gives the full layer output of the norm."""
+        if self.peer is not None:
+            self.layer.check_block()
+            if x.shape[0] == 0:
+                return self.layer.out[:0]
+            self.write_block_partial(x, residual, stream)
+            return self.peer.reduce(stream)
+        return ep_reduce_output(self.layer.block(x, residual, stream), self.group)
 
 
 # ----------------------------------------------------------------------------- all-to-all dispatch and combine

@@ -240,14 +240,16 @@ class MoELayer:
         self.permute(x, stream)
         return self.expert_forward(x, stream, out)["out"]
 
+    def check_block(self) -> None:
+        if self.norm_w is None:
+            raise ValueError("block() needs norm_w")
 
     def block(self, x: torch.Tensor, residual: torch.Tensor, stream=None,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The norm and the layer: residual [T, H] (bf16 or fp32) becomes residual + x in place, and the layer's
         forward of its RMS norm (norm_w, norm_eps) is returned.  With E4M3 activations the experts read the norm's own
         E4M3 rows (rounded once, from the unrounded norm)."""
-        if self.norm_w is None:
-            raise ValueError("block() needs norm_w")
+        self.check_block()
         T = x.shape[0]
         assert T <= self.max_T and x.shape[1] == self.H
         if T == 0:

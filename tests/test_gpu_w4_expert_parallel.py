@@ -8,7 +8,7 @@ import torch
 
 import moe_inputs as mi
 import serving_router_gate_gb300 as moe
-from serving_router_gate_gb300.expert_parallel import EPMoELayer
+from serving_router_gate_gb300.expert_parallel import EPMoELayer, PeerReduction
 from serving_router_gate_gb300.layer import MoELayer
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +35,50 @@ def test_partials_sum_to_the_one_gpu_layer(world, w4):
         assert moe.moe_get_device_status(rank.layer.ws) == 0
         acc, size = acc + part, size + part.norm()
     assert (acc - full).norm() <= 2.0 ** -7 * size
+
+
+def _norm_case(T=9):
+    cfg, d, shared = _case(T)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    norm = dict(norm_w=(1.0 + 0.2 * torch.randn(cfg.H, generator=g, device="cuda")).to(torch.bfloat16), norm_eps=1e-5)
+    return cfg, d, dict(w4=64, **shared, **norm), torch.randn(T, cfg.H, generator=g, device="cuda") * 3.0
+
+
+def test_block_of_the_ranks_is_the_norm_then_the_layer():
+    cfg, d, options, residual = _norm_case()
+    r0 = residual.clone()
+    full = MoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, True, cfg.T, **options).block(d["x"], r0).double()
+    acc, size = torch.zeros_like(full), full.norm()
+    for r in range(2):
+        rank = EPMoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, True, cfg.T, 2, r, **options)
+        mine = residual.clone()
+        part = rank.block(d["x"], mine).double()
+        assert torch.equal(mine, r0)                      # the stream, replicated
+        acc, size = acc + part, size + part.norm()
+    assert (acc - full).norm() <= 2.0 ** -7 * size
+    rank = EPMoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, True, cfg.T, 2, 0, w4=64)
+    with pytest.raises(ValueError):
+        rank.block(d["x"], residual)                      # no norm
+
+
+def test_block_through_the_peer_reduction():
+    cfg, d, options, residual = _norm_case()
+    r0 = residual.clone()
+    full = MoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, True, cfg.T, **options).block(d["x"], r0).double()
+    reds = PeerReduction.local_set(cfg.T, cfg.H, 2, "cuda")
+    ranks = [EPMoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, True, cfg.T, 2, r, peer=reds[r], **options)
+             for r in range(2)]
+    with pytest.raises(ValueError):                       # refused before the epoch advances
+        EPMoELayer(d["Wg"], d["W1"], d["W2"], cfg.k, True, cfg.T, 2, 0, peer=reds[0], w4=64).block(d["x"], residual)
+    for step in range(3):
+        mine = [residual.clone() for _ in ranks]
+        for rank, m in zip(ranks, mine):                  # every partial and flag before the first reduction
+            rank.write_block_partial(d["x"], m)
+        outs = [rank.peer.reduce() for rank in ranks]
+        torch.cuda.synchronize()
+        assert all(torch.equal(m, r0) for m in mine)
+        assert torch.equal(outs[0], outs[1])
+        parts = [rank.peer.slots[rank.peer.epoch % 2, :cfg.T].double() for rank in ranks]
+        size = full.norm() + sum(p.norm() for p in parts)
+        assert (outs[0].double() - full).norm() <= 2.0 ** -7 * size
+        assert all(moe.moe_get_device_status(rank.peer.ws) == 0 for rank in ranks)
