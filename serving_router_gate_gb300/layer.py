@@ -164,7 +164,10 @@ class MoELayer:
 
     def expert_forward(self, x: torch.Tensor, stream=None, out: Optional[torch.Tensor] = None, x_q=None,
                        x_scale=None) -> dict:
-        """x_q, x_scale: x's rows in E4M3 already (E4M3 activations only), else made from x."""
+        """x_q, x_scale: x's rows in E4M3 already (E4M3 activations with the weights at the output only), else made
+        from x."""
+        if x_q is not None and (not self.act8 or self.on_input):
+            raise ValueError("E4M3 rows are for E4M3 activations (act8=True) with the routing weights at the output")
         v = self.views(x.shape[0])
         if out is not None:
             v["out"] = out
