@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         next_v += d.tiles;
         if (lane < ROWS) {  // (kept when the first copies are on their way)
             xrow = d.row0 + min(lane, d.m - 1);
-            if (d.routed && a.perm_src) xrow = a.perm_src[xrow];
+            if (d.routed && a.perm_src) xrow = in_bounds(xrow, a.rows_cap, a.status) ? a.perm_src[xrow] : -1;
         }
         __syncwarp();
         if (lane == 0) runs[i % W4_RUNS] = d;
@@ -414,6 +414,33 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
     auto row_of = [&](const W4Problem& p, const W4Run& d, int q) {  // weight row g + 8 q from the run's first
         const int r = q * 8 + g;
         return SWIGLU ? (q < 2 ? r : r - 16 + p.N_out) : min(r, p.N_out - 1 - d.n0);
+    };
+
+    // (bounds-checked library) the n bytes at p lie in the run's codes, scales or activations
+    auto inside = [&](const void* p, const void* base, int64_t size, int n) {
+        const int64_t at = static_cast<const uint8_t*>(p) - static_cast<const uint8_t*>(base);
+        return in_bounds(at, size - n + 1, a.status);
+    };
+    auto codes_ok = [&](int run, const void* p) {
+        const bool rt = runs[run % W4_RUNS].routed;
+        const W4Problem& w = rt ? a.rt : a.sh;
+        return inside(p, w.wq, (SWIGLU ? 2 : 1) * (int64_t)w.N_out * (rt ? a.G : 1) * (w.K / 2), 16);
+    };
+    auto scale_ok = [&](int run, const void* p) {
+        const bool rt = runs[run % W4_RUNS].routed;
+        const W4Problem& w = rt ? a.rt : a.sh;
+        return inside(p, w.ws, (SWIGLU ? 2 : 1) * (int64_t)w.N_out * (rt ? a.G : 1) * (w.K / (32 * GS)) * 2, 2);
+    };
+    auto x_ok = [&](int run, const void* p, int n) {
+        const bool rt = runs[run % W4_RUNS].routed;
+        const W4Problem& w = rt ? a.rt : a.sh;
+        return inside(p, w.x, (rt ? (a.perm_src ? a.T : a.rows_cap) : a.rows_sh) * w.K * 2, n);
+    };
+    auto tile_ok = [&](const W4Run& d, int n0) {
+        const int64_t rows = d.routed ? a.rows_cap : a.rows_sh;
+        const int N = d.routed ? a.rt.N_out : a.sh.N_out;
+        return in_bounds(d.row0, rows, a.status) && in_bounds(d.row0 + d.m - 1, rows, a.status) &&
+               in_bounds(SWIGLU ? n0 + TN - 1 : n0, N, a.status);
     };
 
     // rows g, g + 8 from the first base, g + 16, g + 24 (FC1: the up rows g, g + 8) from the second
@@ -464,7 +491,10 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             w_open = true;
             if (GS == 4 || !(w_cut && j + 1 == w_end)) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) w4_cp16(w_slot + w_off + q * 512, (SWIGLU && q >= 2 ? w_base1 : w_base0) + woff[q]);
+                for (int q = 0; q < 4; ++q) {
+                    const uint8_t* src = (SWIGLU && q >= 2 ? w_base1 : w_base0) + woff[q];
+                    if (codes_ok(w_run, src)) w4_cp16(w_slot + w_off + q * 512, src);
+                }
             }
             w_base0 += 64;
             if (SWIGLU) w_base1 += 64;
@@ -536,15 +566,17 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             for (int c = 0; c < C; ++c) {
                 if (c && p_m <= 8) continue;
                 if (GS < 2) {
-                    xb[step % AHEAD][c] = *reinterpret_cast<const uint4*>(xsrc[c] + step * 32);
+                    if (x_ok(p_run, xsrc[c] + step * 32, 16))
+                        xb[step % AHEAD][c] = *reinterpret_cast<const uint4*>(xsrc[c] + step * 32);
                 } else if (step % 2) {  // both steps of a half: a lane's 32 consecutive bytes
-                    w4_ld32<WIDE>(xb[step % AHEAD - 1][c], xb[step % AHEAD][c], xsrc[c] + step / 2 * 64);
+                    if (x_ok(p_run, xsrc[c] + step / 2 * 64, 32))
+                        w4_ld32<WIDE>(xb[step % AHEAD - 1][c], xb[step % AHEAD][c], xsrc[c] + step / 2 * 64);
                 }
             }
         }
     };
     auto load_s = [&](int f, int has) {
-        if (f * 32 * GS < has) sb[f] = __ldg(ssrc + f);
+        if (f * 32 * GS < has && scale_ok(p_run, ssrc + f)) sb[f] = __ldg(ssrc + f);
     };
     float acc[C][2][4] = {};
     int left = 0;  // elements of the stage that is multiplied next
@@ -644,7 +676,8 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
         if (i + 1 == end || i + 1 == cnt) {  // the tile's last stage here
             const W4Run& d = runs[run % W4_RUNS];
             if (!begun && i + 1 == end) {
-                w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, n0, s_x[warp][run % W4_RUNS], acc);
+                if (tile_ok(d, n0))
+                    w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, n0, s_x[warp][run % W4_RUNS], acc);
             } else {
                 float4* o = parts + (warp * 2 + (begun ? 0 : 1)) * (64 * C) + lane;
 #pragma unroll
@@ -699,7 +732,7 @@ __global__ void __launch_bounds__(W4_THREADS, W4_CTAS) w4_kernel(const __grid_co
             }
         }
         const W4Run& d = runs[W4_RUNS];
-        w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, d.n0, s_x[warp][W4_RUNS], acc);
+        if (tile_ok(d, d.n0)) w4_store<SWIGLU, C>(d.routed ? a.rt : a.sh, d, d.n0, s_x[warp][W4_RUNS], acc);
     }
 }
 
