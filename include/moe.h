@@ -496,6 +496,8 @@ MOE_API moe_status_t moe_matvec_w4(const moe_bf16_t *x, const uint8_t *q, const 
  * outside [0, T*k) and of pair_row outside [-1, P_cap) are dropped and flagged;
  * offsets that descend or leave [0, P_cap] are flagged and no routed row is
  * computed (out then holds whatever the workspace held for the routed pairs).
+ * A call repeats itself bit for bit; where a sum over K is cut follows from all
+ * slots' rows, so a token's result may differ in its last bits in another batch.
  * Meant for decode batches (up to about 16 rows per slot); larger batches are
  * right, but a slot's weights are read again, from L2, for every 8 or 16 rows.
  * MOE_ERR_UNSUPPORTED where (ceil(P_cap/8) + S_local - 1) ceil(I/16) ceil(H/128), or

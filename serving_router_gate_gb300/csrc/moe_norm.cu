@@ -15,8 +15,9 @@
 // Bound: HBM.  A row is read once (x and residual) and written once (stream, y,
 // q); the row's values stay in registers between the two reductions.  16384 rows of
 // 7168 with a bf16 stream, y and E4M3 rows: 164 us, 1.06 GB at 6.45 TB/s, 0.95 of this
-// card's copy rate.  Small batches are bound by latency: one row of 2048 1.9 us, 32 of
-// 7168 with an fp32 stream 3.8 us, 777 of 1408 3.7 us, each call behind the last.
+// card's copy rate; with an fp32 stream 237 us, 1.53 GB at 6.43 TB/s.  Small batches are
+// bound by latency: one row of 2048 1.9 us, 32 of 7168 with an fp32 stream 3.8 us, 777 of
+// 1408 3.7 us, each call behind the last.
 //
 // The sum of squares, rstd, y before its rounding and the maximum are binary32.  The
 // stream's bf16 form rounds r once, where the model's next layer would read it.
@@ -109,8 +110,9 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rm
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) tot += red_sum[it][w];
         }
-        // rstd to twice binary32's precision: its rounding would move a whole row of y by up
-        // to 2^-24 and with it every E4M3 code that sits on a boundary
+        // the root's reciprocal in two words: its own rounding, which would move a whole row of
+        // y by up to 2^-24, is taken out.  ms stays one binary32 value: the roundings of the
+        // sum, of the division and of eps move the row by half of theirs
         const float ms = tot / (float)a.H + a.eps;
         const float hi = __frsqrt_rn(ms);
         const float sq = ms * hi, err = fmaf(-sq, hi, 1.f) - fmaf(ms, hi, -sq) * hi;
@@ -172,7 +174,9 @@ cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // A warp to a row while its lanes hold it in two vectors each, then one vector a thread
     // to 2048 values, and a CTA of 224 or 256 threads with four: at 7168 values (16384 rows
     // with E4M3 rows) four of 224 threads take 164 us, two of 448 take 201, one of 896 197
-    // and four of 256 (an eighth of them idle) 175.
+    // and four of 256 (an eighth of them idle) 175.  That width alone was compared; the other
+    // widths of these forms run at (16384 rows, of the copy rate): 4096 0.99, 5120 (a vector of
+    // four idle) 0.90, 6144 0.90, and at 1.06 GB 8192 0.91, 16384 0.84.
     const int vec = L.H / 8;
     if (vec <= 32) return launch_norm_size<1, 32, F32>(L, num_sms, s);
     if (vec <= 64) return launch_norm_size<2, 32, F32>(L, num_sms, s);

@@ -26,9 +26,10 @@ namespace {
 // A code is f / s to the nearest integer, ties to even.  f and s have eight significant
 // bits, so f / s is a tie or at least 2^-12 (relative) away from one: f times the rounded
 // 1 / s gives the integer except at a tie, and there the remainder f - c s, which is exact,
-// tells.  Bound: instruction issue.  65536 x 7168 with groups of 32 (128): 426 (457) us,
-// 2.8 (2.6) TB/s of weights read and codes written; eight IEEE divisions a lane instead
-// 606 (628).  It runs once per weight.
+// tells.  Bound: instruction issue, above all the ALU (16384 x 7168: a scheduler issues in
+// 0.83 of its cycles, the ALU is at 79 %, 251 instructions a warp of words).  65536 x 7168
+// with groups of 32 (128): 426 .. 434 (457 .. 462) us, 2.8 (2.6) TB/s of weights read and
+// codes written; eight IEEE divisions a lane instead 606 (628).  It runs once per weight.
 // ---------------------------------------------------------------------------
 constexpr int W4Q_THREADS = 256;
 constexpr int W4Q_CTAS = 64;  // an SM before they loop; 8: 455 us at the size above
@@ -86,8 +87,9 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 // the inner sum is an mma.sync chain in fp32 over the codes widened to bf16 (c / 64, exact)
 // and the bf16 activations as they are (every product exact), the outer one an fp32 fused
 // multiply-add per group; the matvec's y is rounded once, to bf16, the experts' y not at
-// all.  FC1's h is rounded to bf16, the type that FC2's products take: carried in two bf16
-// words it would double them for an error that is the size of the output's own rounding.
+// all.  FC1's h is rounded to bf16, the type that FC2's products take, as every other weight
+// format of the layer rounds it: the workspace holds it at that width, and with the output's
+// own rounding the experts are 2.3e-3 from 64 bits (2-norm; the output's alone 1.6e-3).
 //
 // The work is a list of tiles, 32 weight rows of one slot (FC1: 16 gate rows and the
 // matching 16 up rows) times up to 8 C activation rows; a tile's K is cut into stages of
@@ -96,25 +98,32 @@ __global__ void __launch_bounds__(W4Q_THREADS) quantize_w4_rows_kernel(const uin
 // fall into.  A warp streams its stages through a ring of its own without a break at a
 // tile's end; it stores the tiles that are all its own, and leaves its part of the at most
 // two that it shares with its neighbours in shared memory, where the warp that ends a tile
-// adds the parts in stage order (no atomics: the order is fixed by the sizes).
+// adds the parts in stage order.  (No atomics: a call repeats itself.  Where a sum over K is cut
+// follows from the list: for a matrix from the sizes, and a row of up to 16 gives the same
+// in any batch; for the experts also from the slots' rows, and a token's sums may be cut
+// elsewhere in another batch.)
 //
 // Bound: HBM for the weights when they are many, else instruction issue.  A stage (2 KB of
-// codes) takes a warp about 265 instructions, 144 of them to widen (nine per word of eight codes),
+// codes) takes a warp about 265 instructions (32768 x 7168 by one row with all else: 272), 144
+// of them to widen (nine per word of eight codes),
 // so the SMs together could take in 9 TB/s; at 16 warps an SM they issue in 0.6 of all
-// cycles (the rest: the ALU's and the tensor pipe's turns, and latency).  tcgen05 would
+// cycles (the rest: the ALU's and the tensor pipe's turns, and latency).  Without the
+// products, the loads alone, 65536 x 7168 takes 40 us.  tcgen05 would
 // want the widened codes stored to shared memory and at least 128 rows a tile; registers
 // feed mma.sync as they are, and a tile of 32 rows splits evenly at one row of activations.
 // What else was measured for 65536 x 7168 by one row when it took 48 us: 24 warps an SM on
 // 80 registers 59 us, 16 warps in one CTA no faster, the ring's loop unrolled by four
-// slower (the instruction cache), codes as E4M3 pieces 70 us (emulated on this part), codes
+// slower (the instruction cache), codes as E4M3 pieces on m16n8k32 70 us, codes
 // left as subnormals with activations scaled by a kernel in front 50 us.
 //
-// Measured (weights not in L2): 65536 x 7168, groups of 128, one row 43.3 .. 45.3 us (two
-// boxes), 242 MB at 5.6 .. 5.3 TB/s; eight rows 47 us, sixteen 67 us.  Eight tokens, 8 of 256
-// experts of 7168 x 2048: 218 .. 234 us for FC1, FC2 and the combine, 1.30 GB at 6.0 .. 5.6
+// Measured (weights not in L2): 65536 x 7168, groups of 128, one row 42.8 .. 45.3 us (several
+// boxes), 242 MB at 5.7 .. 5.3 TB/s; eight rows 46 .. 47 us, sixteen 67 .. 69 us; groups of 64
+// 49, 53 and 105 us, of 32 77, 86 and 129 us.  Eight tokens, 8 of 256
+// experts of 7168 x 2048: 217 .. 234 us for FC1, FC2 and the combine, 1.30 GB at 6.0 .. 5.6
 // TB/s.  32 tokens, 6 of 64 experts of 2048 x 1408 and a shared one of 5632: 68 us (291 MB,
-// 4.3 TB/s); one token of it 19.3 us (45 MB): three kernels of about 6, 6 and 1.3 us
-// behind prologues of 3 us and 1.5 us from each one's end to the next one's start.
+// 4.3 TB/s); one token of it 19.5 us (45 MB), most of it start-up: its 14080 and 7040 stages
+// of FC1 and FC2 would take 6 and 4 us at that batch's rate, and the kernels alone and
+// cold take 13.0, 12.2 and 6.3 us.
 // ---------------------------------------------------------------------------
 constexpr int W4_WARPS = 8;
 constexpr int W4_THREADS = W4_WARPS * 32;
@@ -844,7 +853,10 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
         ready[dev].store(true, std::memory_order_release);
     }
     // No more CTAs than tiles, and no fewer stages to a CTA than its longest tile has
-    // (between one CTA an SM and as many as fit).
+    // (between one CTA an SM and as many as fit).  The rows are on the GPU: a routed slot is
+    // taken to have one row tile, so a few slots with more get fewer CTAs than tiles (one of
+    // 2048 x 768 with 32 rows 13.3 us, 11.3 on a grid for all its tiles; but a grid for all that
+    // T k pairs could make costs a rank with one of 64 slots, 32 tokens, 11.3 us for 10.1).
     constexpr int TN = SWIGLU ? 16 : 32;
     const int n_sh = (L.sh.K + 127) / 128, n_rt = (L.rt.K + 127) / 128;
     const double sh = L.sh.wq ? (double)((L.sh.N_out + TN - 1) / TN) * ((L.rows_sh + 8 * C - 1) / (8 * C)) : 0.0;
@@ -863,9 +875,12 @@ static cudaError_t launch_w4_tiles(const W4Launch& L, int num_sms, cudaStream_t 
 template <bool SWIGLU, int GS>
 static cudaError_t launch_w4_rows(const W4Launch& L, int num_sms, cudaStream_t s) {
     // Passes over the weights in pieces of 8 and of 16 rows (a slot holds rows_cap / G rows on
-    // average): one of 16 takes 1.44 times as long as one of 8 (65536 x 7168: 67 and 47 us; 24 rows
-    // as two of 16 117 us, as three of 8 133; 32 tokens over 64 experts, 3 rows to a slot and
-    // 32 for the shared one, in pieces of 8 68 us, of 16 84).
+    // average; fewer on a rank whose pairs are partly other ranks'): one of 16 takes 1.44 times
+    // as long as one of 8 with groups of 128 (65536 x 7168: 67 and 47 us; 24 rows as two of 16
+    // 117 us, as three of 8 133; 32 tokens over 64 experts, 3 rows to a slot and
+    // 32 for the shared one, in pieces of 8 68 us, of 16 84).  Groups of 32: 1.49 (86 and 129 us).
+    // Groups of 64: 2.0 (53 and 105 us); 9 to 16 rows stay one piece all the same, so that a
+    // row of them gives the same in any batch.
     const double sh = L.sh.wq ? (double)L.sh.N_out * L.sh.K : 0.0;
     const double slots = (double)std::min<int64_t>(L.G, L.rows_cap);
     const double rt = slots * L.rt.N_out * L.rt.K, mean = slots > 0 ? L.rows_cap / slots : 0.0;
