@@ -30,7 +30,7 @@
  *    that timed out) are OR-ed into a status word inside `ws`; read and clear
  *    it with moe_get_device_status.  Kernels never trap: a bad pair is dropped
  *    and flagged, a timed-out wait abandons its tile and flags.
- *  - T = 0 is valid and enqueues nothing.
+ *  - T = 0 is valid and enqueues nothing (a weight's gradient is set to 0).
  *  - Supported sizes: H and I multiples of 64, 1 <= k <= 32, k <= E <= 512,
  *    S (slots) <= 1024, T * k < 2^31; anything else -> MOE_ERR_UNSUPPORTED.
  *
@@ -443,6 +443,121 @@ MOE_API moe_status_t moe_forward_w8a8_rows(const uint8_t *xq, const float *x_sca
 MOE_API moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const void *residual, int residual_f32,
                                    const moe_bf16_t *weight, float eps, int64_t T, int H, void *residual_out,
                                    moe_bf16_t *y, uint8_t *q, float *scale, moe_stream_t stream);
+
+/* moe_add_layernorm -- the same with a layer norm:
+ *     r = residual + x, d = r - sum(r) / H
+ *     y = d / sqrt(sum(d^2) / H + eps) * weight + bias
+ * bias [H] bf16, 16-byte aligned, or NULL (0).  The mean is taken before the squares, so
+ * a row far from zero keeps its variance.  With eps > 0 a row of equal values gives
+ * y = bias.  Everything else as moe_add_rmsnorm. */
+MOE_API moe_status_t moe_add_layernorm(const moe_bf16_t *x, const void *residual, int residual_f32,
+                                   const moe_bf16_t *weight, const moe_bf16_t *bias, float eps, int64_t T, int H,
+                                   void *residual_out, moe_bf16_t *y, uint8_t *q, float *scale, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gradients of the token path: norm, routing weights, sorted rows, combine. */
+/* ------------------------------------------------------------------------ */
+/* The way back of a block whose expert products are differentiated by the caller:
+ *   moe_finalize_bwd         from the block's output to the experts' outputs, the routing
+ *                            weights and the gated shared expert
+ *   moe_permute_bwd          from the experts' inputs to the tokens
+ *   moe_route_bwd            from the routing weights to the logits
+ *   moe_add_rmsnorm_bwd, moe_add_layernorm_bwd   from the norm's output to its input
+ * Every sum is binary32 and has a fixed order: a call repeats itself bit for bit (on one
+ * kind of GPU: the weight gradients are cut by its number of SMs).  bf16 outputs are
+ * rounded once.  T = 0 writes nothing but the weight gradients, which are then 0.
+ * Outputs are written, not added to, and overlap nothing except where a call says so. */
+
+/* Bytes of workspace for these calls (H a multiple of 8): the header, and the partial sums
+ * of a weight gradient.  Returns 0 for an invalid size. */
+MOE_API size_t moe_workspace_size_bwd(int H);
+
+/* The gradient of moe_add_rmsnorm's y at r, per row
+ *     rstd = 1 / sqrt(sum(r^2) / H + eps), g = dy * weight
+ *     dr = dstream + rstd * (g - r * rstd^2 * sum(g r) / H)
+ *     dweight = sum over rows of dy * r * rstd
+ *   dy       [T, H] bf16          gradient of y
+ *   r        [T, H] bf16 (r_f32 = 0) or fp32 (1): the stream moe_add_rmsnorm wrote to
+ *            residual_out (or its x, without a residual)
+ *   dstream  [T, H] of r's type, or NULL: gradient that reaches r past the norm
+ *   dr       [T, H] of r's type out, or NULL: the gradient of the residual and of x
+ *   dx       [T, H] bf16 out, or NULL: the same values
+ *   dweight  [H] fp32 out, or NULL
+ *   ws       with dweight: at least moe_workspace_size_bwd(H) bytes
+ * At least one output is given.  dr may be dstream or r, and dx may be dy.  H: a multiple of 8,
+ * at most 16384.  Pointers 16-byte aligned. */
+MOE_API moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t *dy, const void *r, int r_f32, const moe_bf16_t *weight,
+                                   float eps, int64_t T, int H, const void *dstream, void *dr, moe_bf16_t *dx,
+                                   float *dweight, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The gradient of moe_add_layernorm's y at r: with d = r - sum(r) / H,
+ *     rstd = 1 / sqrt(sum(d^2) / H + eps), g = dy * weight
+ *     dr = dstream + rstd * (g - sum(g) / H - d * rstd^2 * sum(g d) / H)
+ *     dweight = sum over rows of dy * d * rstd, dbias = sum over rows of dy
+ * dbias [H] fp32 out, or NULL.  Everything else as moe_add_rmsnorm_bwd. */
+MOE_API moe_status_t moe_add_layernorm_bwd(const moe_bf16_t *dy, const void *r, int r_f32, const moe_bf16_t *weight,
+                                   float eps, int64_t T, int H, const void *dstream, void *dr, moe_bf16_t *dx,
+                                   float *dweight, float *dbias, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The gradient of moe_finalize,
+ *     out[t] = sum_j topk_w[t,j] y[pair_row[t,j]] + g_t y_shared[t],  g_t = sigmoid(z_t), z_t = x[t] . shared_gate_w:
+ *     dy[pair_row[t,j]] = topk_w[t,j] * dout[t]
+ *     dtopk_w[t,j] = y[pair_row[t,j]] . dout[t]
+ *     dy_shared[t] = g_t * dout[t]
+ *     dgate[t] = g_t (1 - g_t) (y_shared[t] . dout[t])      (the gradient of z_t)
+ *     dshared_gate_w = sum_t dgate[t] x[t]                  (x's own part is moe_permute_bwd's)
+ *   dout     [T, H] bf16, pair_row [T, k] int32, topk_w [T, k] fp32 or NULL (weight 1)
+ *   y        [rows_cap, H] bf16; read for dtopk_w only (else it may be NULL)
+ *   dy       [rows_cap, H] bf16 out; rows that no pair has are left as they were.  dy may be y.
+ *   dtopk_w  [T, k] fp32 out, or NULL; 0 for a pair of row -1.  Needs topk_w.
+ *   y_shared, x [T, H] bf16, shared_gate_w [H] bf16, dy_shared [T, H] bf16 out, dgate [T] fp32
+ *            out: a gated shared expert, or all NULL (without a gate dy_shared is dout)
+ *   dshared_gate_w [H] fp32 out, 16-byte aligned, or NULL
+ *   ws       its status word; with dshared_gate_w at least moe_workspace_size_bwd(H) bytes
+ * pair_row holds a row once (as moe_permute writes it); entries outside [-1, rows_cap) are taken as
+ * -1 and flagged.  H a multiple of 64, k <= 32, T * k < 2^31.  Row pointers 16-byte aligned. */
+MOE_API moe_status_t moe_finalize_bwd(const moe_bf16_t *dout, const moe_bf16_t *y, int64_t rows_cap,
+                                   const int32_t *pair_row, const float *topk_w, int64_t T, int k, int H,
+                                   const moe_bf16_t *y_shared, const moe_bf16_t *x, const moe_bf16_t *shared_gate_w,
+                                   moe_bf16_t *dy, float *dtopk_w, moe_bf16_t *dy_shared, float *dgate,
+                                   float *dshared_gate_w, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The gradient of moe_permute's rows (topk_w NULL) or moe_permute_on_input's, together with
+ * what else reaches the tokens:
+ *     dx[t] = dx_add[t] + sum_j topk_w[t,j] dx_perm[pair_row[t,j]] + dgate[t] shared_gate_w
+ *     dtopk_w[t,j] = x[t] . dx_perm[pair_row[t,j]]
+ * (the rounding of x_perm to bf16 counts as none).
+ *   dx_perm  [rows_cap, H] bf16, pair_row [T, k] int32, topk_w [T, k] fp32 or NULL (weight 1)
+ *   x        [T, H] bf16; read for dtopk_w only (else it may be NULL)
+ *   dx_add   [T, H] bf16 (dx_add_f32 = 0) or fp32 (1), or NULL: the shared experts' and the
+ *            router's gradients of x
+ *   dgate    [T] fp32 and shared_gate_w [H] bf16: the gate's part (moe_finalize_bwd), or both NULL
+ *   dx       [T, H] bf16 out; it may be x, or a bf16 dx_add
+ *   dtopk_w  [T, k] fp32 out, or NULL; 0 for a pair of row -1.  Needs topk_w and x.
+ *   ws       only its status word is used
+ * Bad entries of pair_row, sizes and alignment as moe_finalize_bwd. */
+MOE_API moe_status_t moe_permute_bwd(const moe_bf16_t *dx_perm, int64_t rows_cap, const int32_t *pair_row,
+                                   const float *topk_w, const moe_bf16_t *x, const void *dx_add, int dx_add_f32,
+                                   const float *dgate, const moe_bf16_t *shared_gate_w, int64_t T, int k, int H,
+                                   moe_bf16_t *dx, float *dtopk_w, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* The gradient of moe_route's (and moe_route_grouped's) weights with respect to the logits,
+ * the chosen experts held fixed: with c = sum_j topk_w[t,j] dtopk_w[t,j]
+ *     dlogits[t,e] = sum_j [e = topk_ids[t,j]] topk_w[t,j] dtopk_w[t,j] - c p[t,e]
+ * p the softmax of the logits (renorm = 0), or the sum of the topk_w of the pairs of expert e
+ * (renorm = 1: 0 for the experts not chosen).
+ *   topk_ids, topk_w [T, k]  as moe_route wrote them (moe_permute zeroes the weights of
+ *            non-local pairs in place: keep a copy)
+ *   dtopk_w  [T, k] fp32     summed over the ranks where experts are spread over several
+ *   logits   [T, E] fp32     x . gate_w with logit_bias added (needed with renorm = 0 only, else
+ *            not read and may be NULL)
+ *   dlogits  [T, E] fp32 out; it may be logits
+ *   ws       only its status word is used
+ * gate_w's gradient is dlogits^T x, x's part dlogits gate_w, logit_bias's the column sums.  An id
+ * outside [0, E) is flagged and its pair left out.  logits and dlogits 16-byte aligned. */
+MOE_API moe_status_t moe_route_bwd(const int32_t *topk_ids, const float *topk_w, const float *dtopk_w,
+                                   const float *logits, int64_t T, int E, int k, int renorm, float *dlogits,
+                                   void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* 4-bit weights with group scales, bf16 activations.                        */

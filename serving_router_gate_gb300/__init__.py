@@ -32,7 +32,8 @@ __all__ = [
     "moe_grouped_fc2_scatter", "moe_ep_signal", "moe_ep_reduce", "moe_ipc_export", "moe_ipc_import",
     "moe_ipc_close", "MOE_IPC_HANDLE_BYTES",
     "MOE_A2A_TO_GEMM", "MOE_A2A_TO_EXCHANGE", "moe_add_rmsnorm", "moe_forward_w8a8_rows", "moe_quantize_w4_rows",
-    "moe_matvec_w4", "moe_forward_w4", "moe_workspace_size_w4",
+    "moe_matvec_w4", "moe_forward_w4", "moe_workspace_size_w4", "moe_add_layernorm", "moe_add_rmsnorm_bwd",
+    "moe_add_layernorm_bwd", "moe_finalize_bwd", "moe_permute_bwd", "moe_route_bwd", "moe_workspace_size_bwd",
 ]
 
 MOE_OK = 0
@@ -61,7 +62,8 @@ EXPORTED_SYMBOLS = (
     "moe_launch_events_arm", "moe_launch_events_mark", "moe_launch_events_used", "moe_a2a_regroup",
     "moe_grouped_fc2_scatter", "moe_ep_signal", "moe_ep_reduce", "moe_ipc_export", "moe_ipc_import",
     "moe_ipc_close", "moe_add_rmsnorm", "moe_forward_w8a8_rows", "moe_quantize_w4_rows", "moe_matvec_w4",
-    "moe_forward_w4", "moe_workspace_size_w4",
+    "moe_forward_w4", "moe_workspace_size_w4", "moe_add_layernorm", "moe_add_rmsnorm_bwd", "moe_add_layernorm_bwd",
+    "moe_finalize_bwd", "moe_permute_bwd", "moe_route_bwd", "moe_workspace_size_bwd",
 )
 
 
@@ -126,6 +128,13 @@ def _load():
         "moe_forward_w4": ([P, P, i32, i64, P, P, P, P, P, i32, i32, i32, P, P, i64, i32, P, P, P, P, i32, P, P, P, sz,
                             P], i32),
         "moe_workspace_size_w4": ([i64, i32, i32, i32, i32], sz),
+        "moe_add_layernorm": ([P, P, i32, P, P, ctypes.c_float, i64, i32, P, P, P, P, P], i32),
+        "moe_workspace_size_bwd": ([i32], sz),
+        "moe_add_rmsnorm_bwd": ([P, P, i32, P, ctypes.c_float, i64, i32, P, P, P, P, P, sz, P], i32),
+        "moe_add_layernorm_bwd": ([P, P, i32, P, ctypes.c_float, i64, i32, P, P, P, P, P, P, sz, P], i32),
+        "moe_finalize_bwd": ([P, P, i64, P, P, i64, i32, i32, P, P, P, P, P, P, P, P, P, sz, P], i32),
+        "moe_permute_bwd": ([P, i64, P, P, P, P, i32, P, P, i64, i32, i32, P, P, P, sz, P], i32),
+        "moe_route_bwd": ([P, P, P, P, i64, i32, i32, i32, P, P, sz, P], i32),
         "moe_debug_wait_timeout": ([P, sz, u64, P], i32),
         "moe_set_wait_timeout_ns": ([u64], None),
         "moe_route_noalloc": ([P, P, P, i64, i32, i32, i32, i32, P, P, P], i32),
@@ -549,6 +558,114 @@ def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y, q=None, scale=Non
                               _ptr(q, "q", torch.uint8, (T, H), allow_none=True),
                               _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream))
     _check("moe_add_rmsnorm", st)
+
+
+def moe_add_layernorm(x, residual, weight, bias, eps, residual_out, y, q=None, scale=None, stream=None):
+    """moe_add_rmsnorm with a layer norm: y = bf16((r - mean(r)) / sqrt(var(r) + eps) * weight + bias), bias [H] bf16
+    or None."""
+    T, H = x.shape
+    f32 = residual is not None and residual.dtype is _f32
+    rt = _f32 if f32 else _bf16
+    st = _lib.moe_add_layernorm(_ptr(x, "x", _bf16, (T, H)), _ptr(residual, "residual", rt, (T, H), allow_none=True),
+                                f32, _ptr(weight, "weight", _bf16, (H,)),
+                                _ptr(bias, "bias", _bf16, (H,), allow_none=True), eps, T, H,
+                                _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True),
+                                _ptr(y, "y", _bf16, (T, H), allow_none=True),
+                                _ptr(q, "q", torch.uint8, (T, H), allow_none=True),
+                                _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream))
+    _check("moe_add_layernorm", st)
+
+
+def moe_workspace_size_bwd(H) -> int:
+    """Bytes of workspace the gradient calls need for rows of H values."""
+    n = _lib.moe_workspace_size_bwd(H)
+    if n == 0:
+        raise MoEError("moe_workspace_size_bwd", MOE_ERR_UNSUPPORTED)
+    return int(n)
+
+
+def _norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight):
+    T, H = dy.shape
+    f32 = r.dtype is _f32
+    rt = _f32 if f32 else _bf16
+    return (_ptr(dy, "dy", _bf16, (T, H)), _ptr(r, "r", rt, (T, H)), f32, _ptr(weight, "weight", _bf16, (H,)), eps, T, H,
+            _ptr(dstream, "dstream", rt, (T, H), allow_none=True), _ptr(dr, "dr", rt, (T, H), allow_none=True),
+            _ptr(dx, "dx", _bf16, (T, H), allow_none=True), _ptr(dweight, "dweight", _f32, (H,), allow_none=True))
+
+
+def _ws(ws):
+    return _ptr(ws, "ws", torch.uint8, allow_none=True), 0 if ws is None else ws.numel()
+
+
+def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream=None):
+    """The gradient of moe_add_rmsnorm's y at its stream r (residual_out): dy [T, H] bf16; r [T, H] bf16 or fp32;
+    dstream [T, H] of r's type, the gradient that reaches r past the norm, or None; dr [T, H] of r's type (it may be
+    dstream or r) = dstream + the norm's part; dx the same in bf16 (it may be dy); dweight [H] fp32.  Outputs may be
+    None; ws (moe_workspace_size_bwd) is needed with dweight only."""
+    st = _lib.moe_add_rmsnorm_bwd(*_norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight), *_ws(ws),
+                                  _stream(stream))
+    _check("moe_add_rmsnorm_bwd", st)
+
+
+def moe_add_layernorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, dbias, ws, stream=None):
+    """The gradient of moe_add_layernorm's y at its stream r, arguments as moe_add_rmsnorm_bwd; dbias [H] fp32 or None."""
+    st = _lib.moe_add_layernorm_bwd(*_norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight),
+                                    _ptr(dbias, "dbias", _f32, (weight.shape[0],), allow_none=True), *_ws(ws),
+                                    _stream(stream))
+    _check("moe_add_layernorm_bwd", st)
+
+
+def moe_finalize_bwd(dout, y, pair_row, topk_w, y_shared, x, shared_gate_w, dy, dtopk_w, dy_shared, dgate,
+                     dshared_gate_w, ws, stream=None):
+    """The gradient of moe_finalize: from dout [T, H] to the experts' outputs dy [rows_cap, H] (it may be y; rows that
+    no pair has are left as they were) and the weights dtopk_w [T, k] fp32 (or None: y may then be None too).  With a
+    gated shared expert (y_shared, x [T, H], shared_gate_w [H]) also dy_shared [T, H], the gate's logit dgate [T] fp32
+    and dshared_gate_w [H] fp32 (or None); without one all six are None."""
+    T, H = dout.shape
+    k = pair_row.shape[1]
+    rows_cap = dy.shape[0]
+    wp, wb = _ws(ws)
+    st = _lib.moe_finalize_bwd(
+        _ptr(dout, "dout", _bf16, (T, H)), _ptr(y, "y", _bf16, (rows_cap, H), allow_none=True), rows_cap,
+        _ptr(pair_row, "pair_row", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), T, k, H,
+        _ptr(y_shared, "y_shared", _bf16, (T, H), allow_none=True), _ptr(x, "x", _bf16, (T, H), allow_none=True),
+        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), _ptr(dy, "dy", _bf16, (rows_cap, H)),
+        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True),
+        _ptr(dy_shared, "dy_shared", _bf16, (T, H), allow_none=True), _ptr(dgate, "dgate", _f32, (T,), allow_none=True),
+        _ptr(dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True), wp, wb, _stream(stream))
+    _check("moe_finalize_bwd", st)
+
+
+def moe_permute_bwd(dx_perm, pair_row, topk_w, x, dx_add, dgate, shared_gate_w, dx, dtopk_w, ws, stream=None):
+    """The gradient of moe_permute's rows (topk_w None) or moe_permute_on_input's: dx [T, H] bf16 = dx_add [T, H] (bf16 or
+    fp32, or None) + sum_j topk_w[t,j] dx_perm[pair_row[t,j]] + dgate[t] shared_gate_w (or both None); dtopk_w [T, k]
+    fp32 = x[t] . dx_perm[pair_row[t,j]], or None (x may then be None).  dx may be x or a bf16 dx_add."""
+    T, k = pair_row.shape
+    rows_cap, H = dx_perm.shape
+    f32 = dx_add is not None and dx_add.dtype is _f32
+    wp, wb = _ws(ws)
+    st = _lib.moe_permute_bwd(
+        _ptr(dx_perm, "dx_perm", _bf16, (rows_cap, H)), rows_cap, _ptr(pair_row, "pair_row", _i32, (T, k)),
+        _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), _ptr(x, "x", _bf16, (T, H), allow_none=True),
+        _ptr(dx_add, "dx_add", _f32 if f32 else _bf16, (T, H), allow_none=True), f32,
+        _ptr(dgate, "dgate", _f32, (T,), allow_none=True),
+        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), T, k, H, _ptr(dx, "dx", _bf16, (T, H)),
+        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True), wp, wb, _stream(stream))
+    _check("moe_permute_bwd", st)
+
+
+def moe_route_bwd(topk_ids, topk_w, dtopk_w, logits, renorm, dlogits, ws, stream=None):
+    """The gradient of the routing weights topk_w [T, k] (as moe_route wrote them) with respect to the logits: dlogits
+    [T, E] fp32 from dtopk_w [T, k] fp32.  logits [T, E] fp32 is read without renorm only (else it may be None); dlogits
+    may be logits."""
+    T, k = topk_ids.shape
+    E = dlogits.shape[1]
+    wp, wb = _ws(ws)
+    st = _lib.moe_route_bwd(_ptr(topk_ids, "topk_ids", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k)),
+                            _ptr(dtopk_w, "dtopk_w", _f32, (T, k)),
+                            _ptr(logits, "logits", _f32, (T, E), allow_none=True), T, E, k, int(bool(renorm)),
+                            _ptr(dlogits, "dlogits", _f32, (T, E)), wp, wb, _stream(stream))
+    _check("moe_route_bwd", st)
 
 
 def moe_quantize_w4_rows(w, q, scale, stream=None):

@@ -727,22 +727,150 @@ moe_status_t moe_forward_w8a8_rows(const uint8_t* xq, const float* x_scale, cons
 // longest row the norm takes (a CTA holds one in registers)
 constexpr int kNormMaxH = 16384;
 
+// The arguments of either norm; *run is false where there is nothing to do.
+static moe_status_t norm_args(const NormLaunch& L, int residual_f32, bool* run) {
+    *run = false;
+    if (L.T < 0 || L.H <= 0 || (residual_f32 != 0 && residual_f32 != 1) || !(L.eps >= 0.f && L.eps <= FLT_MAX))
+        return MOE_ERR_INVALID_ARG;
+    if (L.H % 8 != 0 || L.H > kNormMaxH || L.T >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (L.T == 0) return MOE_OK;
+    if (!L.x || !L.weight || (L.residual_out && !L.residual) || (L.q == nullptr) != (L.scale == nullptr) ||
+        (!L.residual_out && !L.y && !L.q))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(L.x, 16) || !aligned(L.residual, 16) || !aligned(L.weight, 16) || !aligned(L.bias, 16) ||
+        !aligned(L.residual_out, 16) || !aligned(L.y, 16) || !aligned(L.q, 8) || !aligned(L.scale, 4))
+        return MOE_ERR_INVALID_ARG;
+    *run = true;
+    return MOE_OK;
+}
+
 moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const void* residual, int residual_f32, const moe_bf16_t* weight,
                              float eps, int64_t T, int H, void* residual_out, moe_bf16_t* y, uint8_t* q, float* scale,
                              moe_stream_t stream) {
     MOE_NVTX("moe_add_rmsnorm");
-    if (T < 0 || H <= 0 || (residual_f32 != 0 && residual_f32 != 1) || !(eps >= 0.f && eps <= FLT_MAX))
-        return MOE_ERR_INVALID_ARG;
-    if (H % 8 != 0 || H > kNormMaxH || T >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
-    if (T == 0) return MOE_OK;
-    if (!x || !weight || (residual_out && !residual) || (q == nullptr) != (scale == nullptr) ||
-        (!residual_out && !y && !q))
-        return MOE_ERR_INVALID_ARG;
-    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(residual_out, 16) ||
-        !aligned(y, 16) || !aligned(q, 8) || !aligned(scale, 4))
-        return MOE_ERR_INVALID_ARG;
     const NormLaunch L = {x, residual, weight, residual_out, y, q, scale, T, H, eps, residual_f32 == 1};
-    return cuda_status(launch_add_rmsnorm(L, device_sms(), (cudaStream_t)stream));
+    bool run;
+    const moe_status_t st = norm_args(L, residual_f32, &run);
+    return run ? cuda_status(launch_add_rmsnorm(L, device_sms(), (cudaStream_t)stream)) : st;
+}
+
+moe_status_t moe_add_layernorm(const moe_bf16_t* x, const void* residual, int residual_f32, const moe_bf16_t* weight,
+                               const moe_bf16_t* bias, float eps, int64_t T, int H, void* residual_out, moe_bf16_t* y,
+                               uint8_t* q, float* scale, moe_stream_t stream) {
+    MOE_NVTX("moe_add_layernorm");
+    const NormLaunch L = {x, residual, weight, residual_out, y, q, scale, T, H, eps, residual_f32 == 1, bias};
+    bool run;
+    const moe_status_t st = norm_args(L, residual_f32, &run);
+    return run ? cuda_status(launch_add_layernorm(L, device_sms(), (cudaStream_t)stream)) : st;
+}
+
+// ---- gradients -----------------------------------------------------------------
+
+static size_t bwd_need(int64_t H) { return kWsHeaderBytes + (size_t)kBwdPartials * 2 * (size_t)H * 4; }
+
+size_t moe_workspace_size_bwd(int H) { return H <= 0 || H % 8 != 0 || H > (1 << 20) ? 0 : bwd_need(H); }
+
+static moe_status_t norm_bwd_call(NormBwdLaunch L, int r_f32, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (L.T < 0 || L.H <= 0 || (r_f32 != 0 && r_f32 != 1) || !(L.eps >= 0.f && L.eps <= FLT_MAX))
+        return MOE_ERR_INVALID_ARG;
+    if (L.H % 8 != 0 || L.H > kNormMaxH || L.T >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (!aligned(L.dweight, 16) || !aligned(L.dbias, 16)) return MOE_ERR_INVALID_ARG;
+    if (L.T == 0) {  // sums over no rows
+        cudaError_t e = L.dweight ? cudaMemsetAsync(L.dweight, 0, (size_t)L.H * 4, s) : cudaSuccess;
+        if (e == cudaSuccess && L.dbias) e = cudaMemsetAsync(L.dbias, 0, (size_t)L.H * 4, s);
+        return cuda_status(e);
+    }
+    if (!L.dy || !L.r || !L.weight || (!L.dr && !L.dx && !L.dweight && !L.dbias)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(L.dy, 16) || !aligned(L.r, 16) || !aligned(L.weight, 16) || !aligned(L.dstream, 16) ||
+        !aligned(L.dr, 16) || !aligned(L.dx, 16) || !aligned(ws, 16))
+        return MOE_ERR_INVALID_ARG;
+    if ((L.dweight || L.dbias) && (!ws || ws_bytes < bwd_need(L.H))) return MOE_ERR_WORKSPACE;
+    if (L.dweight || L.dbias) L.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeaderBytes);
+    return cuda_status(launch_norm_bwd(L, device_sms(), s));
+}
+
+moe_status_t moe_add_rmsnorm_bwd(const moe_bf16_t* dy, const void* r, int r_f32, const moe_bf16_t* weight, float eps,
+                                 int64_t T, int H, const void* dstream, void* dr, moe_bf16_t* dx, float* dweight,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_NVTX("moe_add_rmsnorm_bwd");
+    return norm_bwd_call({dy, r, weight, dstream, dr, dx, dweight, nullptr, nullptr, T, H, eps, r_f32 == 1, false},
+                         r_f32, ws, ws_bytes, stream);
+}
+
+moe_status_t moe_add_layernorm_bwd(const moe_bf16_t* dy, const void* r, int r_f32, const moe_bf16_t* weight, float eps,
+                                   int64_t T, int H, const void* dstream, void* dr, moe_bf16_t* dx, float* dweight,
+                                   float* dbias, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_NVTX("moe_add_layernorm_bwd");
+    return norm_bwd_call({dy, r, weight, dstream, dr, dx, dweight, dbias, nullptr, T, H, eps, r_f32 == 1, true}, r_f32,
+                         ws, ws_bytes, stream);
+}
+
+moe_status_t moe_finalize_bwd(const moe_bf16_t* dout, const moe_bf16_t* y, int64_t rows_cap, const int32_t* pair_row,
+                              const float* topk_w, int64_t T, int k, int H, const moe_bf16_t* y_shared,
+                              const moe_bf16_t* x, const moe_bf16_t* shared_gate_w, moe_bf16_t* dy, float* dtopk_w,
+                              moe_bf16_t* dy_shared, float* dgate, float* dshared_gate_w, void* ws, size_t ws_bytes,
+                              moe_stream_t stream) {
+    MOE_NVTX("moe_finalize_bwd");
+    if (T < 0 || k <= 0 || H <= 0 || rows_cap < 0) return MOE_ERR_INVALID_ARG;
+    if (!dim_ok(H) || k > 32 || T >= (int64_t(1) << 31) / k || rows_cap >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    const bool gated = shared_gate_w != nullptr;
+    if ((!gated && (y_shared || x || dy_shared || dgate || dshared_gate_w)) || (dtopk_w && !topk_w) ||
+        !aligned(dshared_gate_w, 16))
+        return MOE_ERR_INVALID_ARG;
+    if (T == 0)
+        return dshared_gate_w
+                   ? cuda_status(cudaMemsetAsync(dshared_gate_w, 0, (size_t)H * 4, (cudaStream_t)stream)) : MOE_OK;
+    if (!dout || !pair_row || (rows_cap > 0 && (!dy || (dtopk_w && !y))) ||
+        (gated && (!y_shared || !x || !dy_shared || !dgate)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(pair_row, 4) || !aligned(topk_w, 4) || !aligned(y_shared, 16) ||
+        !aligned(x, 16) || !aligned(shared_gate_w, 16) || !aligned(dy, 16) || !aligned(dtopk_w, 4) ||
+        !aligned(dy_shared, 16) || !aligned(dgate, 4) || !aligned(ws, 16))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < (dshared_gate_w ? bwd_need(H) : kWsHeaderBytes)) return MOE_ERR_WORKSPACE;
+    FinalizeBwdLaunch L = {dout, y, rows_cap, pair_row, topk_w, T, k, H, dy, dtopk_w, y_shared, x, shared_gate_w,
+                           dy_shared, dgate, dshared_gate_w};
+    L.part = reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHeaderBytes);
+    L.hdr = static_cast<WsHeader*>(ws);
+    return cuda_status(launch_finalize_bwd(L, device_sms(), (cudaStream_t)stream));
+}
+
+moe_status_t moe_permute_bwd(const moe_bf16_t* dx_perm, int64_t rows_cap, const int32_t* pair_row, const float* topk_w,
+                             const moe_bf16_t* x, const void* dx_add, int dx_add_f32, const float* dgate,
+                             const moe_bf16_t* shared_gate_w, int64_t T, int k, int H, moe_bf16_t* dx, float* dtopk_w,
+                             void* ws, size_t ws_bytes, moe_stream_t stream) {
+    MOE_NVTX("moe_permute_bwd");
+    if (T < 0 || k <= 0 || H <= 0 || rows_cap < 0 || (dx_add_f32 != 0 && dx_add_f32 != 1)) return MOE_ERR_INVALID_ARG;
+    if (!dim_ok(H) || k > 32 || T >= (int64_t(1) << 31) / k || rows_cap >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if ((rows_cap > 0 && !dx_perm) || !pair_row || !dx || (dgate == nullptr) != (shared_gate_w == nullptr) ||
+        (dtopk_w && (!topk_w || !x)))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(dx_perm, 16) || !aligned(pair_row, 4) || !aligned(topk_w, 4) || !aligned(x, 16) || !aligned(dx_add, 16) ||
+        !aligned(dgate, 4) || !aligned(shared_gate_w, 16) || !aligned(dx, 16) || !aligned(dtopk_w, 4) || !aligned(ws, 16))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < kWsHeaderBytes) return MOE_ERR_WORKSPACE;
+    const PermuteBwdLaunch L = {dx_perm, rows_cap, pair_row, topk_w, x, dx_add, dx_add_f32 == 1, dgate, shared_gate_w,
+                                T, k, H, dx, dtopk_w, static_cast<WsHeader*>(ws)};
+    return cuda_status(launch_permute_bwd(L, device_sms(), (cudaStream_t)stream));
+}
+
+moe_status_t moe_route_bwd(const int32_t* topk_ids, const float* topk_w, const float* dtopk_w, const float* logits,
+                           int64_t T, int E, int k, int renorm, float* dlogits, void* ws, size_t ws_bytes,
+                           moe_stream_t stream) {
+    MOE_NVTX("moe_route_bwd");
+    if (T < 0 || E <= 0 || k <= 0 || k > E || (renorm != 0 && renorm != 1)) return MOE_ERR_INVALID_ARG;
+    if (k > 32 || E > 512 || T >= (int64_t(1) << 31) / k) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!topk_ids || !topk_w || !dtopk_w || !dlogits || (!renorm && !logits)) return MOE_ERR_INVALID_ARG;
+    if (!aligned(topk_ids, 4) || !aligned(topk_w, 4) || !aligned(dtopk_w, 4) || !aligned(logits, 16) ||
+        !aligned(dlogits, 16) || !aligned(ws, 16))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < kWsHeaderBytes) return MOE_ERR_WORKSPACE;
+    const RouteBwdLaunch L = {topk_ids, topk_w, dtopk_w, renorm ? nullptr : logits, T, E, k, dlogits,
+                              static_cast<WsHeader*>(ws)};
+    return cuda_status(launch_route_bwd(L, device_sms(), (cudaStream_t)stream));
 }
 
 static bool w4_group_ok(int K, int group) { return (group == 32 || group == 64 || group == 128) && K % group == 0; }

@@ -61,6 +61,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint4 pack8(const float f[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
+
 // ---------------------------------------------------------------------------
 // Time and bounded waits
 // ---------------------------------------------------------------------------
@@ -604,7 +609,7 @@ struct PlaceRowsLaunch {
 };
 cudaError_t launch_place_rows(const PlaceRowsLaunch& L, int num_sms, cudaStream_t s);
 
-// The residual's addition, the norm and its E4M3 rows (moe_add_rmsnorm).
+// The residual's addition, the norm and its E4M3 rows (moe_add_rmsnorm, moe_add_layernorm).
 struct NormLaunch {
     const uint16_t* x;        // [T, H] bf16
     const void* residual;     // [T, H] bf16 or (f32) fp32, or null
@@ -617,8 +622,89 @@ struct NormLaunch {
     int H;
     float eps;
     bool f32;
+    const uint16_t* bias = nullptr;  // [H] bf16, or null (layer norm only)
 };
 cudaError_t launch_add_rmsnorm(const NormLaunch& L, int num_sms, cudaStream_t s);
+cudaError_t launch_add_layernorm(const NormLaunch& L, int num_sms, cudaStream_t s);
+
+// The gradients of the two norms (moe_add_rmsnorm_bwd, moe_add_layernorm_bwd).
+struct NormBwdLaunch {
+    const uint16_t* dy;       // [T, H] bf16
+    const void* r;            // [T, H] bf16 or (f32) fp32
+    const uint16_t* weight;   // [H] bf16
+    const void* dstream;      // of r's type, or null
+    void* dr;                 // of r's type, or null
+    uint16_t* dx;             // [T, H] bf16, or null
+    float* dweight;           // [H], or null
+    float* dbias;             // [H], or null (layer norm only)
+    float* part;              // [kBwdPartials][2][H] scratch
+    int64_t T;
+    int H;
+    float eps;
+    bool f32, ln;
+};
+// rows of partial column sums that a workspace holds (moe_workspace_size_bwd)
+constexpr int kBwdPartials = 304;
+cudaError_t launch_norm_bwd(const NormBwdLaunch& L, int num_sms, cudaStream_t s);
+// out0[h] = sum over i of part[i * stride + h], out1[h] of part[i * stride + H + h] (or null), i = 0 .. n-1
+// in a fixed order
+cudaError_t launch_sum_partials(const float* part, int n, int64_t stride, int H, float* out0, float* out1,
+                                cudaStream_t s);
+
+// The gradient of the weighted combine (moe_finalize_bwd).
+struct FinalizeBwdLaunch {
+    const uint16_t* dout;     // [T, H]
+    const uint16_t* y;        // [rows_cap, H], with dw
+    int64_t rows_cap;
+    const int32_t* pair_row;  // [T, k]
+    const float* w;           // [T, k], or null: 1
+    int64_t T;
+    int k, H;
+    uint16_t* dy;             // [rows_cap, H]
+    float* dw;                // [T, k], or null
+    // the gated shared expert, or all null
+    const uint16_t* y_sh;     // [T, H]
+    const uint16_t* x;        // [T, H]
+    const uint16_t* gate_w;   // [H]
+    uint16_t* dy_sh;          // [T, H]
+    float* dgate;             // [T] gradient of the gate's logit
+    float* dgate_w;           // [H], or null
+    float* part;              // [kBwdPartials][H] scratch, with dgate_w
+    WsHeader* hdr;
+};
+cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& L, int num_sms, cudaStream_t s);
+
+// The gradient of the sorted (and weighted) rows (moe_permute_bwd).
+struct PermuteBwdLaunch {
+    const uint16_t* dx_perm;  // [rows_cap, H]
+    int64_t rows_cap;
+    const int32_t* pair_row;  // [T, k]
+    const float* w;           // [T, k], or null: 1
+    const uint16_t* x;        // [T, H], with dw
+    const void* add;          // [T, H] bf16 or (add_f32) fp32, or null
+    bool add_f32;
+    const float* dgate;       // [T] and gate_w [H], or null
+    const uint16_t* gate_w;
+    int64_t T;
+    int k, H;
+    uint16_t* dx;             // [T, H]
+    float* dw;                // [T, k], or null
+    WsHeader* hdr;
+};
+cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStream_t s);
+
+// The gradient of softmax, top-k and renormalisation (moe_route_bwd).
+struct RouteBwdLaunch {
+    const int32_t* ids;       // [T, k]
+    const float* w;           // [T, k]
+    const float* dw;          // [T, k]
+    const float* logits;      // [T, E], or null: renormalised
+    int64_t T;
+    int E, k;
+    float* dlogits;           // [T, E]
+    WsHeader* hdr;
+};
+cudaError_t launch_route_bwd(const RouteBwdLaunch& L, int num_sms, cudaStream_t s);
 
 // Products with 4-bit weights (moe_matvec_w4, moe_forward_w4): one problem has A rows
 // x [., K] and packed weights of 2 N_out (SwiGLU: gate, then up) or N_out rows per slot.

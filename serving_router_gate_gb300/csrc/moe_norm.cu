@@ -49,11 +49,6 @@ __device__ __forceinline__ void nm_load_res(const void* res, int64_t off, float 
     }
 }
 
-__device__ __forceinline__ uint4 nm_pack8(const float f[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
-
 // Smallest e >= -126 with amax <= 448 * 2^e (448 = 1.75 * 2^8), from the binary32 fields.
 __device__ __forceinline__ int nm_exponent(float amax) {
     const uint32_t b = __float_as_uint(amax);
@@ -67,12 +62,27 @@ __device__ __forceinline__ uint32_t nm_e4m3x4(const float* f, float inv) {
     return lo | (hi << 16);
 }
 
+// Sum of v over a row's WARPS warps (red: one word each), the same in every thread.
+template <int WARPS>
+__device__ __forceinline__ float nm_row_sum(float v, float* red) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (WARPS == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float tot = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) tot += red[w];
+    return tot;
+}
+
 // THREADS threads per row at a time, each with VPT vectors of 8 values (grid-stride over
 // rows): a CTA, or (THREADS = 32) each of its NM_WARPS warps by itself.
-template <int VPT, int THREADS, bool F32>
-__global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rmsnorm_kernel(const __grid_constant__ NormLaunch a) {
+template <int VPT, int THREADS, bool F32, bool LN>
+__global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_norm_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ float red_sum[2][WARPS];
+    __shared__ float red_mean[2][LN ? WARPS : 1];
     __shared__ uint32_t red_max[2][WARPS];
     constexpr bool ALONE = THREADS == 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -98,18 +108,20 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rm
                 for (int i = 0; i < 8; ++i) f[j][i] += r[i];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i], f[j][i], ss);
+            for (int i = 0; i < 8; ++i) ss = LN ? ss + f[j][i] : fmaf(f[j][i], f[j][i], ss);
         }
+        float mean = 0.f;
+        if (LN) {
+            mean = nm_row_sum<WARPS>(ss, red_mean[it]) / (float)a.H;
+            ss = 0.f;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-        float tot = ss;
-        if (!ALONE) {
-            if (lane == 0) red_sum[it][warp] = ss;
-            __syncthreads();
-            tot = 0.f;
+            for (int j = 0; j < VPT; ++j) {
+                if (first + j * THREADS >= vec) continue;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) tot += red_sum[it][w];
+                for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i] - mean, f[j][i] - mean, ss);
+            }
         }
+        const float tot = nm_row_sum<WARPS>(ss, red_sum[it]);
         // the root's reciprocal in two words: its own rounding, which would move a whole row of
         // y by up to 2^-24, is taken out.  ms stays one binary32 value: the roundings of the
         // sum, of the division and of eps move the row by half of theirs
@@ -129,17 +141,21 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rm
                     p[0] = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
                     p[1] = make_float4(f[j][4], f[j][5], f[j][6], f[j][7]);
                 } else {
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + base + 8 * v) = nm_pack8(f[j]);
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + base + 8 * v) = pack8(f[j]);
                 }
             }
             float w[8];
             nm_load8(a.weight + 8 * v, w);
+            float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (LN && a.bias) nm_load8(a.bias + 8 * v, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                f[j][i] = fmaf(f[j][i], hi, f[j][i] * lo) * w[i];
+                const float d = LN ? f[j][i] - mean : f[j][i];
+                f[j][i] = fmaf(d, hi, d * lo) * w[i];
+                if (LN) f[j][i] += b[i];
                 mx = max(mx, __float_as_uint(f[j][i]) & 0x7FFFFFFFu);
             }
-            if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = nm_pack8(f[j]);
+            if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = pack8(f[j]);
         }
         if (!a.q) continue;
         mx = __reduce_max_sync(0xffffffffu, mx);
@@ -162,14 +178,14 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rm
     }
 }
 
-template <int VPT, int THREADS, bool F32>
+template <int VPT, int THREADS, bool F32, bool LN>
 cudaError_t launch_norm_size(const NormLaunch& L, int num_sms, cudaStream_t s) {
     constexpr int ROWS = THREADS == 32 ? NM_WARPS : 1;
     const unsigned grid = (unsigned)std::min<int64_t>((L.T + ROWS - 1) / ROWS, (int64_t)num_sms * NM_CTAS);
-    return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, THREADS, F32>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
+    return launch_k(LN ? "add_layernorm" : "add_rmsnorm", add_norm_kernel<VPT, THREADS, F32, LN>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
 }
 
-template <bool F32>
+template <bool F32, bool LN>
 cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // A warp to a row while its lanes hold it in two vectors each, then one vector a thread
     // to 2048 values, and a CTA of 224 or 256 threads with four: at 7168 values (16384 rows
@@ -178,20 +194,24 @@ cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // widths of these forms run at (16384 rows, of the copy rate): 4096 0.99, 5120 (a vector of
     // four idle) 0.90, 6144 0.90, and at 1.06 GB 8192 0.91, 16384 0.84.
     const int vec = L.H / 8;
-    if (vec <= 32) return launch_norm_size<1, 32, F32>(L, num_sms, s);
-    if (vec <= 64) return launch_norm_size<2, 32, F32>(L, num_sms, s);
-    if (vec <= 128) return launch_norm_size<1, 128, F32>(L, num_sms, s);
-    if (vec <= 256) return launch_norm_size<1, 256, F32>(L, num_sms, s);
-    if (vec <= 512) return launch_norm_size<2, 256, F32>(L, num_sms, s);
-    if (vec <= 896) return launch_norm_size<4, 224, F32>(L, num_sms, s);
-    if (vec <= 1024) return launch_norm_size<4, 256, F32>(L, num_sms, s);
-    return launch_norm_size<4, 512, F32>(L, num_sms, s);
+    if (vec <= 32) return launch_norm_size<1, 32, F32, LN>(L, num_sms, s);
+    if (vec <= 64) return launch_norm_size<2, 32, F32, LN>(L, num_sms, s);
+    if (vec <= 128) return launch_norm_size<1, 128, F32, LN>(L, num_sms, s);
+    if (vec <= 256) return launch_norm_size<1, 256, F32, LN>(L, num_sms, s);
+    if (vec <= 512) return launch_norm_size<2, 256, F32, LN>(L, num_sms, s);
+    if (vec <= 896) return launch_norm_size<4, 224, F32, LN>(L, num_sms, s);
+    if (vec <= 1024) return launch_norm_size<4, 256, F32, LN>(L, num_sms, s);
+    return launch_norm_size<4, 512, F32, LN>(L, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const NormLaunch& L, int num_sms, cudaStream_t s) {
-    return L.f32 ? launch_norm_type<true>(L, num_sms, s) : launch_norm_type<false>(L, num_sms, s);
+    return L.f32 ? launch_norm_type<true, false>(L, num_sms, s) : launch_norm_type<false, false>(L, num_sms, s);
+}
+
+cudaError_t launch_add_layernorm(const NormLaunch& L, int num_sms, cudaStream_t s) {
+    return L.f32 ? launch_norm_type<true, true>(L, num_sms, s) : launch_norm_type<false, true>(L, num_sms, s);
 }
 
 }  // namespace moe
