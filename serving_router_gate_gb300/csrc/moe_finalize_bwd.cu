@@ -112,57 +112,126 @@ __global__ void __launch_bounds__(FB_WARPS * 32) gate_weight_kernel(const float*
     o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
 }
 
-// A warp to a token; up to 8 pairs' dots at a time.
-__global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a) {
+// A token's row is spread over `split` of a CTA's warps (1, 2, 4 or 8).  A warp first lists
+// its token's pairs that have a row, then takes two vectors of 8 values a lane at a time,
+// PB_BATCH pairs' rows of both in flight before they are used.  MAXK: k at most; DW: with
+// the weights' gradients, a lane's share of every pair's dot product stays in a register.
+constexpr int PB_BATCH = 4;
+
+template <int MAXK, bool DW>
+__global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a,
+                                                                  int split) {
+    __shared__ int32_t s_row[FB_WARPS][MAXK], s_pair[FB_WARPS][MAXK];
+    __shared__ float s_w[FB_WARPS][MAXK], s_dot[FB_WARPS][DW ? MAXK : 1];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
-    for (int64_t t = (int64_t)blockIdx.x * FB_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * FB_WARPS) {
-        int32_t my_row = -1;
-        float my_w = 1.f, my_dot = 0.f;
-        if (lane < a.k) {
-            my_row = pair_row_of(a.pair_row, t * a.k + lane, a.rows_cap, &a.hdr->status);
-            if (a.w) my_w = a.w[t * a.k + lane];
+    const int part = warp & (split - 1), tokens = FB_WARPS / split;
+    for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
+        const int64_t t = t0 + warp / split;
+        const bool live_t = t < a.T;
+        int32_t row = -1;
+        float w = 1.f;
+        if (live_t && lane < a.k) {
+            row = pair_row_of(a.pair_row, t * a.k + lane, a.rows_cap, part == 0 ? &a.hdr->status : nullptr);
+            if (a.w) w = a.w[t * a.k + lane];
         }
-        const float dz = a.dgate ? a.dgate[t] : 0.f;
-        for (int v0 = 0; v0 < vec; v0 += 32) {
-            const int v = v0 + lane;
-            const bool in = v < vec;
-            float x[8] = {}, acc[8] = {};
-            if (in && a.dw) unpack8(reinterpret_cast<const uint4*>(a.x + t * a.H)[v], x);
-            if (in && a.add) {
-                if (a.add_f32) {
-                    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.add) + t * a.H) + 2 * v;
-                    const float4 lo = p[0], hi = p[1];
-                    acc[0] = lo.x; acc[1] = lo.y; acc[2] = lo.z; acc[3] = lo.w;
-                    acc[4] = hi.x; acc[5] = hi.y; acc[6] = hi.z; acc[7] = hi.w;
-                } else {
-                    unpack8(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.add) + t * a.H)[v], acc);
-                }
-            }
-            for (int j = 0; j < a.k; ++j) {
-                const int32_t r = __shfl_sync(0xffffffffu, my_row, j);
-                const float w = __shfl_sync(0xffffffffu, my_w, j);
-                if (r < 0) continue;
-                float d[8] = {}, dot = 0.f;
-                if (in) unpack8(reinterpret_cast<const uint4*>(a.dx_perm + (int64_t)r * a.H)[v], d);
-                for (int i = 0; i < 8; ++i) {
-                    acc[i] = fmaf(w, d[i], acc[i]);
-                    dot = fmaf(x[i], d[i], dot);
-                }
-                if (a.dw) {
-                    dot = warp_sum(dot);
-                    if (lane == j) my_dot += dot;
-                }
-            }
-            if (in && a.dgate) {
-                float g[8];
-                unpack8(reinterpret_cast<const uint4*>(a.gate_w)[v], g);
-                for (int i = 0; i < 8; ++i) acc[i] = fmaf(dz, g[i], acc[i]);
-            }
-            if (in) reinterpret_cast<uint4*>(a.dx + t * a.H)[v] = pack8(acc);
+        const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+        const int n = __popc(live);
+        __syncwarp();
+        if (row >= 0) {
+            const int i = __popc(live & ((1u << lane) - 1));
+            s_row[warp][i] = row;
+            s_w[warp][i] = w;
+            s_pair[warp][i] = lane;
         }
-        if (a.dw && lane < a.k) a.dw[t * a.k + lane] = my_dot;
+        __syncwarp();
+        float dot[DW ? MAXK : 1] = {};
+        const float dz = live_t && a.dgate ? a.dgate[t] : 0.f;
+        const int last = live_t ? vec : 0;
+        for (int v0 = part * 64 + lane; v0 < last; v0 += split * 64) {
+            const bool two = v0 + 32 < vec;
+            const int64_t at = t * a.H + 8 * v0;
+            uint4 xp[2];
+            float acc[2][8] = {};
+            if (DW) {
+                xp[0] = *reinterpret_cast<const uint4*>(a.x + at);  // not __ldg: dx may be x
+                xp[1] = two ? reinterpret_cast<const uint4*>(a.x + at)[32] : make_uint4(0, 0, 0, 0);
+            }
+            if (a.add) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u && !two) continue;
+                    if (a.add_f32) {
+                        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.add) + at + 256 * u);
+                        const float4 lo = q[0], hi = q[1];
+                        acc[u][0] = lo.x; acc[u][1] = lo.y; acc[u][2] = lo.z; acc[u][3] = lo.w;
+                        acc[u][4] = hi.x; acc[u][5] = hi.y; acc[u][6] = hi.z; acc[u][7] = hi.w;
+                    } else {
+                        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.add) + at + 256 * u), acc[u]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int j0 = 0; j0 < MAXK; j0 += PB_BATCH) {
+                if (j0 >= n) break;
+                uint4 ld[PB_BATCH][2];
+#pragma unroll
+                for (int b = 0; b < PB_BATCH; ++b) {
+                    const bool ok = j0 + b < n;
+                    const uint4* q = reinterpret_cast<const uint4*>(a.dx_perm + (ok ? (int64_t)s_row[warp][j0 + b] * a.H : 0)) + v0;
+                    ld[b][0] = ok ? __ldg(q) : make_uint4(0, 0, 0, 0);
+                    ld[b][1] = ok && two ? __ldg(q + 32) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int b = 0; b < PB_BATCH; ++b) {
+                    if (j0 + b >= n) continue;
+                    const float wj = s_w[warp][j0 + b];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float d[8], x[8];
+                        unpack8(ld[b][u], d);
+                        if (DW) unpack8(xp[u], x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            acc[u][i] = fmaf(wj, d[i], acc[u][i]);
+                            if (DW) dot[j0 + b] = fmaf(x[i], d[i], dot[j0 + b]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                if (u && !two) continue;
+                if (a.dgate) {
+                    float g[8];
+                    unpack8(__ldg(reinterpret_cast<const uint4*>(a.gate_w) + v0 + 32 * u), g);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) acc[u][i] = fmaf(dz, g[i], acc[u][i]);
+                }
+                reinterpret_cast<uint4*>(a.dx + at)[32 * u] = pack8(acc[u]);
+            }
+        }
+        if (DW) {
+            float mine = 0.f;
+#pragma unroll
+            for (int j = 0; j < MAXK; ++j) {
+                if (j >= n) break;
+                const float d = warp_sum(dot[j]);
+                if (lane == j) mine = d;
+            }
+            if (split > 1) {
+                if (lane < n) s_dot[warp][lane] = mine;
+                __syncthreads();
+                if (part == 0 && lane < n)
+                    for (int q = 1; q < split; ++q) mine += s_dot[warp + q][lane];
+            }
+            if (part == 0 && live_t) {
+                if (lane < n) a.dw[t * a.k + s_pair[warp][lane]] = mine;
+                if (lane < a.k && row < 0) a.dw[t * a.k + lane] = 0.f;
+            }
+            if (split > 1) __syncthreads();  // the next token's dots
+        }
     }
 }
 
@@ -181,8 +250,14 @@ cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& L, int num_sms, cudaStr
 }
 
 cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((L.T + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
-    return launch_k("permute_bwd", permute_bwd_kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L);
+    // a row over as many warps as still leave two CTAs an SM
+    int split = 1;
+    while (split < FB_WARPS && L.T * split < 2LL * num_sms * FB_WARPS) split *= 2;
+    const int tokens = FB_WARPS / split;
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T + tokens - 1) / tokens, (int64_t)num_sms * 64);
+    const auto kernel = L.k <= 8 ? (L.dw ? permute_bwd_kernel<8, true> : permute_bwd_kernel<8, false>)
+                                 : (L.dw ? permute_bwd_kernel<32, true> : permute_bwd_kernel<32, false>);
+    return launch_k("permute_bwd", kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L, split);
 }
 
 }  // namespace moe
