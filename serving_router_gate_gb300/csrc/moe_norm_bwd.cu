@@ -8,13 +8,16 @@
 // The row's statistics are taken again from r: the row has to be read for d anyway.  All
 // sums are binary32; dr is rounded once for each of its outputs.
 //
-// Bound: HBM (8 bytes and about 20 operations an element with a bf16 stream).  A row
-// belongs to a group of warps, each thread to the same columns of every row of its group,
-// so the weight's sums stay in registers to the end of a persistent grid; a CTA's groups
-// then add theirs in order, and a second kernel adds the CTAs'.  A thread copies its own
-// columns of the rows to come into shared memory (cp.async): the copies need no barrier,
-// and a row's one barrier (the layer norm's two: the mean comes first, so that a row far
-// from zero keeps its variance) joins its warps' sums.
+// Bound: HBM (8 bytes an element with a bf16 stream) and not far behind it the issue rate:
+// the two passes over a row take about 14 instructions an element, half of them conversions,
+// so the arithmetic is done on pairs (f32x2), the weight lies in shared memory in binary32,
+// and every address of a row is a base and a constant.  A row belongs to a group of warps,
+// each thread to the same columns of every row of its group, so the weight's sums stay in
+// registers to the end of a persistent grid; a CTA's groups then add theirs in order, and a
+// second kernel adds the CTAs'.  A thread copies its own columns of the rows to come into
+// shared memory (cp.async): the copies need no barrier, and a row's one barrier (the layer
+// norm's two: the mean comes first, so that a row far from zero keeps its variance) joins its
+// warps' sums.
 #include <algorithm>
 
 #include "moe_internal.cuh"
@@ -22,13 +25,12 @@
 namespace moe {
 namespace {
 
-constexpr int NB_WARPS = 16;           // warps of a CTA at most
-constexpr int NB_THREADS = NB_WARPS * 32;
-constexpr int NB_STAGES = 4;           // rows in flight per group at most
-constexpr int NB_SMEM = 227 * 1024;    // of an SM, less 1 KB a CTA
+constexpr int NB_WARPS = 16;           // warps of a CTA at most, one CTA an SM
+constexpr int NB_SMEM = 227 * 1024 - 1024;  // of a CTA, less the static arrays
+constexpr int NB_F32_ROWS = 48 * 1024; // of an fp32 stream's rows, one for each of a CTA's groups
 
 struct NormBwdPlan {
-    int gw, groups, stages;  // warps of a group, groups of a CTA, ring slots
+    int gw, groups, slots;   // warps of a group, groups of a CTA, rows that a group's ring holds
     bool ds_ring;            // dstream goes through the ring
 };
 
@@ -40,272 +42,359 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void cp_async_wait_upto(int n) {  // n uniform, below NB_STAGES
+
+__device__ __forceinline__ void cp_async_wait_upto(int n) {  // n uniform, below 3
     if (n == 0) cp_async_wait<0>();
     else if (n == 1) cp_async_wait<1>();
-    else if (n == 2) cp_async_wait<2>();
-    else cp_async_wait<3>();
+    else cp_async_wait<2>();
 }
 
-template <bool F32>
-__device__ __forceinline__ void nb_store(void* p, int64_t off, const float f[8]) {
-    if (F32) {
-        float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + off);
-        q[0] = make_float4(f[0], f[1], f[2], f[3]);
-        q[1] = make_float4(f[4], f[5], f[6], f[7]);
+// Pairs of binary32 values.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_split(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    float lo, hi;
+    f2_split(v, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ f2 f2_bf16(uint32_t w) {
+    return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// C values: a piece of a bf16 row (C = 8: 16 bytes, C = 4: 8 bytes) or of an fp32 one (C = 4).
+template <int C>
+__device__ __forceinline__ void nb_bf16(const void* p, f2 f[C / 2]) {
+    if (C == 8) {
+        const uint4 v = *static_cast<const uint4*>(p);
+        f[0] = f2_bf16(v.x); f[1] = f2_bf16(v.y); f[C / 2 - 2] = f2_bf16(v.z); f[C / 2 - 1] = f2_bf16(v.w);
     } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + off) = pack8(f);
+        const uint2 v = *static_cast<const uint2*>(p);
+        f[0] = f2_bf16(v.x); f[1] = f2_bf16(v.y);
     }
 }
-
+__device__ __forceinline__ void nb_f32(const void* p, f2 f[2]) {
+    const uint4 v = *static_cast<const uint4*>(p);
+    f[0] = f2_make(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
+}
 template <bool F32>
-__device__ __forceinline__ void nb_load(const void* p, int64_t off, float f[8]) {
-    if (F32) {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + off);
-        const float4 a = q[0], b = q[1];
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-    } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + off), f);
+__device__ __forceinline__ void nb_stream(const void* p, f2 f[F32 ? 2 : 4]) {
+    if (F32) nb_f32(p, f);
+    else nb_bf16<8>(p, f);
+}
+template <int C>
+__device__ __forceinline__ void nb_put_bf16(void* p, const f2 f[C / 2]) {
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) {
+        float lo, hi;
+        f2_split(f[i], lo, hi);
+        w[i] = pack_bf16x2(lo, hi);
     }
+    if (C == 8) *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[C / 2 - 2], w[C / 2 - 1]);
+    else *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void nb_put_f32(void* p, const f2 f[2]) {
+    float v[4];
+    f2_split(f[0], v[0], v[1]);
+    f2_split(f[1], v[2], v[3]);
+    *static_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// 8 values of slot[0], or (F32) of slot[0] and slot[n]: a thread's pieces lie n apart.
-template <bool F32>
-__device__ __forceinline__ void nb_slot(const uint4* slot, int n, float f[8]) {
-    const uint4 a = slot[0];
-    if (F32) {
-        const uint4 b = slot[n];
-        f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-        f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-    } else {
-        unpack8(a, f);
-    }
-}
-
-__device__ __forceinline__ float nb_xor_add(float v, int from) {
-    for (int off = from; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+__device__ __forceinline__ float nb_warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
 }
 
-// The warp's sum of a in lanes 0..15 and of b in lanes 16..31.
-__device__ __forceinline__ float nb_sum2(float a, float b, int lane) {
-    const bool hi = lane & 16;
-    const float got = __shfl_xor_sync(0xffffffffu, hi ? a : b, 16);
-    return nb_xor_add((hi ? b : a) + got, 8);
+// Sums of N values (a power of two) over 32 lanes, or (HALF) over lanes 0..15 and over 16..31:
+// half of the values go to the other half of the lanes until one is left, so lane l ends with
+// the sum of v[l / (lanes / N)].
+template <int N, bool HALF>
+__device__ __forceinline__ float nb_sums(float (&v)[N], int lane) {
+    int off = HALF ? 8 : 16;
+#pragma unroll
+    for (int n = N / 2; n > 0; n /= 2, off /= 2) {
+        const bool hi = lane & off;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+    }
+#pragma unroll
+    for (int o = (HALF ? 8 : 16) / N; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    return v[0];
 }
 
-// VPT vectors of 8 columns a thread.
-template <int VPT, bool F32, bool LN>
-__global__ void __launch_bounds__(NB_THREADS, VPT <= 2 ? 2 : 1)
+// The group's sums of N values, the same in every thread.  red: N floats a warp of the CTA.
+template <int N, typename Sync>
+__device__ __forceinline__ void nb_group_sums(float (&v)[N], float* red, int gw, int group, int warp, int lane,
+                                              const Sync& sync) {
+    float mine = nb_sums<N, false>(v, lane);
+    if (gw == 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / N));
+        return;
+    }
+    if (lane % (32 / N) == 0) red[warp * N + lane / (32 / N)] = mine;
+    sync();
+    const int w = lane & 15;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = w < gw ? red[(group * gw + w) * N + i] : 0.f;
+    mine = nb_sums<N, true>(v, lane);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (16 / N));
+}
+
+// NP pieces a thread: 8 columns of a bf16 stream, or 4 of an fp32 one (16 bytes either way, so
+// that a warp's copies and stores cover whole lines).  A warp's pieces lie side by side.
+template <int NP, bool F32, bool LN>
+__global__ void __launch_bounds__(NB_WARPS * 32, 1)
     norm_bwd_kernel(const __grid_constant__ NormBwdLaunch a, const __grid_constant__ NormBwdPlan p) {
-    extern __shared__ uint4 ring[];
-    __shared__ float4 red[2][NB_WARPS];
-    __shared__ float red_sum[2][NB_WARPS];
-    constexpr int RP = F32 ? 2 : 1;  // 16-byte pieces of a vector of r
-    const int nthr = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int gthr = p.gw * 32, group = warp / p.gw, col = tid - group * gthr, vec = a.H / 8;
-    const int pieces = VPT * (1 + RP + (p.ds_ring ? RP : 0));  // a stage's, of every thread
+    extern __shared__ uint4 smem[];  // [gw * NP pieces] weight, then [warp][slot] r, dy, dstream
+    constexpr int C = F32 ? 4 : 8, P = C / 2, SB = F32 ? 4 : 2;  // columns, pairs of a piece; bytes of a stream value
+    constexpr int NS = LN ? 4 : 2;                               // a row's sums: d^2, g d (and g)
+    constexpr int DY = NP * 512, DS = DY + NP * 64 * C;          // a slot's dy and dstream
+    __shared__ float red[2][NB_WARPS * NS];
+    __shared__ float red_mean[2][NB_WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = warp / p.gw, gwarp = warp - group * p.gw;
+    const int slot_bytes = DS + (p.ds_ring ? NP * 512 : 0);
+    const int col = (gwarp * NP * 32 + lane) * C;                // of piece 0; piece k: + k * 32 * C
+    uint32_t valid = 0;
+#pragma unroll
+    for (int k = 0; k < NP; ++k) valid |= (uint32_t)(col + k * 32 * C < a.H) << k;
+    // dy is copied 8 columns a lane whatever a piece holds: with an fp32 stream a lane uses what
+    // others copied, which the warp's barriers below are for
+    constexpr int DYC = NP * C / 8;
+    const int dy_col = gwarp * NP * 32 * C + lane * 8;
+    uint32_t dy_valid = 0;
+#pragma unroll
+    for (int k = 0; k < DYC; ++k) dy_valid |= (uint32_t)(dy_col + k * 256 < a.H) << k;
     const float inv_h = 1.f / (float)a.H;
     const int64_t stride = (int64_t)gridDim.x * p.groups;
     const int64_t first = (int64_t)group * gridDim.x + blockIdx.x;
-    float dw[VPT][8] = {}, db[LN ? VPT : 1][8] = {};
+    const auto group_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.gw * 32) : "memory"); };
+    char* const weights = reinterpret_cast<char*>(smem) + (gwarp * NP * P * 16 + lane) * 16;
+    char* const ring = reinterpret_cast<char*>(smem) + p.gw * NP * 128 * C + warp * p.slots * slot_bytes;
+
+    f2 dw[NP][P] = {}, db[LN ? NP : 1][P] = {};
     pdl_wait();
     pdl_trigger();
-    const auto fetch = [&](int64_t row, int stage) {
+    const auto fetch = [&](int64_t row, int at) {
         if (row < a.T) {
-            const uint32_t s = smem_u32(ring + (size_t)stage * pieces * nthr + tid);
+            const uint32_t s = smem_u32(ring) + at;
+            const char* r = static_cast<const char*>(a.r) + (row * a.H + col) * SB;
+            const char* dy = reinterpret_cast<const char*>(a.dy + row * a.H + dy_col);
+            const char* ds = static_cast<const char*>(a.dstream) + (row * a.H + col) * SB;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int v = col + j * gthr;
-                if (v >= vec) continue;
-                const int64_t off = row * a.H + 8 * v;
-                cp_async16(s + (j * nthr) * 16, a.dy + off);
-#pragma unroll
-                for (int i = 0; i < RP; ++i) {
-                    cp_async16(s + ((VPT + RP * j + i) * nthr) * 16,
-                               static_cast<const char*>(a.r) + off * (F32 ? 4 : 2) + 16 * i);
-                    if (p.ds_ring)
-                        cp_async16(s + ((VPT + RP * (VPT + j) + i) * nthr) * 16,
-                                   static_cast<const char*>(a.dstream) + off * (F32 ? 4 : 2) + 16 * i);
-                }
+            for (int k = 0; k < NP; ++k) {
+                if (!(valid >> k & 1)) continue;
+                cp_async16(s + lane * 16 + k * 512, r + k * 512);
+                if (p.ds_ring) cp_async16(s + lane * 16 + DS + k * 512, ds + k * 512);
             }
+#pragma unroll
+            for (int k = 0; k < DYC; ++k)
+                if (dy_valid >> k & 1) cp_async16(s + lane * 16 + DY + k * 512, dy + k * 512);
         }
         cp_async_commit();
     };
-    const auto group_sync = [&] {
-        if (p.gw == 1) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(gthr) : "memory");
+    for (int s = 0; s < p.slots; ++s) fetch(first + s * stride, s * slot_bytes);
+    // the weight in binary32, once a CTA
+    if (group == 0) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            f2 w[P] = {};
+            if (valid >> k & 1) nb_bf16<C>(a.weight + col + k * 32 * C, w);
+#pragma unroll
+            for (int i = 0; i < P / 2; ++i) nb_put_f32(weights + (k * (P / 2) + i) * 512, w + 2 * i);
+        }
+    }
+    __syncthreads();
+    const auto weight = [&](int k, f2 w[P]) {
+#pragma unroll
+        for (int i = 0; i < P / 2; ++i) nb_f32(weights + (k * (P / 2) + i) * 512, w + 2 * i);
     };
-    for (int s = 0; s < p.stages; ++s) fetch(first + s * stride, s);
-    int stage = 0, it = 0;
+    int at = 0, it = 0;
     for (int64_t row = first; row < a.T; row += stride, it ^= 1) {
-        const uint4* slot = ring + (size_t)stage * pieces * nthr + tid;
-        cp_async_wait_upto(p.stages - 1);
-        float r[VPT][8];
+        cp_async_wait_upto(p.slots - 1);
+        if (F32) __syncwarp();
+        const char* slot = ring + at;
         float mean = 0.f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            if (col + j * gthr >= vec) continue;
-            nb_slot<F32>(slot + (VPT + RP * j) * nthr, nthr, r[j]);
-            if (LN)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mean += r[j][i];
-        }
         if (LN) {
-            mean = nb_xor_add(mean, 16);
-            if (p.gw > 1) {
-                if (lane == 0) red_sum[it][warp] = mean;
-                group_sync();
-                mean = 0.f;
-                for (int w = 0; w < p.gw; ++w) mean += red_sum[it][group * p.gw + w];
+            f2 sum = 0;
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                if (!(valid >> k & 1)) continue;
+                f2 r[P];
+                nb_stream<F32>(slot + lane * 16 + k * 512, r);
+#pragma unroll
+                for (int i = 0; i < P; ++i) sum = f2_add(sum, r[i]);
             }
-            mean *= inv_h;
+            float m[1] = {f2_sum(sum)};
+            nb_group_sums<1>(m, red_mean[it], p.gw, group, warp, lane, group_sync);
+            mean = m[0] * -inv_h;
         }
-        float sd = 0.f, sg = 0.f, sgd = 0.f;
+        f2 sd = 0, sg = 0, sgd = 0;
+        const f2 off = f2_make(mean, mean);
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = col + j * gthr;
-            if (v >= vec) continue;
-            float g[8], w[8];
-            unpack8(slot[j * nthr], g);
-            unpack8(__ldg(reinterpret_cast<const uint4*>(a.weight) + v), w);
+        for (int k = 0; k < NP; ++k) {
+            if (!(valid >> k & 1)) continue;
+            f2 r[P], g[P], w[P];
+            nb_stream<F32>(slot + lane * 16 + k * 512, r);
+            nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g);
+            weight(k, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = LN ? r[j][i] - mean : r[j][i], gw = g[i] * w[i];
-                sd = fmaf(d, d, sd);
-                if (LN) sg += gw;
-                sgd = fmaf(gw, d, sgd);
+            for (int i = 0; i < P; ++i) {
+                const f2 d = LN ? f2_add(r[i], off) : r[i], gw = f2_mul(g[i], w[i]);
+                sd = f2_fma(d, d, sd);
+                sgd = f2_fma(gw, d, sgd);
+                if (LN) sg = f2_add(sg, gw);
             }
         }
-        // red[.][warp] = {sd, sgd, sg}
-        const float two = nb_sum2(sd, sgd, lane);
-        if (LN) sg = nb_xor_add(sg, 16);
-        float* out = reinterpret_cast<float*>(&red[it][warp]);
-        if (lane == 0) out[0] = two;
-        if (lane == 16) out[1] = two;
-        if (LN && lane == 1) out[2] = sg;
-        group_sync();
-        sd = sg = sgd = 0.f;
-        for (int w = 0; w < p.gw; ++w) {
-            const float4 q = red[it][group * p.gw + w];
-            sd += q.x;
-            sgd += q.y;
-            if (LN) sg += q.z;
-        }
-        const float rstd = rsqrtf(sd / (float)a.H + a.eps);
-        const float mg = LN ? sg * inv_h : 0.f, mgd = rstd * rstd * (sgd * inv_h);
+        float sums[NS] = {};
+        sums[0] = f2_sum(sd);
+        sums[1] = f2_sum(sgd);
+        if (LN) sums[NS - 2] = f2_sum(sg);
+        nb_group_sums<NS>(sums, red[it], p.gw, group, warp, lane, group_sync);
+        const float rstd = rsqrtf(fmaf(sums[0], inv_h, a.eps));
+        const float mg = LN ? -sums[NS - 2] * inv_h : 0.f, mgd = -rstd * rstd * (sums[1] * inv_h);
+        const f2 rstd2 = f2_make(rstd, rstd), mg2 = f2_make(mg, mg), mgd2 = f2_make(mgd, mgd);
+        const int64_t out = row * a.H + col;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = col + j * gthr;
-            if (v >= vec) continue;
-            const int64_t off = row * a.H + 8 * v;
-            float g[8], w[8], o[8] = {};
-            unpack8(slot[j * nthr], g);
-            nb_slot<F32>(slot + (VPT + RP * j) * nthr, nthr, r[j]);
-            unpack8(__ldg(reinterpret_cast<const uint4*>(a.weight) + v), w);
-            if (p.ds_ring) nb_slot<F32>(slot + (VPT + RP * (VPT + j)) * nthr, nthr, o);
-            else if (a.dstream) nb_load<F32>(a.dstream, off, o);
+        for (int k = 0; k < NP; ++k) {
+            if (!(valid >> k & 1)) continue;
+            f2 r[P], g[P], w[P], o[P] = {};
+            nb_stream<F32>(slot + lane * 16 + k * 512, r);
+            nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g);
+            weight(k, w);
+            if (p.ds_ring) nb_stream<F32>(slot + lane * 16 + DS + k * 512, o);
+            else if (a.dstream) nb_stream<F32>(static_cast<const char*>(a.dstream) + out * SB + k * 512, o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = LN ? r[j][i] - mean : r[j][i];
-                dw[j][i] = fmaf(g[i], d * rstd, dw[j][i]);
-                if (LN) db[j][i] += g[i];
-                o[i] = fmaf(rstd, fmaf(g[i], w[i], -mg) - d * mgd, o[i]);
+            for (int i = 0; i < P; ++i) {
+                const f2 d = LN ? f2_add(r[i], off) : r[i];
+                dw[k][i] = f2_fma(g[i], f2_mul(d, rstd2), dw[k][i]);
+                if (LN) db[LN ? k : 0][i] = f2_add(db[LN ? k : 0][i], g[i]);
+                const f2 gw = LN ? f2_fma(g[i], w[i], mg2) : f2_mul(g[i], w[i]);
+                o[i] = f2_fma(rstd2, f2_fma(d, mgd2, gw), o[i]);
             }
-            if (a.dr) nb_store<F32>(a.dr, off, o);
-            if (a.dx) nb_store<false>(a.dx, off, o);
+            if (a.dr) {
+                if (F32) nb_put_f32(static_cast<float*>(a.dr) + out + k * 32 * C, o);
+                else nb_put_bf16<C>(static_cast<uint16_t*>(a.dr) + out + k * 32 * C, o);
+            }
+            if (a.dx) nb_put_bf16<C>(a.dx + out + k * 32 * C, o);
         }
-        fetch(row + p.stages * stride, stage);
-        stage = stage + 1 == p.stages ? 0 : stage + 1;
+        if (F32) __syncwarp();
+        fetch(row + p.slots * stride, at);
+        at += slot_bytes;
+        if (at == p.slots * slot_bytes) at = 0;
     }
     cp_async_wait<0>();
     if (!a.dweight && !a.dbias) return;
+    // the groups' sums, one group behind the other, in the shared memory of the weight and the ring
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.H;
-    if (p.groups == 1) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = col + j * gthr;
-            if (v >= vec) continue;
-            nb_store<true>(part, 8 * v, dw[j]);
-            if (LN) nb_store<true>(part, a.H + 8 * v, db[j]);
-        }
-        return;
-    }
-    // the groups' sums, one group behind the other, in the ring's memory
-    float* acc = reinterpret_cast<float*>(ring);
+    float* acc = reinterpret_cast<float*>(smem);
     for (int g = 0; g < p.groups; ++g) {
-        __syncthreads();
+        if (p.groups > 1) __syncthreads();
         if (g != group) continue;
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = col + j * gthr;
-            if (v >= vec) continue;
+        for (int k = 0; k < NP; ++k) {
+            if (!(valid >> k & 1)) continue;
 #pragma unroll
             for (int b = 0; b < (LN ? 2 : 1); ++b) {
-                float* q = acc + b * a.H + 8 * v;
-                float s[8];
+                f2* s = b ? db[LN ? k : 0] : dw[k];
+                const int c = b * a.H + col + k * 32 * C;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] = b ? db[LN ? j : 0][i] : dw[j][i];
-                if (g > 0) {
-                    float o[8];
-                    nb_load<true>(q, 0, o);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s[i] += o[i];
+                for (int i = 0; i < P; i += 2) {
+                    if (g > 0) {
+                        f2 o[2];
+                        nb_f32(acc + c + 2 * i, o);
+                        s[i] = f2_add(o[0], s[i]);
+                        s[i + 1] = f2_add(o[1], s[i + 1]);
+                    }
+                    nb_put_f32((g + 1 < p.groups ? acc : part) + c + 2 * i, s + i);
                 }
-                if (g + 1 < p.groups) nb_store<true>(q, 0, s);
-                else nb_store<true>(part, b * a.H + 8 * v, s);
             }
         }
     }
 }
 
-// A CTA adds 32 columns: warp w takes the partial rows w, w + 32, ..., then the warps' sums
-// are added in order.
-constexpr int SP_WARPS = 32;
+// A CTA adds 32 columns: warp w takes the partial rows w, w + 32, ..., SP_BATCH of them in
+// flight, then each warp adds one of the columns over the warps' sums.
+constexpr int SP_WARPS = 32, SP_BATCH = 8;
 
 __global__ void __launch_bounds__(SP_WARPS * 32) sum_partials_kernel(const float* part, int n, int64_t stride, int H,
                                                                    float* out0, float* out1) {
     __shared__ float red[SP_WARPS][33];
-    pdl_wait();
-    pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     float* out = blockIdx.y ? out1 : out0;
+    pdl_wait();
+    pdl_trigger();
     float s = 0.f;
-    if (col < H && out)
-        for (int i = warp; i < n; i += SP_WARPS) s += part[i * stride + (int64_t)blockIdx.y * H + col];
+    if (col < H && out) {
+        const float* p = part + (int64_t)blockIdx.y * H + col;
+        for (int i0 = warp; i0 < n; i0 += SP_WARPS * SP_BATCH) {
+            float v[SP_BATCH];
+#pragma unroll
+            for (int b = 0; b < SP_BATCH; ++b) v[b] = i0 + SP_WARPS * b < n ? p[(i0 + SP_WARPS * b) * stride] : 0.f;
+#pragma unroll
+            for (int b = 0; b < SP_BATCH; ++b) s += v[b];
+        }
+    }
     red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && col < H && out) {
-        s = 0.f;
-        for (int w = 0; w < SP_WARPS; ++w) s += red[w][lane];
-        out[col] = s;
-    }
+    s = nb_warp_sum(red[lane][warp]);
+    if (lane == 0 && blockIdx.x * 32 + warp < H && out) out[blockIdx.x * 32 + warp] = s;
 }
 
-template <int VPT, bool F32, bool LN>
+template <int NP, bool F32, bool LN>
 cudaError_t launch_norm_bwd_size(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
+    constexpr int C = F32 ? 4 : 8;
     NormBwdPlan p;
-    const int vec = L.H / 8;
-    p.gw = (vec + VPT * 32 - 1) / (VPT * 32);
+    p.gw = (L.H + NP * 32 * C - 1) / (NP * 32 * C);
+    const size_t weight = (size_t)p.gw * NP * 128 * C, stream = (size_t)p.gw * NP * 512;
+    const size_t slot = stream + (size_t)p.gw * NP * 64 * C;  // a row of a group, without dstream
+    // dstream stays out of the ring where it leaves no room for two rows
+    p.ds_ring = L.dstream && weight + 2 * (slot + stream) <= NB_SMEM;
+    const size_t row = slot + (p.ds_ring ? stream : 0);
+    // The rows that an SM holds: past about 50 KB on their way the memory slows down with an
+    // fp32 stream (28672 rows of 2048, RMS: 2 groups of 2 rows 144 us, of 3 164, 4 groups of 2
+    // 154), and a little with a bf16 one (4 groups of 2 77 us, of 3 78, of 4 83; 8 groups 84);
+    // the layer norm takes longer over a row and wants the third (fp32, 14336 rows of 4096: 150
+    // us against 200, 154 with a fourth).
     p.groups = NB_WARPS / p.gw;
-    const int threads = p.gw * p.groups * 32;
-    const size_t per = (size_t)threads * VPT * 16, rp = F32 ? 2 : 1;
-    // two CTAs an SM where each then holds two stages, else one; dstream stays out of the ring
-    // where it leaves no room for two
-    p.ds_ring = L.dstream != nullptr;
-    int ctas = VPT <= 2 ? 2 : 1;
-    if (ctas == 2 && 2 * per * (1 + rp + (p.ds_ring ? rp : 0)) > NB_SMEM / 2 - 1024) ctas = 1;
-    if (2 * per * (1 + rp + (p.ds_ring ? rp : 0)) > NB_SMEM - 1024) p.ds_ring = false;
-    const size_t stage = per * (1 + rp + (p.ds_ring ? rp : 0)), room = NB_SMEM / ctas - 1024;
-    p.stages = (int)std::min<size_t>(NB_STAGES, room / stage);
-    const size_t smem = p.stages * stage;  // at least the 8 * H bytes that the groups' sums take
-    const auto kernel = norm_bwd_kernel<VPT, F32, LN>;
+    if (F32) p.groups = std::max(1, std::min(p.groups, (int)(NB_F32_ROWS / row)));
+    p.slots = (int)std::min<size_t>(F32 && !LN ? 2 : 3, (NB_SMEM - weight) / (p.groups * row));
+    const size_t smem = weight + p.groups * p.slots * row;  // at least the 8 * H bytes that the groups' sums take
+    const auto kernel = norm_bwd_kernel<NP, F32, LN>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = (int)std::min<int64_t>((L.T + p.groups - 1) / p.groups, std::min(ctas * num_sms, kBwdPartials));
-    e = launch_k(LN ? "layernorm_bwd" : "rmsnorm_bwd", kernel, dim3(grid), dim3(threads), smem, s, L, p);
+    const int grid = (int)std::min<int64_t>((L.T + p.groups - 1) / p.groups, std::min(num_sms, kBwdPartials));
+    e = launch_k(LN ? "layernorm_bwd" : "rmsnorm_bwd", kernel, dim3(grid), dim3(p.gw * p.groups * 32), smem, s, L, p);
     if (e != cudaSuccess || (!L.dweight && !L.dbias)) return e;
     return launch_sum_partials(L.part, grid, 2 * (int64_t)L.H, L.H, L.dweight, L.dbias, s);
 }
@@ -313,8 +402,8 @@ cudaError_t launch_norm_bwd_size(const NormBwdLaunch& L, int num_sms, cudaStream
 template <int VPT>
 cudaError_t launch_norm_bwd_vpt(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
     if (L.f32)
-        return L.ln ? launch_norm_bwd_size<VPT, true, true>(L, num_sms, s)
-                    : launch_norm_bwd_size<VPT, true, false>(L, num_sms, s);
+        return L.ln ? launch_norm_bwd_size<2 * VPT, true, true>(L, num_sms, s)
+                    : launch_norm_bwd_size<2 * VPT, true, false>(L, num_sms, s);
     return L.ln ? launch_norm_bwd_size<VPT, false, true>(L, num_sms, s)
                 : launch_norm_bwd_size<VPT, false, false>(L, num_sms, s);
 }
@@ -328,9 +417,20 @@ cudaError_t launch_sum_partials(const float* part, int n, int64_t stride, int H,
 }
 
 cudaError_t launch_norm_bwd(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
-    // a vector a thread up to 4096 values, two up to 8192, four beyond
-    if (L.H <= 4096) return launch_norm_bwd_vpt<1>(L, num_sms, s);
-    return L.H <= 8192 ? launch_norm_bwd_vpt<2>(L, num_sms, s) : launch_norm_bwd_vpt<4>(L, num_sms, s);
+    // Columns a thread: 16 while that leaves few warps idle, else 32, which shares what a row
+    // costs beside its elements among more of them.  58.7 M elements, us with 16 / 32: bf16, RMS
+    // 2048 77 / 84, 5120 90 / 80 (10 warps / 15), 7168 79 / 79; layer norm 1024 57 / 63, 1408 84 /
+    // 85, 2048 92 / 83, 7168 112 / 92; fp32, layer norm 4096 150 / 166, 5120 144 / 180, 7168 160 / 147.
+    bool wide;
+    if (L.f32) {
+        wide = L.H > 6144;
+    } else if (L.ln) {
+        wide = L.H > 1536;
+    } else {
+        const int gw = (L.H + 511) / 512;
+        wide = gw > NB_WARPS || NB_WARPS / gw * gw < 14;
+    }
+    return wide ? launch_norm_bwd_vpt<4>(L, num_sms, s) : launch_norm_bwd_vpt<2>(L, num_sms, s);
 }
 
 }  // namespace moe
