@@ -18,6 +18,9 @@
 // shared memory (cp.async): the copies need no barrier, and a row's one barrier (the layer
 // norm's two: the mean comes first, so that a row far from zero keeps its variance) joins its
 // warps' sums.
+//
+// Narrow rows keep r, dy and the weight in registers from one pass to the next; rows of more
+// columns a thread read them again (the weight from shared memory, in binary32).
 #include <algorithm>
 
 #include "moe_internal.cuh"
@@ -28,6 +31,10 @@ namespace {
 constexpr int NB_WARPS = 16;           // warps of a CTA at most, one CTA an SM
 constexpr int NB_SMEM = 227 * 1024 - 1024;  // of a CTA, less the static arrays
 constexpr int NB_F32_ROWS = 48 * 1024; // of an fp32 stream's rows, one for each of a CTA's groups
+
+// What a kernel keeps: the row's r, dy and the weight in registers from one pass to the next, or
+// the weight in shared memory in binary32, or nothing.
+enum { NB_REGISTERS, NB_SHARED, NB_NOTHING };
 
 struct NormBwdPlan {
     int gw, groups, slots;   // warps of a group, groups of a CTA, rows that a group's ring holds
@@ -43,10 +50,11 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void cp_async_wait_upto(int n) {  // n uniform, below 3
+__device__ __forceinline__ void cp_async_wait_upto(int n) {  // n uniform, at most 3
     if (n == 0) cp_async_wait<0>();
     else if (n == 1) cp_async_wait<1>();
-    else cp_async_wait<2>();
+    else if (n == 2) cp_async_wait<2>();
+    else cp_async_wait<3>();
 }
 
 // Pairs of binary32 values.
@@ -162,8 +170,18 @@ __device__ __forceinline__ void nb_group_sums(float (&v)[N], float* red, int gw,
     if (lane % (32 / N) == 0) red[warp * N + lane / (32 / N)] = mine;
     sync();
     const int w = lane & 15;
+    const float* q = red + (group * gw + (w < gw ? w : 0)) * N;
+    if (N == 4) {
+        const float4 f = *reinterpret_cast<const float4*>(q);
+        v[0] = f.x; v[1 % N] = f.y; v[2 % N] = f.z; v[3 % N] = f.w;
+    } else if (N == 2) {
+        const float2 f = *reinterpret_cast<const float2*>(q);
+        v[0] = f.x; v[1 % N] = f.y;
+    } else {
+        v[0] = q[0];
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = w < gw ? red[(group * gw + w) * N + i] : 0.f;
+    for (int i = 0; i < N; ++i) v[i] = w < gw ? v[i] : 0.f;
     mine = nb_sums<N, true>(v, lane);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (16 / N));
@@ -171,15 +189,16 @@ __device__ __forceinline__ void nb_group_sums(float (&v)[N], float* red, int gw,
 
 // NP pieces a thread: 8 columns of a bf16 stream, or 4 of an fp32 one (16 bytes either way, so
 // that a warp's copies and stores cover whole lines).  A warp's pieces lie side by side.
-template <int NP, bool F32, bool LN>
+template <int NP, bool F32, bool LN, int KEEP>
 __global__ void __launch_bounds__(NB_WARPS * 32, 1)
     norm_bwd_kernel(const __grid_constant__ NormBwdLaunch a, const __grid_constant__ NormBwdPlan p) {
-    extern __shared__ uint4 smem[];  // [gw * NP pieces] weight, then [warp][slot] r, dy, dstream
+    extern __shared__ uint4 smem[];  // [NB_SHARED: gw * NP pieces of weight], [warp][slot] r, dy, dstream
+    constexpr bool HOLD = KEEP == NB_REGISTERS, W_SMEM = KEEP == NB_SHARED;
     constexpr int C = F32 ? 4 : 8, P = C / 2, SB = F32 ? 4 : 2;  // columns, pairs of a piece; bytes of a stream value
     constexpr int NS = LN ? 4 : 2;                               // a row's sums: d^2, g d (and g)
     constexpr int DY = NP * 512, DS = DY + NP * 64 * C;          // a slot's dy and dstream
-    __shared__ float red[2][NB_WARPS * NS];
-    __shared__ float red_mean[2][NB_WARPS];
+    __shared__ alignas(16) float red[2][NB_WARPS * NS];
+    __shared__ float red_mean[2][LN ? NB_WARPS : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.gw, gwarp = warp - group * p.gw;
     const int slot_bytes = DS + (p.ds_ring ? NP * 512 : 0);
@@ -199,7 +218,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
     const int64_t first = (int64_t)group * gridDim.x + blockIdx.x;
     const auto group_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.gw * 32) : "memory"); };
     char* const weights = reinterpret_cast<char*>(smem) + (gwarp * NP * P * 16 + lane) * 16;
-    char* const ring = reinterpret_cast<char*>(smem) + p.gw * NP * 128 * C + warp * p.slots * slot_bytes;
+    char* const ring = reinterpret_cast<char*>(smem) + (W_SMEM ? p.gw * NP * 128 * C : 0) + warp * p.slots * slot_bytes;
 
     f2 dw[NP][P] = {}, db[LN ? NP : 1][P] = {};
     pdl_wait();
@@ -223,55 +242,62 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         cp_async_commit();
     };
     for (int s = 0; s < p.slots; ++s) fetch(first + s * stride, s * slot_bytes);
-    // the weight in binary32, once a CTA
-    if (group == 0) {
+    f2 held_w[HOLD ? NP : 1][P] = {};
+    if (HOLD || (W_SMEM && group == 0)) {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
             f2 w[P] = {};
             if (valid >> k & 1) nb_bf16<C>(a.weight + col + k * 32 * C, w);
 #pragma unroll
-            for (int i = 0; i < P / 2; ++i) nb_put_f32(weights + (k * (P / 2) + i) * 512, w + 2 * i);
+            for (int i = 0; i < P; ++i)
+                if (HOLD) held_w[HOLD ? k : 0][i] = w[i];
+                else if (i % 2 == 0) nb_put_f32(weights + (k * (P / 2) + i / 2) * 512, w + i);
         }
     }
-    __syncthreads();
-    const auto weight = [&](int k, f2 w[P]) {
+    if (W_SMEM) __syncthreads();
+    const auto read_weight = [&](int k, f2 w[P]) {
+        if (W_SMEM) {
 #pragma unroll
-        for (int i = 0; i < P / 2; ++i) nb_f32(weights + (k * (P / 2) + i) * 512, w + 2 * i);
+            for (int i = 0; i < P / 2; ++i) nb_f32(weights + (k * (P / 2) + i) * 512, w + 2 * i);
+        } else {
+            nb_bf16<C>(a.weight + col + k * 32 * C, w);
+        }
     };
     int at = 0, it = 0;
     for (int64_t row = first; row < a.T; row += stride, it ^= 1) {
         cp_async_wait_upto(p.slots - 1);
         if (F32) __syncwarp();
         const char* slot = ring + at;
-        float mean = 0.f;
+        f2 r[NP][P], g[NP][P];  // NB_REGISTERS: kept from one pass to the next
+        float mean = 0.f;       // negated
         if (LN) {
             f2 sum = 0;
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
                 if (!(valid >> k & 1)) continue;
-                f2 r[P];
-                nb_stream<F32>(slot + lane * 16 + k * 512, r);
+                nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
 #pragma unroll
-                for (int i = 0; i < P; ++i) sum = f2_add(sum, r[i]);
+                for (int i = 0; i < P; ++i) sum = f2_add(sum, r[k][i]);
             }
             float m[1] = {f2_sum(sum)};
             nb_group_sums<1>(m, red_mean[it], p.gw, group, warp, lane, group_sync);
             mean = m[0] * -inv_h;
         }
-        f2 sd = 0, sg = 0, sgd = 0;
         const f2 off = f2_make(mean, mean);
+        f2 sd = 0, sg = 0, sgd = 0;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
             if (!(valid >> k & 1)) continue;
-            f2 r[P], g[P], w[P];
-            nb_stream<F32>(slot + lane * 16 + k * 512, r);
-            nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g);
-            weight(k, w);
+            f2 w[P];
+            if (!LN || !HOLD) nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
+            nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g[k]);
+            if (!HOLD) read_weight(k, w);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const f2 d = LN ? f2_add(r[i], off) : r[i], gw = f2_mul(g[i], w[i]);
-                sd = f2_fma(d, d, sd);
-                sgd = f2_fma(gw, d, sgd);
+                if (LN) r[k][i] = f2_add(r[k][i], off);
+                const f2 gw = f2_mul(g[k][i], HOLD ? held_w[HOLD ? k : 0][i] : w[i]);
+                sd = f2_fma(r[k][i], r[k][i], sd);
+                sgd = f2_fma(gw, r[k][i], sgd);
                 if (LN) sg = f2_add(sg, gw);
             }
         }
@@ -287,18 +313,21 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
             if (!(valid >> k & 1)) continue;
-            f2 r[P], g[P], w[P], o[P] = {};
-            nb_stream<F32>(slot + lane * 16 + k * 512, r);
-            nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g);
-            weight(k, w);
+            f2 w[P], o[P] = {};
+            if (!HOLD) {
+                nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
+                nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g[k]);
+                read_weight(k, w);
+            }
             if (p.ds_ring) nb_stream<F32>(slot + lane * 16 + DS + k * 512, o);
             else if (a.dstream) nb_stream<F32>(static_cast<const char*>(a.dstream) + out * SB + k * 512, o);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                const f2 d = LN ? f2_add(r[i], off) : r[i];
-                dw[k][i] = f2_fma(g[i], f2_mul(d, rstd2), dw[k][i]);
-                if (LN) db[LN ? k : 0][i] = f2_add(db[LN ? k : 0][i], g[i]);
-                const f2 gw = LN ? f2_fma(g[i], w[i], mg2) : f2_mul(g[i], w[i]);
+                const f2 wi = HOLD ? held_w[HOLD ? k : 0][i] : w[i];
+                const f2 d = LN && !HOLD ? f2_add(r[k][i], off) : r[k][i];
+                dw[k][i] = f2_fma(g[k][i], f2_mul(d, rstd2), dw[k][i]);
+                if (LN) db[LN ? k : 0][i] = f2_add(db[LN ? k : 0][i], g[k][i]);
+                const f2 gw = LN ? f2_fma(g[k][i], wi, mg2) : f2_mul(g[k][i], wi);
                 o[i] = f2_fma(rstd2, f2_fma(d, mgd2, gw), o[i]);
             }
             if (a.dr) {
@@ -314,7 +343,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
     }
     cp_async_wait<0>();
     if (!a.dweight && !a.dbias) return;
-    // the groups' sums, one group behind the other, in the shared memory of the weight and the ring
+    // the groups' sums, one group behind the other, in the ring's memory
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.H;
     float* acc = reinterpret_cast<float*>(smem);
     for (int g = 0; g < p.groups; ++g) {
@@ -371,26 +400,10 @@ __global__ void __launch_bounds__(SP_WARPS * 32) sum_partials_kernel(const float
     if (lane == 0 && blockIdx.x * 32 + warp < H && out) out[blockIdx.x * 32 + warp] = s;
 }
 
-template <int NP, bool F32, bool LN>
-cudaError_t launch_norm_bwd_size(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
-    constexpr int C = F32 ? 4 : 8;
-    NormBwdPlan p;
-    p.gw = (L.H + NP * 32 * C - 1) / (NP * 32 * C);
-    const size_t weight = (size_t)p.gw * NP * 128 * C, stream = (size_t)p.gw * NP * 512;
-    const size_t slot = stream + (size_t)p.gw * NP * 64 * C;  // a row of a group, without dstream
-    // dstream stays out of the ring where it leaves no room for two rows
-    p.ds_ring = L.dstream && weight + 2 * (slot + stream) <= NB_SMEM;
-    const size_t row = slot + (p.ds_ring ? stream : 0);
-    // The rows that an SM holds: past about 50 KB on their way the memory slows down with an
-    // fp32 stream (28672 rows of 2048, RMS: 2 groups of 2 rows 144 us, of 3 164, 4 groups of 2
-    // 154), and a little with a bf16 one (4 groups of 2 77 us, of 3 78, of 4 83; 8 groups 84);
-    // the layer norm takes longer over a row and wants the third (fp32, 14336 rows of 4096: 150
-    // us against 200, 154 with a fourth).
-    p.groups = NB_WARPS / p.gw;
-    if (F32) p.groups = std::max(1, std::min(p.groups, (int)(NB_F32_ROWS / row)));
-    p.slots = (int)std::min<size_t>(F32 && !LN ? 2 : 3, (NB_SMEM - weight) / (p.groups * row));
-    const size_t smem = weight + p.groups * p.slots * row;  // at least the 8 * H bytes that the groups' sums take
-    const auto kernel = norm_bwd_kernel<NP, F32, LN>;
+template <int NP, bool F32, bool LN, int KEEP>
+cudaError_t launch_norm_bwd_kernel(const NormBwdLaunch& L, const NormBwdPlan& p, size_t smem, int num_sms,
+                                   cudaStream_t s) {
+    const auto kernel = norm_bwd_kernel<NP, F32, LN, KEEP>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int grid = (int)std::min<int64_t>((L.T + p.groups - 1) / p.groups, std::min(num_sms, kBwdPartials));
@@ -399,13 +412,37 @@ cudaError_t launch_norm_bwd_size(const NormBwdLaunch& L, int num_sms, cudaStream
     return launch_sum_partials(L.part, grid, 2 * (int64_t)L.H, L.H, L.dweight, L.dbias, s);
 }
 
-template <int VPT>
-cudaError_t launch_norm_bwd_vpt(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
-    if (L.f32)
-        return L.ln ? launch_norm_bwd_size<2 * VPT, true, true>(L, num_sms, s)
-                    : launch_norm_bwd_size<2 * VPT, true, false>(L, num_sms, s);
-    return L.ln ? launch_norm_bwd_size<VPT, false, true>(L, num_sms, s)
-                : launch_norm_bwd_size<VPT, false, false>(L, num_sms, s);
+template <bool F32, bool LN>
+cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
+    // 16 columns a thread, or 32, which shares what a row costs beside its elements among more
+    // of them and lets two groups of warps work on a CTA's rows where 16 allow one; us with 16 /
+    // 32, 58.7 M elements: bf16, RMS 4096 77 / 78, 5120 84 / 80 (10 warps / 15), 7168 76 / 78;
+    // bf16, layer norm 1024 55 / 63, 1408 78 / 85, 2048 86 / 83, 4096 91 / 83, 7168 103 / 92;
+    // fp32, layer norm 4096 153 / 170, 5120 145 / 173, 7168 163 / 147.
+    const int narrow = (L.H + 511) / 512;  // warps of a group, 16 columns a thread
+    const bool wide = F32 ? L.H > 6144 : LN ? L.H > 2048 : narrow > NB_WARPS || NB_WARPS / narrow * narrow < 14;
+    const int columns = wide ? 32 : 16;
+    NormBwdPlan p;
+    p.gw = (L.H + columns * 32 - 1) / (columns * 32);
+    const size_t stream = (size_t)p.gw * 32 * columns * (F32 ? 4 : 2), weight = wide ? (size_t)p.gw * 128 * columns : 0;
+    const size_t slot = stream + (size_t)p.gw * 64 * columns;  // a row of a group, without dstream
+    // dstream stays out of the ring where it leaves no room for two rows
+    p.ds_ring = L.dstream && 2 * (slot + stream) <= NB_SMEM;
+    const size_t row = slot + (p.ds_ring ? stream : 0);
+    // The rows that an SM holds: past about 50 KB on their way the memory slows down with an
+    // fp32 stream (28672 rows of 2048, RMS: 2 groups of 2 rows 142 us, of 3 163, 4 groups of 2
+    // 153), and a little with a bf16 one (4 groups of 2 76 us, of 3 78, of 4 82); the layer norm
+    // takes longer over a row and wants the third (fp32, 14336 rows of 4096: 153 us against 193).
+    p.groups = NB_WARPS / p.gw;
+    if (F32) p.groups = std::max(1, std::min(p.groups, (int)(NB_F32_ROWS / row)));
+    const bool w_smem = wide && weight + 2 * p.groups * row <= NB_SMEM;
+    const size_t below = w_smem ? weight : 0;
+    p.slots = (int)std::min<size_t>(F32 && !LN ? 2 : 3, (NB_SMEM - below) / (p.groups * row));
+    const size_t smem = std::max(below + p.groups * p.slots * row, (size_t)8 * L.H);  // the groups' sums take 8 * H
+    constexpr int NP = F32 ? 4 : 2;
+    if (!wide) return launch_norm_bwd_kernel<NP, F32, LN, NB_REGISTERS>(L, p, smem, num_sms, s);
+    if (w_smem) return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_SHARED>(L, p, smem, num_sms, s);
+    return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_NOTHING>(L, p, smem, num_sms, s);
 }
 
 }  // namespace
@@ -417,20 +454,8 @@ cudaError_t launch_sum_partials(const float* part, int n, int64_t stride, int H,
 }
 
 cudaError_t launch_norm_bwd(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
-    // Columns a thread: 16 while that leaves few warps idle, else 32, which shares what a row
-    // costs beside its elements among more of them.  58.7 M elements, us with 16 / 32: bf16, RMS
-    // 2048 77 / 84, 5120 90 / 80 (10 warps / 15), 7168 79 / 79; layer norm 1024 57 / 63, 1408 84 /
-    // 85, 2048 92 / 83, 7168 112 / 92; fp32, layer norm 4096 150 / 166, 5120 144 / 180, 7168 160 / 147.
-    bool wide;
-    if (L.f32) {
-        wide = L.H > 6144;
-    } else if (L.ln) {
-        wide = L.H > 1536;
-    } else {
-        const int gw = (L.H + 511) / 512;
-        wide = gw > NB_WARPS || NB_WARPS / gw * gw < 14;
-    }
-    return wide ? launch_norm_bwd_vpt<4>(L, num_sms, s) : launch_norm_bwd_vpt<2>(L, num_sms, s);
+    if (L.f32) return L.ln ? launch_norm_bwd_type<true, true>(L, num_sms, s) : launch_norm_bwd_type<true, false>(L, num_sms, s);
+    return L.ln ? launch_norm_bwd_type<false, true>(L, num_sms, s) : launch_norm_bwd_type<false, false>(L, num_sms, s);
 }
 
 }  // namespace moe
