@@ -11,17 +11,12 @@
 #include <algorithm>
 
 #include "moe_internal.cuh"
+#include "moe_row_sums.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int FB_WARPS = 8;
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
 
 __device__ __forceinline__ int32_t pair_row_of(const int32_t* pair_row, int64_t p, int64_t rows_cap, int32_t* status) {
     const int32_t r = pair_row[p];
@@ -30,64 +25,175 @@ __device__ __forceinline__ int32_t pair_row_of(const int32_t* pair_row, int64_t 
     return -1;
 }
 
-// A warp to a pair, or (the last T warps, with a gate) to a token's shared expert.
+// A warp to a pair; FB_BATCH vectors of dout and of y a lane in flight before they are used.
+constexpr int FB_BATCH = 4;
+
 __global__ void __launch_bounds__(FB_WARPS * 32) finalize_bwd_kernel(const __grid_constant__ FinalizeBwdLaunch a) {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
-    const int64_t pairs = a.T * a.k, units = pairs + (a.gate_w ? a.T : 0);
-    for (int64_t u = (int64_t)blockIdx.x * FB_WARPS + warp; u < units; u += (int64_t)gridDim.x * FB_WARPS) {
-        if (u < pairs) {
-            const int64_t t = u / a.k;
-            const int32_t r = pair_row_of(a.pair_row, u, a.rows_cap, lane == 0 ? &a.hdr->status : nullptr);
-            float dot = 0.f;
-            if (r >= 0) {
-                const float w = a.w ? a.w[u] : 1.f;
-                const uint4* dout = reinterpret_cast<const uint4*>(a.dout + t * a.H);
-                const uint16_t* y = a.y + (int64_t)r * a.H;
-                uint4* dy = reinterpret_cast<uint4*>(a.dy + (int64_t)r * a.H);
-                for (int v = lane; v < vec; v += 32) {
-                    float d[8], f[8];
-                    unpack8(dout[v], d);
-                    if (a.dw) {
-                        unpack8(reinterpret_cast<const uint4*>(y)[v], f);
-                        for (int i = 0; i < 8; ++i) dot = fmaf(d[i], f[i], dot);
+    const int64_t pairs = a.T * a.k;
+    for (int64_t u = (int64_t)blockIdx.x * FB_WARPS + warp; u < pairs; u += (int64_t)gridDim.x * FB_WARPS) {
+        const int64_t t = u / a.k;
+        const int32_t r = pair_row_of(a.pair_row, u, a.rows_cap, lane == 0 ? &a.hdr->status : nullptr);
+        float dot = 0.f;
+        if (r >= 0) {
+            const float w = a.w ? a.w[u] : 1.f;
+            const uint4* dout = reinterpret_cast<const uint4*>(a.dout + t * a.H);
+            const uint4* y = reinterpret_cast<const uint4*>(a.y + (int64_t)r * a.H);  // not __ldg: dy may be y
+            uint4* dy = reinterpret_cast<uint4*>(a.dy + (int64_t)r * a.H);
+            for (int v0 = lane; v0 < vec; v0 += 32 * FB_BATCH) {
+                uint4 d[FB_BATCH], f[FB_BATCH];
+#pragma unroll
+                for (int b = 0; b < FB_BATCH; ++b) {
+                    const bool ok = v0 + 32 * b < vec;
+                    d[b] = ok ? dout[v0 + 32 * b] : make_uint4(0, 0, 0, 0);
+                    f[b] = ok && a.dw ? y[v0 + 32 * b] : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int b = 0; b < FB_BATCH; ++b) {
+                    float x[8], z[8];
+                    unpack8(d[b], x);
+                    unpack8(f[b], z);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot = fmaf(x[i], z[i], dot);
+                        x[i] *= w;
                     }
-                    for (int i = 0; i < 8; ++i) d[i] *= w;
-                    dy[v] = pack8(d);
+                    if (v0 + 32 * b < vec) dy[v0 + 32 * b] = pack8(x);
                 }
             }
-            if (a.dw) {
-                dot = warp_sum(dot);
-                if (lane == 0) a.dw[u] = dot;
-            }
-        } else {
-            const int64_t t = u - pairs;
-            const uint4* dout = reinterpret_cast<const uint4*>(a.dout + t * a.H);
-            const uint4* ysh = reinterpret_cast<const uint4*>(a.y_sh + t * a.H);
-            const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.H);
-            const uint4* gw = reinterpret_cast<const uint4*>(a.gate_w);
-            float z = 0.f, dot = 0.f;
-            for (int v = lane; v < vec; v += 32) {
-                float d[8], f[8];
-                unpack8(x[v], d);
-                unpack8(gw[v], f);
-                for (int i = 0; i < 8; ++i) z = fmaf(d[i], f[i], z);
-                unpack8(dout[v], d);
-                unpack8(ysh[v], f);
-                for (int i = 0; i < 8; ++i) dot = fmaf(d[i], f[i], dot);
-            }
-            z = warp_sum(z);
+        }
+        if (a.dw) {
             dot = warp_sum(dot);
-            const float g = 1.f / (1.f + expf(-z));
-            if (lane == 0) a.dgate[t] = g * (1.f / (1.f + expf(z))) * dot;
-            uint4* dysh = reinterpret_cast<uint4*>(a.dy_sh + t * a.H);
-            for (int v = lane; v < vec; v += 32) {
-                float d[8];
-                unpack8(dout[v], d);
-                for (int i = 0; i < 8; ++i) d[i] *= g;
-                dysh[v] = pack8(d);
+            if (lane == 0) a.dw[u] = dot;
+        }
+    }
+}
+
+// The gated shared expert of rows of at most GB_MAX_H values: a group of gw warps to a token,
+// 16 columns a thread (the same ones of every token, so that the gate weight's sums stay in
+// registers over a persistent grid), the next token's rows in flight.  A CTA's groups add
+// their sums in order, the CTAs' are added by another kernel.
+constexpr int GB_WARPS = 16, GB_MAX_H = GB_WARPS * 512;
+
+__device__ __forceinline__ float gate_of(float z) { return 1.f / (1.f + expf(-z)); }
+
+__global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid_constant__ FinalizeBwdLaunch a, int gw,
+                                                                  int groups) {
+    __shared__ alignas(16) float red[2][GB_WARPS * 2];
+    extern __shared__ float4 acc[];  // with more than one group: H floats
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
+    const int group = warp / gw, col = (warp - group * gw) * 64 + lane;  // in vectors of 8: col and col + 32
+    const bool in[2] = {col < vec, col + 32 < vec};
+    const auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(gw * 32) : "memory"); };
+    const int64_t stride = (int64_t)gridDim.x * groups;
+    float sum[2][8] = {};
+    uint4 w[2] = {}, next[3][2] = {};
+    pdl_wait();
+    pdl_trigger();
+    const uint16_t* const src[3] = {a.dout, a.y_sh, a.x};
+    const auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (t < a.T && in[j]) next[s][j] = __ldg(reinterpret_cast<const uint4*>(src[s] + t * a.H) + col + 32 * j);
+    };
+    int64_t t = (int64_t)group * gridDim.x + blockIdx.x;
+    fetch(t);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if (in[j]) w[j] = __ldg(reinterpret_cast<const uint4*>(a.gate_w) + col + 32 * j);
+    for (int it = 0; t < a.T; t += stride, it ^= 1) {
+        uint4 cur[3][2];
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) cur[s][j] = next[s][j];
+        fetch(t + stride);
+        float dots[2] = {0.f, 0.f};  // x . gate_w, dout . y_sh
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float p[8], q[8];
+            unpack8(cur[2][j], p);
+            unpack8(w[j], q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dots[0] = fmaf(p[i], q[i], dots[0]);
+            unpack8(cur[0][j], p);
+            unpack8(cur[1][j], q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dots[1] = fmaf(p[i], q[i], dots[1]);
+        }
+        group_sums<2>(dots, red[it], gw, group * gw, warp, lane, sync);
+        const float g = gate_of(dots[0]), dz = g * gate_of(-dots[0]) * dots[1];
+        if (col == 0) a.dgate[t] = dz;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!in[j]) continue;
+            float d[8], x[8];
+            unpack8(cur[0][j], d);
+            unpack8(cur[2][j], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] *= g;
+                sum[j][i] = fmaf(dz, x[i], sum[j][i]);
             }
+            reinterpret_cast<uint4*>(a.dy_sh + t * a.H)[col + 32 * j] = pack8(d);
+        }
+    }
+    if (!a.dgate_w) return;
+    float4* const part = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.H);
+    for (int g = 0; g < groups; ++g) {
+        if (groups > 1) __syncthreads();
+        if (g != group) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if (!in[j]) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int at = 2 * (col + 32 * j) + h;
+                float4 s = make_float4(sum[j][4 * h], sum[j][4 * h + 1], sum[j][4 * h + 2], sum[j][4 * h + 3]);
+                if (g > 0) {
+                    const float4 o = acc[at];
+                    s.x += o.x; s.y += o.y; s.z += o.z; s.w += o.w;
+                }
+                (g + 1 < groups ? acc : part)[at] = s;
+            }
+        }
+    }
+}
+
+// The same for any H, without the gate weight's gradient: a warp to a token, its rows read twice.
+__global__ void __launch_bounds__(FB_WARPS * 32) gate_rows_kernel(const __grid_constant__ FinalizeBwdLaunch a) {
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
+    for (int64_t t = (int64_t)blockIdx.x * FB_WARPS + warp; t < a.T; t += (int64_t)gridDim.x * FB_WARPS) {
+        const uint4* dout = reinterpret_cast<const uint4*>(a.dout + t * a.H);
+        const uint4* ysh = reinterpret_cast<const uint4*>(a.y_sh + t * a.H);
+        const uint4* x = reinterpret_cast<const uint4*>(a.x + t * a.H);
+        const uint4* gw = reinterpret_cast<const uint4*>(a.gate_w);
+        float z = 0.f, dot = 0.f;
+        for (int v = lane; v < vec; v += 32) {
+            float d[8], f[8];
+            unpack8(x[v], d);
+            unpack8(gw[v], f);
+            for (int i = 0; i < 8; ++i) z = fmaf(d[i], f[i], z);
+            unpack8(dout[v], d);
+            unpack8(ysh[v], f);
+            for (int i = 0; i < 8; ++i) dot = fmaf(d[i], f[i], dot);
+        }
+        z = warp_sum(z);
+        dot = warp_sum(dot);
+        const float g = gate_of(z);
+        if (lane == 0) a.dgate[t] = g * gate_of(-z) * dot;
+        uint4* dysh = reinterpret_cast<uint4*>(a.dy_sh + t * a.H);
+        for (int v = lane; v < vec; v += 32) {
+            float d[8];
+            unpack8(dout[v], d);
+            for (int i = 0; i < 8; ++i) d[i] *= g;
+            dysh[v] = pack8(d);
         }
     }
 }
@@ -238,15 +344,26 @@ __global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& L, int num_sms, cudaStream_t s) {
-    const int64_t units = L.T * L.k + (L.gate_w ? L.T : 0);
-    const unsigned grid = (unsigned)std::min<int64_t>((units + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T * L.k + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
     cudaError_t e = launch_k("finalize_bwd", finalize_bwd_kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L);
+    if (e != cudaSuccess || !L.gate_w) return e;
+    int parts;
+    if (L.H <= GB_MAX_H) {
+        const int gw = (L.H + 511) / 512, groups = GB_WARPS / gw;
+        parts = (int)std::min<int64_t>((L.T + groups - 1) / groups, std::min(num_sms, kBwdPartials));
+        e = launch_k("gate_bwd", gate_bwd_kernel, dim3(parts), dim3(gw * groups * 32),
+                     groups > 1 ? (size_t)L.H * 4 : 0, s, L, gw, groups);
+    } else {
+        const unsigned rows = (unsigned)std::min<int64_t>((L.T + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
+        e = launch_k("gate_rows_bwd", gate_rows_kernel, dim3(rows), dim3(FB_WARPS * 32), 0, s, L);
+        if (e != cudaSuccess || !L.dgate_w) return e;
+        parts = (int)std::min<int64_t>(L.T, kBwdPartials);
+        e = launch_k("gate_weight_bwd", gate_weight_kernel,
+                     dim3((L.H / 8 + FB_WARPS * 32 - 1) / (FB_WARPS * 32), parts), dim3(FB_WARPS * 32), 0, s, L.dgate,
+                     L.x, L.T, L.H, L.part);
+    }
     if (e != cudaSuccess || !L.dgate_w) return e;
-    const int splits = (int)std::min<int64_t>(L.T, kBwdPartials);
-    e = launch_k("gate_weight_bwd", gate_weight_kernel, dim3((L.H / 8 + FB_WARPS * 32 - 1) / (FB_WARPS * 32), splits),
-                 dim3(FB_WARPS * 32), 0, s, L.dgate, L.x, L.T, L.H, L.part);
-    if (e != cudaSuccess) return e;
-    return launch_sum_partials(L.part, splits, L.H, L.H, L.dgate_w, nullptr, s);
+    return launch_sum_partials(L.part, parts, L.H, L.H, L.dgate_w, nullptr, s);
 }
 
 cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStream_t s) {

@@ -24,6 +24,7 @@
 #include <algorithm>
 
 #include "moe_internal.cuh"
+#include "moe_row_sums.cuh"
 
 namespace moe {
 namespace {
@@ -131,62 +132,6 @@ __device__ __forceinline__ void nb_put_f32(void* p, const f2 f[2]) {
     *static_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-__device__ __forceinline__ float nb_warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
-
-// Sums of N values (a power of two) over 32 lanes, or (HALF) over lanes 0..15 and over 16..31:
-// half of the values go to the other half of the lanes until one is left, so lane l ends with
-// the sum of v[l / (lanes / N)].
-template <int N, bool HALF>
-__device__ __forceinline__ float nb_sums(float (&v)[N], int lane) {
-    int off = HALF ? 8 : 16;
-#pragma unroll
-    for (int n = N / 2; n > 0; n /= 2, off /= 2) {
-        const bool hi = lane & off;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const float give = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
-            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-        }
-    }
-#pragma unroll
-    for (int o = (HALF ? 8 : 16) / N; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
-    return v[0];
-}
-
-// The group's sums of N values, the same in every thread.  red: N floats a warp of the CTA.
-template <int N, typename Sync>
-__device__ __forceinline__ void nb_group_sums(float (&v)[N], float* red, int gw, int group, int warp, int lane,
-                                              const Sync& sync) {
-    float mine = nb_sums<N, false>(v, lane);
-    if (gw == 1) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / N));
-        return;
-    }
-    if (lane % (32 / N) == 0) red[warp * N + lane / (32 / N)] = mine;
-    sync();
-    const int w = lane & 15;
-    const float* q = red + (group * gw + (w < gw ? w : 0)) * N;
-    if (N == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(q);
-        v[0] = f.x; v[1 % N] = f.y; v[2 % N] = f.z; v[3 % N] = f.w;
-    } else if (N == 2) {
-        const float2 f = *reinterpret_cast<const float2*>(q);
-        v[0] = f.x; v[1 % N] = f.y;
-    } else {
-        v[0] = q[0];
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = w < gw ? v[i] : 0.f;
-    mine = nb_sums<N, true>(v, lane);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (16 / N));
-}
-
 // NP pieces a thread: 8 columns of a bf16 stream, or 4 of an fp32 one (16 bytes either way, so
 // that a warp's copies and stores cover whole lines).  A warp's pieces lie side by side.
 template <int NP, bool F32, bool LN, int KEEP>
@@ -280,7 +225,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
                 for (int i = 0; i < P; ++i) sum = f2_add(sum, r[k][i]);
             }
             float m[1] = {f2_sum(sum)};
-            nb_group_sums<1>(m, red_mean[it], p.gw, group, warp, lane, group_sync);
+            group_sums<1>(m, red_mean[it], p.gw, group * p.gw, warp, lane, group_sync);
             mean = m[0] * -inv_h;
         }
         const f2 off = f2_make(mean, mean);
@@ -305,7 +250,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         sums[0] = f2_sum(sd);
         sums[1] = f2_sum(sgd);
         if (LN) sums[NS - 2] = f2_sum(sg);
-        nb_group_sums<NS>(sums, red[it], p.gw, group, warp, lane, group_sync);
+        group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync);
         const float rstd = rsqrtf(fmaf(sums[0], inv_h, a.eps));
         const float mg = LN ? -sums[NS - 2] * inv_h : 0.f, mgd = -rstd * rstd * (sums[1] * inv_h);
         const f2 rstd2 = f2_make(rstd, rstd), mg2 = f2_make(mg, mg), mgd2 = f2_make(mgd, mgd);
@@ -396,7 +341,7 @@ __global__ void __launch_bounds__(SP_WARPS * 32) sum_partials_kernel(const float
     }
     red[warp][lane] = s;
     __syncthreads();
-    s = nb_warp_sum(red[lane][warp]);
+    s = warp_sum(red[lane][warp]);
     if (lane == 0 && blockIdx.x * 32 + warp < H && out) out[blockIdx.x * 32 + warp] = s;
 }
 
