@@ -90,7 +90,9 @@ __global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid
     const int64_t stride = (int64_t)gridDim.x * groups;
     float sum[2][8] = {};
     uint4 w[2] = {}, next[3][2] = {};
-    pdl_wait();
+    // Starts while finalize_bwd_kernel still runs: that kernel let it start after its own wait, so
+    // what this one reads is there, and neither writes what the other touches.  Its wait at the
+    // end makes its end that of both.
     pdl_trigger();
     const uint16_t* const src[3] = {a.dout, a.y_sh, a.x};
     const auto fetch = [&](int64_t t) {
@@ -142,6 +144,7 @@ __global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid
             reinterpret_cast<uint4*>(a.dy_sh + t * a.H)[col + 32 * j] = pack8(d);
         }
     }
+    pdl_wait();
     if (!a.dgate_w) return;
     float4* const part = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.H);
     for (int g = 0; g < groups; ++g) {
