@@ -22,6 +22,7 @@
 // Narrow rows keep r, dy and the weight in registers from one pass to the next; rows of more
 // columns a thread read them again (the weight from shared memory, in binary32).
 #include <algorithm>
+#include <atomic>
 
 #include "moe_internal.cuh"
 #include "moe_row_sums.cuh"
@@ -316,41 +317,59 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
     }
 }
 
-// A CTA adds 32 columns: warp w takes the partial rows w, w + 32, ..., SP_BATCH of them in
-// flight, then each warp adds one of the columns over the warps' sums.
-constexpr int SP_WARPS = 32, SP_BATCH = 8;
+// A CTA adds 4 * SP_QUADS columns: a thread takes 4 columns of the partial rows l, l + SP_LANES,
+// ..., SP_BATCH of them in flight (so that 152 rows are one round), then the lanes' sums are added
+// in order.
+constexpr int SP_QUADS = 16, SP_LANES = 16, SP_BATCH = 10;
 
-__global__ void __launch_bounds__(SP_WARPS * 32) sum_partials_kernel(const float* part, int n, int64_t stride, int H,
-                                                                   float* out0, float* out1) {
-    __shared__ float red[SP_WARPS][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x * 32 + lane;
+__global__ void __launch_bounds__(SP_QUADS * SP_LANES) sum_partials_kernel(const float* part, int n, int64_t stride,
+                                                                         int H, float* out0, float* out1) {
+    __shared__ float red[SP_LANES][SP_QUADS * 4];
+    const int quad = threadIdx.x % SP_QUADS, lane = threadIdx.x / SP_QUADS;
+    const int first = blockIdx.x * SP_QUADS * 4, col = first + 4 * quad;
     float* out = blockIdx.y ? out1 : out0;
     pdl_wait();
     pdl_trigger();
-    float s = 0.f;
-    if (col < H && out) {
+    if (!out) return;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < H) {
         const float* p = part + (int64_t)blockIdx.y * H + col;
-        for (int i0 = warp; i0 < n; i0 += SP_WARPS * SP_BATCH) {
-            float v[SP_BATCH];
+        for (int i0 = lane; i0 < n; i0 += SP_LANES * SP_BATCH) {
+            float4 v[SP_BATCH];
 #pragma unroll
-            for (int b = 0; b < SP_BATCH; ++b) v[b] = i0 + SP_WARPS * b < n ? p[(i0 + SP_WARPS * b) * stride] : 0.f;
+            for (int b = 0; b < SP_BATCH; ++b) {
+                const int i = i0 + SP_LANES * b;
+                v[b] = i < n ? *reinterpret_cast<const float4*>(p + i * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll
-            for (int b = 0; b < SP_BATCH; ++b) s += v[b];
+            for (int b = 0; b < SP_BATCH; ++b) {
+                s.x += v[b].x; s.y += v[b].y; s.z += v[b].z; s.w += v[b].w;
+            }
         }
     }
-    red[warp][lane] = s;
+    *reinterpret_cast<float4*>(&red[lane][4 * quad]) = s;
     __syncthreads();
-    s = warp_sum(red[lane][warp]);
-    if (lane == 0 && blockIdx.x * 32 + warp < H && out) out[blockIdx.x * 32 + warp] = s;
+    if (threadIdx.x < SP_QUADS * 4 && first + threadIdx.x < H) {
+        float t = 0.f;
+#pragma unroll
+        for (int l = 0; l < SP_LANES; ++l) t += red[l][threadIdx.x];
+        out[first + threadIdx.x] = t;
+    }
 }
 
 template <int NP, bool F32, bool LN, int KEEP>
 cudaError_t launch_norm_bwd_kernel(const NormBwdLaunch& L, const NormBwdPlan& p, size_t smem, int num_sms,
                                    cudaStream_t s) {
     const auto kernel = norm_bwd_kernel<NP, F32, LN, KEEP>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> granted[64];  // per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !granted[dev].load()) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)NB_SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) granted[dev].store(true);
+    }
     const int grid = (int)std::min<int64_t>((L.T + p.groups - 1) / p.groups, std::min(num_sms, kBwdPartials));
     e = launch_k(LN ? "layernorm_bwd" : "rmsnorm_bwd", kernel, dim3(grid), dim3(p.gw * p.groups * 32), smem, s, L, p);
     if (e != cudaSuccess || (!L.dweight && !L.dbias)) return e;
@@ -394,7 +413,8 @@ cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream
 
 cudaError_t launch_sum_partials(const float* part, int n, int64_t stride, int H, float* out0, float* out1,
                                 cudaStream_t s) {
-    return launch_k("sum_partials", sum_partials_kernel, dim3((H + 31) / 32, out1 ? 2 : 1), dim3(SP_WARPS * 32), 0, s,
+    return launch_k("sum_partials", sum_partials_kernel, dim3((H + 4 * SP_QUADS - 1) / (4 * SP_QUADS), out1 ? 2 : 1),
+                    dim3(SP_QUADS * SP_LANES), 0, s,
                     part, n, stride, H, out0, out1);
 }
 
