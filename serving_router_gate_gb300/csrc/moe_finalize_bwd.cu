@@ -11,7 +11,7 @@
 #include <algorithm>
 
 #include "moe_internal.cuh"
-#include "moe_row_sums.cuh"
+#include "moe_rows.cuh"
 
 namespace moe {
 namespace {
@@ -222,14 +222,19 @@ __global__ void __launch_bounds__(FB_WARPS * 32) gate_weight_kernel(const float*
 }
 
 // A token's row is spread over `split` of a CTA's warps (1, 2, 4 or 8).  A warp first lists
-// its token's pairs that have a row, then takes two vectors of 8 values a lane at a time,
-// PB_BATCH pairs' rows of both in flight before they are used.  MAXK: k at most; DW: with
+// its token's pairs that have a row, then takes U vectors of 8 values a lane at a time, with
+// PB_LOADS of the pairs' vectors in flight before they are used.  MAXK: k at most; DW: with
 // the weights' gradients, a lane's share of every pair's dot product stays in a register.
-constexpr int PB_BATCH = 4;
+// U and the CTAs an SM are those that measured best: without DW 2 and 3 (8191 tokens of 7168,
+// half of 8 pairs: 121 us; 1 and 4: 122, 2 and 2: 130), with it 1 and 4, which leaves 64
+// registers for 32 warps an SM (4096 tokens of 7168, 8 pairs: 106 us; 2 and 3: 118, 1 and 3:
+// 119, 2 and 2: 138).
+constexpr int PB_LOADS = 8;
 
-template <int MAXK, bool DW>
-__global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a,
+template <int MAXK, bool DW, int U, int CTAS>
+__global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a,
                                                                   int split) {
+    constexpr int BATCH = PB_LOADS / U;
     __shared__ int32_t s_row[FB_WARPS][MAXK], s_pair[FB_WARPS][MAXK];
     __shared__ float s_w[FB_WARPS][MAXK], s_dot[FB_WARPS][DW ? MAXK : 1];
     pdl_wait();
@@ -258,18 +263,18 @@ __global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid
         float dot[DW ? MAXK : 1] = {};
         const float dz = live_t && a.dgate ? a.dgate[t] : 0.f;
         const int last = live_t ? vec : 0;
-        for (int v0 = part * 64 + lane; v0 < last; v0 += split * 64) {
-            const bool two = v0 + 32 < vec;
+        for (int v0 = part * 32 * U + lane; v0 < last; v0 += split * 32 * U) {
+            const bool two = U > 1 && v0 + 32 < vec;
             const int64_t at = t * a.H + 8 * v0;
-            uint4 xp[2];
-            float acc[2][8] = {};
+            uint4 xp[U];
+            float acc[U][8] = {};
             if (DW) {
                 xp[0] = *reinterpret_cast<const uint4*>(a.x + at);  // not __ldg: dx may be x
-                xp[1] = two ? reinterpret_cast<const uint4*>(a.x + at)[32] : make_uint4(0, 0, 0, 0);
+                if (U > 1) xp[U - 1] = two ? reinterpret_cast<const uint4*>(a.x + at)[32] : make_uint4(0, 0, 0, 0);
             }
             if (a.add) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < U; ++u) {
                     if (u && !two) continue;
                     if (a.add_f32) {
                         const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.add) + at + 256 * u);
@@ -282,35 +287,35 @@ __global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid
                 }
             }
 #pragma unroll
-            for (int j0 = 0; j0 < MAXK; j0 += PB_BATCH) {
+            for (int j0 = 0; j0 < MAXK; j0 += BATCH) {
                 if (j0 >= n) break;
-                uint4 ld[PB_BATCH][2];
+                uint4 ld[BATCH][U];
 #pragma unroll
-                for (int b = 0; b < PB_BATCH; ++b) {
+                for (int b = 0; b < BATCH; ++b) {
                     const bool ok = j0 + b < n;
                     const uint4* q = reinterpret_cast<const uint4*>(a.dx_perm + (ok ? (int64_t)s_row[warp][j0 + b] * a.H : 0)) + v0;
                     ld[b][0] = ok ? __ldg(q) : make_uint4(0, 0, 0, 0);
-                    ld[b][1] = ok && two ? __ldg(q + 32) : make_uint4(0, 0, 0, 0);
+                    if (U > 1) ld[b][U - 1] = ok && two ? __ldg(q + 32) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int b = 0; b < PB_BATCH; ++b) {
+                for (int b = 0; b < BATCH; ++b) {
                     if (j0 + b >= n) continue;
                     const float wj = s_w[warp][j0 + b];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
+                    for (int u = 0; u < U; ++u) {
                         float d[8], x[8];
                         unpack8(ld[b][u], d);
                         if (DW) unpack8(xp[u], x);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             acc[u][i] = fmaf(wj, d[i], acc[u][i]);
-                            if (DW) dot[j0 + b] = fmaf(x[i], d[i], dot[j0 + b]);
+                            if (DW) dot[DW ? j0 + b : 0] = fmaf(x[i], d[i], dot[DW ? j0 + b : 0]);
                         }
                     }
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 if (u && !two) continue;
                 if (a.dgate) {
                     float g[8];
@@ -322,13 +327,8 @@ __global__ void __launch_bounds__(FB_WARPS * 32) permute_bwd_kernel(const __grid
             }
         }
         if (DW) {
-            float mine = 0.f;
-#pragma unroll
-            for (int j = 0; j < MAXK; ++j) {
-                if (j >= n) break;
-                const float d = warp_sum(dot[j]);
-                if (lane == j) mine = d;
-            }
+            float mine = lane_sums<DW ? MAXK : 1, false>(dot, lane);  // to lane j: the sum of pair j
+            mine = __shfl_sync(0xffffffffu, mine, lane * (32 / MAXK) & 31);
             if (split > 1) {
                 if (lane < n) s_dot[warp][lane] = mine;
                 __syncthreads();
@@ -370,13 +370,17 @@ cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& L, int num_sms, cudaStr
 }
 
 cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStream_t s) {
-    // a row over as many warps as still leave two CTAs an SM
+    // A row over as many warps as give every SM a CTA, and where a warp keeps seven vectors a lane
+    // of it, as many as give every SM eight: shorter last waves (4096 tokens of 7168, 8 pairs: 106
+    // us in four parts, 108 in one; without the weights' gradients 81 and 98).
     int split = 1;
-    while (split < FB_WARPS && L.T * split < 2LL * num_sms * FB_WARPS) split *= 2;
+    while (split < FB_WARPS && (L.T * split < (int64_t)num_sms * FB_WARPS ||
+                                (L.T * split < 8LL * num_sms * FB_WARPS && L.H / 8 >= 2 * split * 7 * 32)))
+        split *= 2;
     const int tokens = FB_WARPS / split;
     const unsigned grid = (unsigned)std::min<int64_t>((L.T + tokens - 1) / tokens, (int64_t)num_sms * 64);
-    const auto kernel = L.k <= 8 ? (L.dw ? permute_bwd_kernel<8, true> : permute_bwd_kernel<8, false>)
-                                 : (L.dw ? permute_bwd_kernel<32, true> : permute_bwd_kernel<32, false>);
+    const auto kernel = L.k <= 8 ? (L.dw ? permute_bwd_kernel<8, true, 1, 4> : permute_bwd_kernel<8, false, 2, 3>)
+                                 : (L.dw ? permute_bwd_kernel<32, true, 1, 2> : permute_bwd_kernel<32, false, 2, 3>);
     return launch_k("permute_bwd", kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L, split);
 }
 

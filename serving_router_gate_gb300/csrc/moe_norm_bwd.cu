@@ -25,7 +25,7 @@
 #include <atomic>
 
 #include "moe_internal.cuh"
-#include "moe_row_sums.cuh"
+#include "moe_rows.cuh"
 
 namespace moe {
 namespace {
@@ -57,40 +57,6 @@ __device__ __forceinline__ void cp_async_wait_upto(int n) {  // n uniform, at mo
     else if (n == 1) cp_async_wait<1>();
     else if (n == 2) cp_async_wait<2>();
     else cp_async_wait<3>();
-}
-
-// Pairs of binary32 values.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 f2_make(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f2_split(f2 v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float f2_sum(f2 v) {
-    float lo, hi;
-    f2_split(v, lo, hi);
-    return lo + hi;
-}
-__device__ __forceinline__ f2 f2_bf16(uint32_t w) {
-    return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 // C values: a piece of a bf16 row (C = 8: 16 bytes, C = 4: 8 bytes) or of an fp32 one (C = 4).

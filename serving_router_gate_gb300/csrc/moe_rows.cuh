@@ -1,10 +1,58 @@
-// moe_row_sums.cuh -- sums of a row's values over the lanes of a warp and over a group of
-// warps, in a fixed order, for the gradient kernels.
+// moe_rows.cuh -- for the gradient kernels: arithmetic on pairs of binary32 values, and the sums
+// of a row's values over the lanes of a warp and over a group of warps, in a fixed order.
 #pragma once
 
 #include "moe_internal.cuh"
 
 namespace moe {
+
+// Pairs of binary32 values.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_split(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    float lo, hi;
+    f2_split(v, lo, hi);
+    return lo + hi;
+}
+// Two bf16 values, the first in the lower half.
+__device__ __forceinline__ f2 f2_bf16(uint32_t w) {
+    return f2_make(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void f2_unpack(const uint4& v, f2 f[4]) {
+    f[0] = f2_bf16(v.x);
+    f[1] = f2_bf16(v.y);
+    f[2] = f2_bf16(v.z);
+    f[3] = f2_bf16(v.w);
+}
+__device__ __forceinline__ uint4 f2_pack(const f2 f[4]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_split(f[i], v[2 * i], v[2 * i + 1]);
+    return pack8(v);
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
