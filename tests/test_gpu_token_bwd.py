@@ -343,6 +343,25 @@ def test_route_bwd_bad_ids_are_left_out_and_flagged(renorm):
     assert torch.equal(got, want) and _status(ws) == moe.MOE_ERR_DEVICE_BOUNDS
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_bwd_an_expert_named_twice_gets_the_sum(renorm):
+    logits, ids, w, dw = _route_inputs(40, 60, 6, renorm, seed=5)
+    twice = ids.clone()
+    twice[::2, 4] = twice[::2, 1]
+    twice[::3, 5] = twice[::3, 1]
+    got = _route(logits, twice, w, dw, renorm, _ws())
+    wd = (w * dw).double()
+    c, mag = wd.sum(1, keepdim=True), wd.abs().sum(1, keepdim=True)
+    p = torch.softmax(logits.double(), 1)
+    if renorm:
+        p = torch.zeros_like(p).scatter_add_(1, twice.long(), w.double())
+    want = (-c * p).scatter_add_(1, twice.long(), wd)
+    own = torch.zeros_like(p).scatter_add_(1, twice.long(), wd.abs())
+    ref.inside(got, want, 2.0 ** -18 * (own + mag * p) + 1e-37, "dlogits")
+    again = _route(logits, twice, w, dw, renorm, _ws())
+    assert torch.equal(got, again)
+
+
 def test_route_bwd_of_the_routers_own_weights():
     T, H, E, k = 50, 256, 60, 4
     x, Wg = ref.rnd(T, H, seed=1), ref.rnd(E, H, seed=2, std=0.05, dtype=torch.float32)
