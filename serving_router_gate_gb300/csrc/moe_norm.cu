@@ -1,9 +1,10 @@
 // moe_norm.cu -- the norm in front of an MoE block: the residual's addition, the
-// root-mean-square norm of the sum, and optionally the normalised rows in E4M3
-// with one power-of-two scale per row.  Per row of H values
+// root-mean-square norm or the layer norm of the sum, and optionally the normalised rows in
+// E4M3 with one power-of-two scale per row.  Per row of H values
 //
 //   r = residual + x                        (binary32; stored in the stream's type)
-//   y = (r * rstd) * w,  rstd = 1 / sqrt(sum(r^2) / H + eps)
+//   d = r (RMS norm), r - sum(r) / H (layer norm)
+//   y = (d * rstd) * w [+ b],  rstd = 1 / sqrt(sum(d^2) / H + eps)
 //   y_bf16 = bf16(y)
 //   e = the smallest integer >= -126 with max|y| <= 448 * 2^e
 //   q = e4m3(y * 2^-e), scale = 2^e
@@ -79,7 +80,7 @@ __device__ __forceinline__ float nm_row_sum(float v, float* red) {
 // THREADS threads per row at a time, each with VPT vectors of 8 values (grid-stride over
 // rows): a CTA, or (THREADS = 32) each of its NM_WARPS warps by itself.
 template <int VPT, int THREADS, bool F32, bool LN>
-__global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_norm_kernel(const __grid_constant__ NormLaunch a) {
+__device__ __forceinline__ void add_norm(const NormLaunch& a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ float red_sum[2][WARPS];
     __shared__ float red_mean[2][LN ? WARPS : 1];
@@ -151,8 +152,8 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_no
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float d = LN ? f[j][i] - mean : f[j][i];
-                f[j][i] = fmaf(d, hi, d * lo) * w[i];
-                if (LN) f[j][i] += b[i];
+                const float n = fmaf(d, hi, d * lo);
+                f[j][i] = LN ? fmaf(n, w[i], b[i]) : n * w[i];
                 mx = max(mx, __float_as_uint(f[j][i]) & 0x7FFFFFFFu);
             }
             if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = pack8(f[j]);
@@ -178,11 +179,29 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_no
     }
 }
 
-template <int VPT, int THREADS, bool F32, bool LN>
+constexpr int nm_threads(int threads) { return threads > 32 ? threads : NM_WARPS * 32; }
+
+template <int VPT, int THREADS, bool F32>
+__global__ void __launch_bounds__(nm_threads(THREADS)) add_rmsnorm_kernel(const __grid_constant__ NormLaunch a) {
+    add_norm<VPT, THREADS, F32, false>(a);
+}
+
+// CTAS CTAs an SM: the layer norm's second reduction wants more rows on their way than the
+// registers would leave by themselves.
+template <int VPT, int THREADS, bool F32, int CTAS>
+__global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kernel(const __grid_constant__ NormLaunch a) {
+    add_norm<VPT, THREADS, F32, true>(a);
+}
+
+template <int VPT, int THREADS, bool F32, bool LN, int CTAS>
 cudaError_t launch_norm_size(const NormLaunch& L, int num_sms, cudaStream_t s) {
     constexpr int ROWS = THREADS == 32 ? NM_WARPS : 1;
     const unsigned grid = (unsigned)std::min<int64_t>((L.T + ROWS - 1) / ROWS, (int64_t)num_sms * NM_CTAS);
-    return launch_k(LN ? "add_layernorm" : "add_rmsnorm", add_norm_kernel<VPT, THREADS, F32, LN>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
+    if constexpr (LN)
+        return launch_k("add_layernorm", add_layernorm_kernel<VPT, THREADS, F32, CTAS>, dim3(grid), dim3(THREADS * ROWS), 0,
+                        s, L);
+    else
+        return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, THREADS, F32>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
 }
 
 template <bool F32, bool LN>
@@ -194,14 +213,31 @@ cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // widths of these forms run at (16384 rows, of the copy rate): 4096 0.99, 5120 (a vector of
     // four idle) 0.90, 6144 0.90, and at 1.06 GB 8192 0.91, 16384 0.84.
     const int vec = L.H / 8;
-    if (vec <= 32) return launch_norm_size<1, 32, F32, LN>(L, num_sms, s);
-    if (vec <= 64) return launch_norm_size<2, 32, F32, LN>(L, num_sms, s);
-    if (vec <= 128) return launch_norm_size<1, 128, F32, LN>(L, num_sms, s);
-    if (vec <= 256) return launch_norm_size<1, 256, F32, LN>(L, num_sms, s);
-    if (vec <= 512) return launch_norm_size<2, 256, F32, LN>(L, num_sms, s);
-    if (vec <= 896) return launch_norm_size<4, 224, F32, LN>(L, num_sms, s);
-    if (vec <= 1024) return launch_norm_size<4, 256, F32, LN>(L, num_sms, s);
-    return launch_norm_size<4, 512, F32, LN>(L, num_sms, s);
+    // 58.7 M elements with E4M3 rows, fp32 / bf16 stream, us (114 / 79 at the copy rate): 512 66 / 51,
+    // 1024 116 / 81, 1408 117 / 98, 2048 116 / 81, 4096 113 / 85, 5120 117 / 85, 6144 117 / 92, 7168
+    // 122 / 93 (three CTAs of 448 threads 121 / 100, four of 224 127 / 103), 8192 122 / 96, 16384 135 / 104.
+    if constexpr (LN) {
+        if (vec <= 32) return launch_norm_size<1, 32, F32, true, 6>(L, num_sms, s);
+        if (vec <= 64) return launch_norm_size<2, 32, F32, true, 6>(L, num_sms, s);
+        if (vec <= 128) return launch_norm_size<1, 128, F32, true, 16>(L, num_sms, s);
+        if (vec <= 256) return launch_norm_size<2, 128, F32, true, 12>(L, num_sms, s);
+        if (vec <= 512) return launch_norm_size<2, 256, F32, true, 6>(L, num_sms, s);
+        if (vec <= 640) return launch_norm_size<2, 320, F32, true, 5>(L, num_sms, s);
+        if (vec <= 768) return launch_norm_size<2, 384, F32, true, 4>(L, num_sms, s);
+        if (vec <= 896) return launch_norm_size<4, 224, F32, true, 5>(L, num_sms, s);
+        if (vec <= 1024) return launch_norm_size<2, 512, F32, true, 3>(L, num_sms, s);
+        if (vec <= 1536) return launch_norm_size<4, 384, F32, true, 3>(L, num_sms, s);
+        return launch_norm_size<4, 512, F32, true, 2>(L, num_sms, s);
+    } else {
+        if (vec <= 32) return launch_norm_size<1, 32, F32, false, 0>(L, num_sms, s);
+        if (vec <= 64) return launch_norm_size<2, 32, F32, false, 0>(L, num_sms, s);
+        if (vec <= 128) return launch_norm_size<1, 128, F32, false, 0>(L, num_sms, s);
+        if (vec <= 256) return launch_norm_size<1, 256, F32, false, 0>(L, num_sms, s);
+        if (vec <= 512) return launch_norm_size<2, 256, F32, false, 0>(L, num_sms, s);
+        if (vec <= 896) return launch_norm_size<4, 224, F32, false, 0>(L, num_sms, s);
+        if (vec <= 1024) return launch_norm_size<4, 256, F32, false, 0>(L, num_sms, s);
+        return launch_norm_size<4, 512, F32, false, 0>(L, num_sms, s);
+    }
 }
 
 }  // namespace
