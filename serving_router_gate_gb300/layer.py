@@ -14,7 +14,7 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_NONLOCAL_SKIP, moe_add_rmsnorm, moe_forward, moe_forward_fp8, moe_forward_nvfp4, moe_forward_w4,
+from . import (MOE_NONLOCAL_SKIP, moe_add_layernorm, moe_add_rmsnorm, moe_forward, moe_forward_fp8, moe_forward_nvfp4, moe_forward_w4,
                moe_forward_w8a8, moe_forward_w8a8_rows, moe_permute, moe_quantize_fp8_rows, moe_quantize_nvfp4_rows,
                moe_quantize_w4_rows, moe_route, moe_route_grouped, moe_workspace_init, moe_workspace_size,
                moe_workspace_size_w4, nvfp4_sf_row_bytes)
@@ -29,7 +29,7 @@ class MoELayer:
                  W2s: Optional[torch.Tensor] = None, shared_gate_w: Optional[torch.Tensor] = None,
                  on_input: bool = False, n_group: int = 1, topk_group: int = 1, fp8: bool = False,
                  act8: bool = False, fp4: bool = False, w4: int = 0, norm_w: Optional[torch.Tensor] = None,
-                 norm_eps: float = 1e-6):
+                 norm_eps: float = 1e-6, layer_norm: bool = False, norm_b: Optional[torch.Tensor] = None):
         self.Wg, self.W1, self.W2 = Wg, W1, W2
         # routing applied on the input: rows scaled by the weights, outputs summed unweighted
         self.on_input = bool(on_input)
@@ -119,9 +119,15 @@ class MoELayer:
             self.W1w4, self.W2w4 = quant_w4(W1), quant_w4(W2)
             if W1s is not None:
                 self.W1sw4, self.W2sw4 = quant_w4(W1s), quant_w4(W2s)
-        # the norm in front of the layer (block()): its rows in bf16 for the router and, for
-        # E4M3 activations with the weights at the output, in E4M3 for the experts
+        # the norm in front of the layer (block()), RMS or (layer_norm) a layer norm, with bias norm_b
+        # or without: its rows in bf16 for the router and, for E4M3 activations with the weights at
+        # the output, in E4M3 for the experts
+        if (layer_norm or norm_b is not None) and norm_w is None:
+            raise ValueError("a layer norm needs norm_w")
+        if norm_b is not None and not layer_norm:
+            raise ValueError("norm_b belongs to a layer norm (layer_norm=True)")
         self.norm_w, self.norm_eps = norm_w, float(norm_eps)
+        self.layer_norm, self.norm_b = bool(layer_norm), norm_b
         self.x_norm = self.x_q = self.x_scale = None
         if norm_w is not None:
             self.x_norm = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
@@ -250,8 +256,8 @@ class MoELayer:
     def block(self, x: torch.Tensor, residual: torch.Tensor, stream=None,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
         """The norm and the layer: residual [T, H] (bf16 or fp32) becomes residual + x in place, and the layer's
-        forward of its RMS norm (norm_w, norm_eps) is returned.  With E4M3 activations the experts read the norm's own
-        E4M3 rows (rounded once, from the unrounded norm)."""
+        forward of its norm (norm_w, norm_eps; RMS, or a layer norm) is returned.  With E4M3 activations the experts
+        read the norm's own E4M3 rows (rounded once, from the unrounded norm)."""
         self.check_block()
         T = x.shape[0]
         assert T <= self.max_T and x.shape[1] == self.H
@@ -259,7 +265,10 @@ class MoELayer:
             return self.out[:0] if out is None else out
         xn = self.x_norm[:T]
         xq, xs = (None, None) if self.x_q is None else (self.x_q[:T], self.x_scale[:T])
-        moe_add_rmsnorm(x, residual, self.norm_w, self.norm_eps, residual, xn, xq, xs, stream)
+        if self.layer_norm:
+            moe_add_layernorm(x, residual, self.norm_w, self.norm_b, self.norm_eps, residual, xn, xq, xs, stream)
+        else:
+            moe_add_rmsnorm(x, residual, self.norm_w, self.norm_eps, residual, xn, xq, xs, stream)
         self.route(xn, stream)
         self.permute(xn, stream)
         return self.expert_forward(xn, stream, out, xq, xs)["out"]
