@@ -226,6 +226,34 @@ def test_bwd_on_another_stream_and_in_graphs(ln, H):
             assert all(a is None or torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.parametrize("ln", [False, True])
+def test_bwd_two_calls_at_once_beside_other_work(ln):
+    """Two streams with a workspace each, and a third that keeps the GPU busy: the CTAs' sums are added whoever gets to
+    run, and always in one order."""
+    shapes = [(1700, 2048), (300, 512), (3000, 1024), (20, 7168)]
+    data, want = [], []
+    for i, (T, H) in enumerate(shapes):
+        r, w, _, dy = _inputs(T, H, False, seed=30 + i)
+        data.append((dy, r, w))
+        want.append(_run(ln, dy, r, w, None))
+    outs = [[[torch.zeros_like(t) if t is not None else None for t in w] for w in want] for _ in range(2)]
+    spaces = [_ws(7168), _ws(7168)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    a = ref.rnd(2048, 2048, seed=1)
+    torch.cuda.synchronize()
+    for _ in range(25):
+        with torch.cuda.stream(streams[2]):
+            a @ a
+        for i, d in enumerate(data):
+            for s in range(2):
+                _bwd(ln, *d, None, *outs[s][i], spaces[s], stream=streams[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for got, w in zip(outs[s], want):
+            assert all(g is None or torch.equal(g, x) for g, x in zip(got, w))
+        assert moe.moe_get_device_status(spaces[s]) == 0 and not spaces[s][:moe.MOE_WS_HEADER_BYTES].any()
+
+
 def test_bwd_binding_refuses_what_it_would_misread():
     r, w, _, dy = _inputs(4, 64, False)
     dr, dx, dw, ws = torch.empty_like(r), torch.empty_like(dy), torch.empty(64, device="cuda"), _ws(64)
