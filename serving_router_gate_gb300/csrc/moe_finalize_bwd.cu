@@ -26,10 +26,15 @@ __device__ __forceinline__ int32_t pair_row_of(const int32_t* pair_row, int64_t 
 }
 
 // A warp to a pair; FB_BATCH vectors of dout and of y a lane in flight before they are used.
+//
+// gate_first: launched behind gate_bwd_kernel, this kernel runs beside it.  It may start once
+// every CTA of that one has passed its own wait, so all they both read is there; neither writes
+// what the other touches; and the wait of one CTA at its end makes this kernel's end that of
+// both, for whatever is launched behind it.
 constexpr int FB_BATCH = 4;
 
 __global__ void __launch_bounds__(FB_WARPS * 32) finalize_bwd_kernel(const __grid_constant__ FinalizeBwdLaunch a) {
-    pdl_wait();
+    if (!a.gate_first) pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
     const int64_t pairs = a.T * a.k;
@@ -69,13 +74,17 @@ __global__ void __launch_bounds__(FB_WARPS * 32) finalize_bwd_kernel(const __gri
             if (lane == 0) a.dw[u] = dot;
         }
     }
+    if (a.gate_first && blockIdx.x == 0) pdl_wait();
 }
 
 // The gated shared expert of rows of at most GB_MAX_H values: a group of gw warps to a token,
 // 16 columns a thread (the same ones of every token, so that the gate weight's sums stay in
 // registers over a persistent grid), the next token's rows in flight.  A CTA's groups add
-// their sums in order, the CTAs' are added by another kernel.
-constexpr int GB_WARPS = 16, GB_MAX_H = GB_WARPS * 512;
+// their sums in order, the CTAs' are added by another kernel.  A CTA an SM of GB_CTA_WARPS
+// warps (more only for rows that need them) leaves room for the pairs' CTAs beside it: 4096
+// tokens of 2048, 4 pairs, 35.5 us in all with 8 warps, 38 with 12, 39.6 with 16, 40.6 with 4;
+// 39.1 one behind the other.
+constexpr int GB_WARPS = 16, GB_MAX_H = GB_WARPS * 512, GB_CTA_WARPS = 8;
 
 __device__ __forceinline__ float gate_of(float z) { return 1.f / (1.f + expf(-z)); }
 
@@ -90,9 +99,7 @@ __global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid
     const int64_t stride = (int64_t)gridDim.x * groups;
     float sum[2][8] = {};
     uint4 w[2] = {}, next[3][2] = {};
-    // Starts while finalize_bwd_kernel still runs: that kernel let it start after its own wait, so
-    // what this one reads is there, and neither writes what the other touches.  Its wait at the
-    // end makes its end that of both.
+    pdl_wait();
     pdl_trigger();
     const uint16_t* const src[3] = {a.dout, a.y_sh, a.x};
     const auto fetch = [&](int64_t t) {
@@ -144,7 +151,6 @@ __global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid
             reinterpret_cast<uint4*>(a.dy_sh + t * a.H)[col + 32 * j] = pack8(d);
         }
     }
-    pdl_wait();
     if (!a.dgate_w) return;
     float4* const part = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.H);
     for (int g = 0; g < groups; ++g) {
@@ -346,17 +352,22 @@ __global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const 
 
 }  // namespace
 
-cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& L, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((L.T * L.k + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
-    cudaError_t e = launch_k("finalize_bwd", finalize_bwd_kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L);
-    if (e != cudaSuccess || !L.gate_w) return e;
-    int parts;
-    if (L.H <= GB_MAX_H) {
-        const int gw = (L.H + 511) / 512, groups = GB_WARPS / gw;
+cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& given, int num_sms, cudaStream_t s) {
+    FinalizeBwdLaunch L = given;
+    L.gate_first = L.gate_w && L.H <= GB_MAX_H;
+    int parts = 0;
+    cudaError_t e;
+    if (L.gate_first) {
+        const int gw = (L.H + 511) / 512, groups = std::max(1, GB_CTA_WARPS / gw);
         parts = (int)std::min<int64_t>((L.T + groups - 1) / groups, std::min(num_sms, kBwdPartials));
         e = launch_k("gate_bwd", gate_bwd_kernel, dim3(parts), dim3(gw * groups * 32),
                      groups > 1 ? (size_t)L.H * 4 : 0, s, L, gw, groups);
-    } else {
+        if (e != cudaSuccess) return e;
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T * L.k + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
+    e = launch_k("finalize_bwd", finalize_bwd_kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L);
+    if (e != cudaSuccess || !L.gate_w) return e;
+    if (!L.gate_first) {
         const unsigned rows = (unsigned)std::min<int64_t>((L.T + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
         e = launch_k("gate_rows_bwd", gate_rows_kernel, dim3(rows), dim3(FB_WARPS * 32), 0, s, L);
         if (e != cudaSuccess || !L.dgate_w) return e;

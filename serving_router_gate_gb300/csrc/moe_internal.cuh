@@ -671,6 +671,7 @@ struct FinalizeBwdLaunch {
     float* dgate_w;           // [H], or null
     float* part;              // [kBwdPartials][H] scratch, with dgate_w
     WsHeader* hdr;
+    bool gate_first = false;  // set by launch_finalize_bwd: the shared expert's kernel runs beside the pairs'
 };
 cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& L, int num_sms, cudaStream_t s);
 
