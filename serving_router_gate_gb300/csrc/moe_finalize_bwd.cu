@@ -231,16 +231,18 @@ __global__ void __launch_bounds__(FB_WARPS * 32) gate_weight_kernel(const float*
 // its token's pairs that have a row, then takes U vectors of 8 values a lane at a time, with
 // PB_LOADS of the pairs' vectors in flight before they are used.  MAXK: k at most; DW: with
 // the weights' gradients, a lane's share of every pair's dot product stays in a register.
-// U and the CTAs an SM are those that measured best: without DW 2 and 3 (8191 tokens of 7168,
-// half of 8 pairs: 121 us; 1 and 4: 122, 2 and 2: 130), with it 1 and 4, which leaves 64
-// registers for 32 warps an SM (4096 tokens of 7168, 8 pairs: 106 us; 2 and 3: 118, 1 and 3:
-// 119, 2 and 2: 138).
+// U and the CTAs an SM are those that measured best.  Up to 8 pairs, without DW 2 and 3 (8191
+// tokens of 7168, half of 8 pairs: 121 us; 1 and 4: 122, 2 and 2: 130), with it 1 and 4, which
+// leaves 64 registers for 32 warps an SM (4096 tokens of 7168, 8 pairs: 106 us; 2 and 3: 118, 1
+// and 3: 119, 2 and 2: 138).  Up to 4 pairs 1 and 5 (16384 tokens of 2048, 4 pairs, DW: 68 us; 2
+// and 3: 69, 1 and 4: 74), up to 2 pairs 2 and 4 (16384 tokens of 4096, 2 pairs, DW: 88 us; 4
+// and 2: 89, 4 and 3: 95, as for 8 pairs: 100).
 constexpr int PB_LOADS = 8;
 
 template <int MAXK, bool DW, int U, int CTAS>
 __global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a,
                                                                   int split) {
-    constexpr int BATCH = PB_LOADS / U;
+    constexpr int BATCH = PB_LOADS / U < MAXK ? PB_LOADS / U : MAXK;
     __shared__ int32_t s_row[FB_WARPS][MAXK], s_pair[FB_WARPS][MAXK];
     __shared__ float s_w[FB_WARPS][MAXK], s_dot[FB_WARPS][DW ? MAXK : 1];
     pdl_wait();
@@ -270,18 +272,19 @@ __global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const 
         const float dz = live_t && a.dgate ? a.dgate[t] : 0.f;
         const int last = live_t ? vec : 0;
         for (int v0 = part * 32 * U + lane; v0 < last; v0 += split * 32 * U) {
-            const bool two = U > 1 && v0 + 32 < vec;
+            const auto in = [&](int u) { return u == 0 || v0 + 32 * u < vec; };
             const int64_t at = t * a.H + 8 * v0;
             uint4 xp[U];
             float acc[U][8] = {};
             if (DW) {
-                xp[0] = *reinterpret_cast<const uint4*>(a.x + at);  // not __ldg: dx may be x
-                if (U > 1) xp[U - 1] = two ? reinterpret_cast<const uint4*>(a.x + at)[32] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int u = 0; u < U; ++u)  // not __ldg: dx may be x
+                    xp[u] = in(u) ? reinterpret_cast<const uint4*>(a.x + at)[32 * u] : make_uint4(0, 0, 0, 0);
             }
             if (a.add) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    if (u && !two) continue;
+                    if (!in(u)) continue;
                     if (a.add_f32) {
                         const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(a.add) + at + 256 * u);
                         const float4 lo = q[0], hi = q[1];
@@ -300,8 +303,8 @@ __global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const 
                 for (int b = 0; b < BATCH; ++b) {
                     const bool ok = j0 + b < n;
                     const uint4* q = reinterpret_cast<const uint4*>(a.dx_perm + (ok ? (int64_t)s_row[warp][j0 + b] * a.H : 0)) + v0;
-                    ld[b][0] = ok ? __ldg(q) : make_uint4(0, 0, 0, 0);
-                    if (U > 1) ld[b][U - 1] = ok && two ? __ldg(q + 32) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) ld[b][u] = ok && in(u) ? __ldg(q + 32 * u) : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
                 for (int b = 0; b < BATCH; ++b) {
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const 
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (u && !two) continue;
+                if (!in(u)) continue;
                 if (a.dgate) {
                     float g[8];
                     unpack8(__ldg(reinterpret_cast<const uint4*>(a.gate_w) + v0 + 32 * u), g);
@@ -381,18 +384,22 @@ cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& given, int num_sms, cud
 }
 
 cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStream_t s) {
-    // A row over as many warps as give every SM a CTA, and where a warp keeps seven vectors a lane
+    // A row over as many warps as give every SM a CTA, and where a warp keeps five vectors a lane
     // of it, as many as give every SM eight: shorter last waves (4096 tokens of 7168, 8 pairs: 106
     // us in four parts, 108 in one; without the weights' gradients 81 and 98).
     int split = 1;
     while (split < FB_WARPS && (L.T * split < (int64_t)num_sms * FB_WARPS ||
-                                (L.T * split < 8LL * num_sms * FB_WARPS && L.H / 8 >= 2 * split * 7 * 32)))
+                                (L.T * split < 8LL * num_sms * FB_WARPS && L.H / 8 >= 2 * split * 5 * 32)))
         split *= 2;
     const int tokens = FB_WARPS / split;
     const unsigned grid = (unsigned)std::min<int64_t>((L.T + tokens - 1) / tokens, (int64_t)num_sms * 64);
-    const auto kernel = L.k <= 8 ? (L.dw ? permute_bwd_kernel<8, true, 1, 4> : permute_bwd_kernel<8, false, 2, 3>)
-                                 : (L.dw ? permute_bwd_kernel<32, true, 1, 2> : permute_bwd_kernel<32, false, 2, 3>);
-    return launch_k("permute_bwd", kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L, split);
+    const auto go = [&](auto kernel) {
+        return launch_k("permute_bwd", kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L, split);
+    };
+    if (L.k <= 2) return L.dw ? go(permute_bwd_kernel<2, true, 2, 4>) : go(permute_bwd_kernel<2, false, 2, 4>);
+    if (L.k <= 4) return L.dw ? go(permute_bwd_kernel<4, true, 1, 5>) : go(permute_bwd_kernel<4, false, 1, 5>);
+    if (L.k <= 8) return L.dw ? go(permute_bwd_kernel<8, true, 1, 4>) : go(permute_bwd_kernel<8, false, 2, 3>);
+    return L.dw ? go(permute_bwd_kernel<32, true, 1, 2>) : go(permute_bwd_kernel<32, false, 2, 3>);
 }
 
 }  // namespace moe
