@@ -509,7 +509,9 @@ MOE_API moe_status_t moe_add_layernorm_bwd(const moe_bf16_t *dy, const void *r, 
  *   dout     [T, H] bf16, pair_row [T, k] int32, topk_w [T, k] fp32 or NULL (weight 1)
  *   y        [rows_cap, H] bf16; read for dtopk_w only (else it may be NULL)
  *   dy       [rows_cap, H] bf16 out; rows that no pair has are left as they were.  dy may be y.
- *   dtopk_w  [T, k] fp32 out, or NULL; 0 for a pair of row -1.  Needs topk_w.
+ *   dtopk_w  [T, k] fp32 out, or NULL; 0 for a pair of row -1.  Needs topk_w.  It is the
+ *            gradient of the weights given here: a pair that moe_permute kept with weight 0
+ *            (MOE_NONLOCAL_MOD) has one too, which the mask takes out of the router's
  *   y_shared, x [T, H] bf16, shared_gate_w [H] bf16, dy_shared [T, H] bf16 out, dgate [T] fp32
  *            out: a gated shared expert, or all NULL (without a gate dy_shared is dout)
  *   dshared_gate_w [H] fp32 out, 16-byte aligned, or NULL
