@@ -14,7 +14,7 @@
 // The scales have the form of the activation rows of the E4M3 experts.
 //
 // Bound: HBM.  A row is read once (x and residual) and written once (stream, y,
-// q); the row's values stay in registers between the two reductions.  16384 rows of
+// q); the row's values stay in registers between the reductions.  16384 rows of
 // 7168 with a bf16 stream, y and E4M3 rows: 164 us, 1.06 GB at 6.45 TB/s, 0.95 of this
 // card's copy rate; with an fp32 stream 237 us, 1.53 GB at 6.43 TB/s.  Small batches are
 // bound by latency: one row of 2048 1.9 us, 32 of 7168 with an fp32 stream 3.8 us, 777 of
@@ -63,27 +63,12 @@ __device__ __forceinline__ uint32_t nm_e4m3x4(const float* f, float inv) {
     return lo | (hi << 16);
 }
 
-// Sum of v over a row's WARPS warps (red: one word each), the same in every thread.
-template <int WARPS>
-__device__ __forceinline__ float nm_row_sum(float v, float* red) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (WARPS == 1) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float tot = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) tot += red[w];
-    return tot;
-}
-
 // THREADS threads per row at a time, each with VPT vectors of 8 values (grid-stride over
 // rows): a CTA, or (THREADS = 32) each of its NM_WARPS warps by itself.
-template <int VPT, int THREADS, bool F32, bool LN>
-__device__ __forceinline__ void add_norm(const NormLaunch& a) {
+template <int VPT, int THREADS, bool F32>
+__global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rmsnorm_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ float red_sum[2][WARPS];
-    __shared__ float red_mean[2][LN ? WARPS : 1];
     __shared__ uint32_t red_max[2][WARPS];
     constexpr bool ALONE = THREADS == 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -109,20 +94,18 @@ __device__ __forceinline__ void add_norm(const NormLaunch& a) {
                 for (int i = 0; i < 8; ++i) f[j][i] += r[i];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = LN ? ss + f[j][i] : fmaf(f[j][i], f[j][i], ss);
+            for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i], f[j][i], ss);
         }
-        float mean = 0.f;
-        if (LN) {
-            mean = nm_row_sum<WARPS>(ss, red_mean[it]) / (float)a.H;
-            ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (first + j * THREADS >= vec) continue;
+        for (int off = 16; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        float tot = ss;
+        if (!ALONE) {
+            if (lane == 0) red_sum[it][warp] = ss;
+            __syncthreads();
+            tot = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i] - mean, f[j][i] - mean, ss);
-            }
+            for (int w = 0; w < WARPS; ++w) tot += red_sum[it][w];
         }
-        const float tot = nm_row_sum<WARPS>(ss, red_sum[it]);
         // the root's reciprocal in two words: its own rounding, which would move a whole row of
         // y by up to 2^-24, is taken out.  ms stays one binary32 value: the roundings of the
         // sum, of the division and of eps move the row by half of theirs
@@ -147,13 +130,9 @@ __device__ __forceinline__ void add_norm(const NormLaunch& a) {
             }
             float w[8];
             nm_load8(a.weight + 8 * v, w);
-            float b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (LN && a.bias) nm_load8(a.bias + 8 * v, b);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = LN ? f[j][i] - mean : f[j][i];
-                const float n = fmaf(d, hi, d * lo);
-                f[j][i] = LN ? fmaf(n, w[i], b[i]) : n * w[i];
+                f[j][i] = fmaf(f[j][i], hi, f[j][i] * lo) * w[i];
                 mx = max(mx, __float_as_uint(f[j][i]) & 0x7FFFFFFFu);
             }
             if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = pack8(f[j]);
@@ -179,32 +158,153 @@ __device__ __forceinline__ void add_norm(const NormLaunch& a) {
     }
 }
 
+// The layer norm, laid out like the RMS norm: the mean's reduction, then that of the squares of
+// the deviations from it.  CTAS CTAs an SM: the second reduction wants more rows on their way
+// than the registers would leave by themselves.
 constexpr int nm_threads(int threads) { return threads > 32 ? threads : NM_WARPS * 32; }
 
-template <int VPT, int THREADS, bool F32>
-__global__ void __launch_bounds__(nm_threads(THREADS)) add_rmsnorm_kernel(const __grid_constant__ NormLaunch a) {
-    add_norm<VPT, THREADS, F32, false>(a);
+// Sum of v over a row's WARPS warps (red: one word each), the same in every thread.
+template <int WARPS>
+__device__ __forceinline__ float nm_row_sum(float v, float* red) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (WARPS == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float tot = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) tot += red[w];
+    return tot;
 }
 
-// CTAS CTAs an SM: the layer norm's second reduction wants more rows on their way than the
-// registers would leave by themselves.
 template <int VPT, int THREADS, bool F32, int CTAS>
 __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kernel(const __grid_constant__ NormLaunch a) {
-    add_norm<VPT, THREADS, F32, true>(a);
+    constexpr int WARPS = THREADS / 32;
+    __shared__ float red_mean[2][WARPS];
+    __shared__ float red_sum[2][WARPS];
+    __shared__ uint32_t red_max[2][WARPS];
+    constexpr bool ALONE = THREADS == 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int first = ALONE ? lane : threadIdx.x;
+    const int vec = a.H / 8;
+    pdl_wait();
+    pdl_trigger();
+    int it = 0;
+    const int64_t rows = (int64_t)gridDim.x * (ALONE ? NM_WARPS : 1);
+    for (int64_t row = ALONE ? (int64_t)blockIdx.x * NM_WARPS + warp : blockIdx.x; row < a.T; row += rows, it ^= 1) {
+        const int64_t base = row * a.H;
+        float f[VPT][8];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = first + j * THREADS;
+            if (v >= vec) continue;
+            nm_load8(a.x + base + 8 * v, f[j]);
+            if (a.residual) {
+                float r[8];
+                nm_load_res<F32>(a.residual, base + 8 * v, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[j][i] += r[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += f[j][i];
+        }
+        const float mean = nm_row_sum<WARPS>(sum, red_mean[it]) / (float)a.H;
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            if (first + j * THREADS >= vec) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i] - mean, f[j][i] - mean, ss);
+        }
+        const float tot = nm_row_sum<WARPS>(ss, red_sum[it]);
+        // the root's reciprocal in two words, as for the RMS norm
+        const float ms = tot / (float)a.H + a.eps;
+        const float hi = __frsqrt_rn(ms);
+        const float sq = ms * hi, err = fmaf(-sq, hi, 1.f) - fmaf(ms, hi, -sq) * hi;
+        float lo = 0.5f * hi * err;
+        if (!(fabsf(lo) < hi)) lo = 0.f;  // not finite: an infinite or zero mean square
+        uint32_t mx = 0u;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = first + j * THREADS;
+            if (v >= vec) continue;
+            if (a.residual_out) {
+                if (F32) {
+                    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.residual_out) + base + 8 * v);
+                    p[0] = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
+                    p[1] = make_float4(f[j][4], f[j][5], f[j][6], f[j][7]);
+                } else {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + base + 8 * v) = pack8(f[j]);
+                }
+            }
+            float w[8], b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            nm_load8(a.weight + 8 * v, w);
+            if (a.bias) nm_load8(a.bias + 8 * v, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = f[j][i] - mean;
+                f[j][i] = fmaf(fmaf(d, hi, d * lo), w[i], b[i]);
+                mx = max(mx, __float_as_uint(f[j][i]) & 0x7FFFFFFFu);
+            }
+            if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = pack8(f[j]);
+        }
+        if (!a.q) continue;
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (!ALONE) {
+            if (lane == 0) red_max[it][warp] = mx;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) mx = max(mx, red_max[it][w]);
+        }
+        const int e = nm_exponent(__uint_as_float(mx));
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (first == 0) a.scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = first + j * THREADS;
+            if (v < vec)
+                *reinterpret_cast<uint2*>(a.q + base + 8 * v) =
+                    make_uint2(nm_e4m3x4(f[j], inv), nm_e4m3x4(f[j] + 4, inv));
+        }
+    }
 }
 
-template <int VPT, int THREADS, bool F32, bool LN, int CTAS>
+template <int VPT, int THREADS, bool F32, int CTAS>
+cudaError_t launch_layernorm_size(const NormLaunch& L, int num_sms, cudaStream_t s) {
+    constexpr int ROWS = THREADS == 32 ? NM_WARPS : 1;
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T + ROWS - 1) / ROWS, (int64_t)num_sms * NM_CTAS);
+    return launch_k("add_layernorm", add_layernorm_kernel<VPT, THREADS, F32, CTAS>, dim3(grid), dim3(THREADS * ROWS), 0,
+                    s, L);
+}
+
+template <bool F32>
+cudaError_t launch_layernorm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
+    // 58.7 M elements with E4M3 rows, fp32 / bf16 stream, us (114 / 79 at the copy rate): 512 66 / 51,
+    // 1024 116 / 81, 1408 117 / 98, 2048 116 / 81, 4096 113 / 85, 5120 117 / 85, 6144 117 / 92, 7168
+    // 122 / 93 (three CTAs of 448 threads 121 / 100, four of 224 127 / 103), 8192 122 / 96, 16384 135 / 104.
+    const int vec = L.H / 8;
+    if (vec <= 32) return launch_layernorm_size<1, 32, F32, 6>(L, num_sms, s);
+    if (vec <= 64) return launch_layernorm_size<2, 32, F32, 6>(L, num_sms, s);
+    if (vec <= 128) return launch_layernorm_size<1, 128, F32, 16>(L, num_sms, s);
+    if (vec <= 256) return launch_layernorm_size<2, 128, F32, 12>(L, num_sms, s);
+    if (vec <= 512) return launch_layernorm_size<2, 256, F32, 6>(L, num_sms, s);
+    if (vec <= 640) return launch_layernorm_size<2, 320, F32, 5>(L, num_sms, s);
+    if (vec <= 768) return launch_layernorm_size<2, 384, F32, 4>(L, num_sms, s);
+    if (vec <= 896) return launch_layernorm_size<4, 224, F32, 5>(L, num_sms, s);
+    if (vec <= 1024) return launch_layernorm_size<2, 512, F32, 3>(L, num_sms, s);
+    if (vec <= 1536) return launch_layernorm_size<4, 384, F32, 3>(L, num_sms, s);
+    return launch_layernorm_size<4, 512, F32, 2>(L, num_sms, s);
+}
+
+template <int VPT, int THREADS, bool F32>
 cudaError_t launch_norm_size(const NormLaunch& L, int num_sms, cudaStream_t s) {
     constexpr int ROWS = THREADS == 32 ? NM_WARPS : 1;
     const unsigned grid = (unsigned)std::min<int64_t>((L.T + ROWS - 1) / ROWS, (int64_t)num_sms * NM_CTAS);
-    if constexpr (LN)
-        return launch_k("add_layernorm", add_layernorm_kernel<VPT, THREADS, F32, CTAS>, dim3(grid), dim3(THREADS * ROWS), 0,
-                        s, L);
-    else
-        return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, THREADS, F32>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
+    return launch_k("add_rmsnorm", add_rmsnorm_kernel<VPT, THREADS, F32>, dim3(grid), dim3(THREADS * ROWS), 0, s, L);
 }
 
-template <bool F32, bool LN>
+template <bool F32>
 cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // A warp to a row while its lanes hold it in two vectors each, then one vector a thread
     // to 2048 values, and a CTA of 224 or 256 threads with four: at 7168 values (16384 rows
@@ -213,41 +313,24 @@ cudaError_t launch_norm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // widths of these forms run at (16384 rows, of the copy rate): 4096 0.99, 5120 (a vector of
     // four idle) 0.90, 6144 0.90, and at 1.06 GB 8192 0.91, 16384 0.84.
     const int vec = L.H / 8;
-    // 58.7 M elements with E4M3 rows, fp32 / bf16 stream, us (114 / 79 at the copy rate): 512 66 / 51,
-    // 1024 116 / 81, 1408 117 / 98, 2048 116 / 81, 4096 113 / 85, 5120 117 / 85, 6144 117 / 92, 7168
-    // 122 / 93 (three CTAs of 448 threads 121 / 100, four of 224 127 / 103), 8192 122 / 96, 16384 135 / 104.
-    if constexpr (LN) {
-        if (vec <= 32) return launch_norm_size<1, 32, F32, true, 6>(L, num_sms, s);
-        if (vec <= 64) return launch_norm_size<2, 32, F32, true, 6>(L, num_sms, s);
-        if (vec <= 128) return launch_norm_size<1, 128, F32, true, 16>(L, num_sms, s);
-        if (vec <= 256) return launch_norm_size<2, 128, F32, true, 12>(L, num_sms, s);
-        if (vec <= 512) return launch_norm_size<2, 256, F32, true, 6>(L, num_sms, s);
-        if (vec <= 640) return launch_norm_size<2, 320, F32, true, 5>(L, num_sms, s);
-        if (vec <= 768) return launch_norm_size<2, 384, F32, true, 4>(L, num_sms, s);
-        if (vec <= 896) return launch_norm_size<4, 224, F32, true, 5>(L, num_sms, s);
-        if (vec <= 1024) return launch_norm_size<2, 512, F32, true, 3>(L, num_sms, s);
-        if (vec <= 1536) return launch_norm_size<4, 384, F32, true, 3>(L, num_sms, s);
-        return launch_norm_size<4, 512, F32, true, 2>(L, num_sms, s);
-    } else {
-        if (vec <= 32) return launch_norm_size<1, 32, F32, false, 0>(L, num_sms, s);
-        if (vec <= 64) return launch_norm_size<2, 32, F32, false, 0>(L, num_sms, s);
-        if (vec <= 128) return launch_norm_size<1, 128, F32, false, 0>(L, num_sms, s);
-        if (vec <= 256) return launch_norm_size<1, 256, F32, false, 0>(L, num_sms, s);
-        if (vec <= 512) return launch_norm_size<2, 256, F32, false, 0>(L, num_sms, s);
-        if (vec <= 896) return launch_norm_size<4, 224, F32, false, 0>(L, num_sms, s);
-        if (vec <= 1024) return launch_norm_size<4, 256, F32, false, 0>(L, num_sms, s);
-        return launch_norm_size<4, 512, F32, false, 0>(L, num_sms, s);
-    }
+    if (vec <= 32) return launch_norm_size<1, 32, F32>(L, num_sms, s);
+    if (vec <= 64) return launch_norm_size<2, 32, F32>(L, num_sms, s);
+    if (vec <= 128) return launch_norm_size<1, 128, F32>(L, num_sms, s);
+    if (vec <= 256) return launch_norm_size<1, 256, F32>(L, num_sms, s);
+    if (vec <= 512) return launch_norm_size<2, 256, F32>(L, num_sms, s);
+    if (vec <= 896) return launch_norm_size<4, 224, F32>(L, num_sms, s);
+    if (vec <= 1024) return launch_norm_size<4, 256, F32>(L, num_sms, s);
+    return launch_norm_size<4, 512, F32>(L, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rmsnorm(const NormLaunch& L, int num_sms, cudaStream_t s) {
-    return L.f32 ? launch_norm_type<true, false>(L, num_sms, s) : launch_norm_type<false, false>(L, num_sms, s);
+    return L.f32 ? launch_norm_type<true>(L, num_sms, s) : launch_norm_type<false>(L, num_sms, s);
 }
 
 cudaError_t launch_add_layernorm(const NormLaunch& L, int num_sms, cudaStream_t s) {
-    return L.f32 ? launch_norm_type<true, true>(L, num_sms, s) : launch_norm_type<false, true>(L, num_sms, s);
+    return L.f32 ? launch_layernorm_type<true>(L, num_sms, s) : launch_layernorm_type<false>(L, num_sms, s);
 }
 
 }  // namespace moe
