@@ -32,7 +32,8 @@ namespace {
 
 constexpr int NB_WARPS = 16;           // warps of a CTA at most, one CTA an SM
 constexpr int NB_SMEM = 227 * 1024 - 1024;  // of a CTA, less the static arrays
-constexpr int NB_F32_ROWS = 48 * 1024; // of an fp32 stream's rows, one for each of a CTA's groups
+// bytes of an fp32 stream's rows, one for each of a CTA's groups, and where there are few rows
+constexpr int NB_F32_ROWS = 48 * 1024, NB_F32_FEW = 64 * 1024;
 
 // What a kernel keeps: the row's r, dy and the weight in registers from one pass to the next, or
 // the weight in shared memory in binary32, or nothing.
@@ -363,8 +364,14 @@ cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream
     // fp32 stream (28672 rows of 2048, RMS: 2 groups of 2 rows 142 us, of 3 163, 4 groups of 2
     // 153), and a little with a bf16 one (4 groups of 2 76 us, of 3 78, of 4 82); the layer norm
     // takes longer over a row and wants the third (fp32, 14336 rows of 4096: 153 us against 193).
-    p.groups = NB_WARPS / p.gw;
-    if (F32) p.groups = std::max(1, std::min(p.groups, (int)(NB_F32_ROWS / row)));
+    // Few rows an SM want fewer groups than a long run of them: a start of fewer copies and fewer
+    // sums to add at the end, and no SM without rows.  12 warps instead of 16 (RMS: always), us:
+    // bf16, RMS 4096 rows of 2048 16.6 / 18.1, 8192 of 1024 16.9 / 18.7; layer norm 4096 of 2048
+    // 20.1 / 21.7, but 28672 99 / 86.
+    const bool few = L.T < 40LL * num_sms;
+    p.groups = (!wide && p.gw <= 4 && (few || !LN) ? 12 : NB_WARPS) / p.gw;
+    if (F32) p.groups = std::max(1, std::min(p.groups, (int)((few ? NB_F32_FEW : NB_F32_ROWS) / row)));
+    p.groups = (int)std::min<int64_t>(p.groups, (L.T + num_sms - 1) / num_sms);
     const bool w_smem = wide && weight + 2 * p.groups * row <= NB_SMEM;
     const size_t below = w_smem ? weight : 0;
     p.slots = (int)std::min<size_t>(F32 && !LN ? 2 : 3, (NB_SMEM - below) / (p.groups * row));
