@@ -33,46 +33,62 @@ __device__ __forceinline__ int32_t pair_row_of(const int32_t* pair_row, int64_t 
 // both, for whatever is launched behind it.
 constexpr int FB_BATCH = 4;
 
+// PP: pairs a warp takes at a time, for rows so short that one of them does not fill a batch (16384
+// tokens of 256, 8 pairs: 36 us with four, 56 with one).
+template <int PP>
 __global__ void __launch_bounds__(FB_WARPS * 32) finalize_bwd_kernel(const __grid_constant__ FinalizeBwdLaunch a) {
+    constexpr int V = FB_BATCH / PP;  // vectors of a pair in flight a lane
     if (!a.gate_first) pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
-    const int64_t pairs = a.T * a.k;
-    for (int64_t u = (int64_t)blockIdx.x * FB_WARPS + warp; u < pairs; u += (int64_t)gridDim.x * FB_WARPS) {
-        const int64_t t = u / a.k;
-        const int32_t r = pair_row_of(a.pair_row, u, a.rows_cap, lane == 0 ? &a.hdr->status : nullptr);
-        float dot = 0.f;
-        if (r >= 0) {
-            const float w = a.w ? a.w[u] : 1.f;
-            const uint4* dout = reinterpret_cast<const uint4*>(a.dout + t * a.H);
-            const uint4* y = reinterpret_cast<const uint4*>(a.y + (int64_t)r * a.H);  // not __ldg: dy may be y
-            uint4* dy = reinterpret_cast<uint4*>(a.dy + (int64_t)r * a.H);
-            for (int v0 = lane; v0 < vec; v0 += 32 * FB_BATCH) {
-                uint4 d[FB_BATCH], f[FB_BATCH];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, vec = a.H / 8;
+    const uint32_t pairs = (uint32_t)(a.T * a.k);  // below 2^31
+    for (int64_t u0 = ((int64_t)blockIdx.x * warps + warp) * PP; u0 < pairs; u0 += (int64_t)gridDim.x * warps * PP) {
+        int32_t r[PP];
+        float w[PP], dot[PP] = {};
+        const uint4 *dout[PP], *y[PP];
+        uint4* dy[PP];
 #pragma unroll
-                for (int b = 0; b < FB_BATCH; ++b) {
-                    const bool ok = v0 + 32 * b < vec;
-                    d[b] = ok ? dout[v0 + 32 * b] : make_uint4(0, 0, 0, 0);
-                    f[b] = ok && a.dw ? y[v0 + 32 * b] : make_uint4(0, 0, 0, 0);
+        for (int p = 0; p < PP; ++p) {
+            const uint32_t u = (uint32_t)u0 + p;
+            r[p] = PP == 1 || u < pairs ? pair_row_of(a.pair_row, u, a.rows_cap, lane == 0 ? &a.hdr->status : nullptr) : -1;
+            w[p] = r[p] >= 0 && a.w ? a.w[u] : 1.f;
+            const int64_t row = r[p] >= 0 ? r[p] : 0;
+            dout[p] = reinterpret_cast<const uint4*>(a.dout + (int64_t)(u / (uint32_t)a.k) * a.H);
+            y[p] = reinterpret_cast<const uint4*>(a.y + row * a.H);  // not __ldg: dy may be y
+            dy[p] = reinterpret_cast<uint4*>(a.dy + row * a.H);
+        }
+        const int end = PP == 1 && r[0] < 0 ? 0 : vec;
+        for (int v0 = lane; v0 < end; v0 += 32 * V) {
+            uint4 d[PP][V], f[PP][V];
+#pragma unroll
+            for (int p = 0; p < PP; ++p)
+#pragma unroll
+                for (int b = 0; b < V; ++b) {
+                    const bool ok = (PP == 1 || r[p] >= 0) && v0 + 32 * b < vec;
+                    d[p][b] = ok ? dout[p][v0 + 32 * b] : make_uint4(0, 0, 0, 0);
+                    f[p][b] = ok && a.dw ? y[p][v0 + 32 * b] : make_uint4(0, 0, 0, 0);
                 }
 #pragma unroll
-                for (int b = 0; b < FB_BATCH; ++b) {
+            for (int p = 0; p < PP; ++p)
+#pragma unroll
+                for (int b = 0; b < V; ++b) {
                     float x[8], z[8];
-                    unpack8(d[b], x);
-                    unpack8(f[b], z);
+                    unpack8(d[p][b], x);
+                    unpack8(f[p][b], z);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        dot = fmaf(x[i], z[i], dot);
-                        x[i] *= w;
+                        dot[p] = fmaf(x[i], z[i], dot[p]);
+                        x[i] *= w[p];
                     }
-                    if (v0 + 32 * b < vec) dy[v0 + 32 * b] = pack8(x);
+                    if ((PP == 1 || r[p] >= 0) && v0 + 32 * b < vec) dy[p][v0 + 32 * b] = pack8(x);
                 }
+        }
+        if (a.dw)
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                dot[p] = warp_sum(dot[p]);
+                if (lane == 0 && (PP == 1 || (uint32_t)u0 + p < pairs)) a.dw[u0 + p] = dot[p];
             }
-        }
-        if (a.dw) {
-            dot = warp_sum(dot);
-            if (lane == 0) a.dw[u] = dot;
-        }
     }
     if (a.gate_first && blockIdx.x == 0) pdl_wait();
 }
@@ -248,7 +264,7 @@ __global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const 
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vec = a.H / 8;
-    const int part = warp & (split - 1), tokens = FB_WARPS / split;
+    const int part = warp & (split - 1), tokens = (blockDim.x >> 5) / split;
     for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.T; t0 += (int64_t)gridDim.x * tokens) {
         const int64_t t = t0 + warp / split;
         const bool live_t = t < a.T;
@@ -367,8 +383,13 @@ cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& given, int num_sms, cud
                      groups > 1 ? (size_t)L.H * 4 : 0, s, L, gw, groups);
         if (e != cudaSuccess) return e;
     }
-    const unsigned grid = (unsigned)std::min<int64_t>((L.T * L.k + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
-    e = launch_k("finalize_bwd", finalize_bwd_kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L);
+    // CTAs of few warps leave less of an SM idle at the end (16384 pairs of 2048: 24.9 us with four
+    // warps, 25.2 with eight)
+    constexpr int WARPS = 4;
+    const int pp = L.H <= 256 ? 4 : L.H <= 512 ? 2 : 1;
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T * L.k + WARPS * pp - 1) / (WARPS * pp), (int64_t)num_sms * 128);
+    const auto kernel = pp == 4 ? finalize_bwd_kernel<4> : pp == 2 ? finalize_bwd_kernel<2> : finalize_bwd_kernel<1>;
+    e = launch_k("finalize_bwd", kernel, dim3(grid), dim3(WARPS * 32), 0, s, L);
     if (e != cudaSuccess || !L.gate_w) return e;
     if (!L.gate_first) {
         const unsigned rows = (unsigned)std::min<int64_t>((L.T + FB_WARPS - 1) / FB_WARPS, (int64_t)num_sms * 64);
@@ -391,10 +412,10 @@ cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStrea
     while (split < FB_WARPS && (L.T * split < (int64_t)num_sms * FB_WARPS ||
                                 (L.T * split < 8LL * num_sms * FB_WARPS && L.H / 8 >= 2 * split * 5 * 32)))
         split *= 2;
-    const int tokens = FB_WARPS / split;
-    const unsigned grid = (unsigned)std::min<int64_t>((L.T + tokens - 1) / tokens, (int64_t)num_sms * 64);
+    const int warps = std::max(split, 2), tokens = warps / split;  // few warps: less of an SM idle at the end
+    const unsigned grid = (unsigned)std::min<int64_t>((L.T + tokens - 1) / tokens, (int64_t)num_sms * 128);
     const auto go = [&](auto kernel) {
-        return launch_k("permute_bwd", kernel, dim3(grid), dim3(FB_WARPS * 32), 0, s, L, split);
+        return launch_k("permute_bwd", kernel, dim3(grid), dim3(warps * 32), 0, s, L, split);
     };
     if (L.k <= 2) return L.dw ? go(permute_bwd_kernel<2, true, 2, 4>) : go(permute_bwd_kernel<2, false, 2, 4>);
     if (L.k <= 4) return L.dw ? go(permute_bwd_kernel<4, true, 1, 5>) : go(permute_bwd_kernel<4, false, 1, 5>);
