@@ -77,6 +77,14 @@ def test_bwd_row_counts_with_a_streams_gradient(T, H, ln):
     _check(ln, dy, r, w, ds, _run(ln, dy, r, w, ds))
 
 
+@pytest.mark.parametrize("H", [200, 1024, 2048, 5120, 7168])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("ln", [False, True])
+def test_bwd_many_rows_an_sm(H, f32, ln):
+    r, w, _, dy = _inputs(7001, H, f32, seed=13)
+    _check(ln, dy, r, w, None, _run(ln, dy, r, w, None))
+
+
 @pytest.mark.parametrize("ln", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("H", [256, 1024, 7168])
