@@ -461,6 +461,57 @@ def test_on_another_stream_and_in_graphs():
     assert _status(ws2) == 0
 
 
+def test_no_rows_at_all():
+    """A rank that holds no expert of the batch: no rows, every pair -1."""
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    T, k, H = 9, 3, 192
+    ws = _ws(H)
+    pr = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    none, w = torch.empty(0, H, **bf), torch.zeros(T, k, device="cuda")
+    dw = torch.full((T, k), 4.0, device="cuda")
+    moe.moe_finalize_bwd(ref.rnd(T, H), none, pr, w, None, None, None, none, dw, None, None, None, ws)
+    assert not dw.any()
+    add, dx, dw = ref.rnd(T, H, seed=1), torch.empty(T, H, **bf), torch.full((T, k), 4.0, device="cuda")
+    moe.moe_permute_bwd(none, pr, w, ref.rnd(T, H, seed=2), add, None, None, dx, dw, ws)
+    assert torch.equal(dx, add) and not dw.any() and _status(ws) == 0
+
+
+@pytest.mark.parametrize("H", [256, 2048, 8320])
+def test_calls_that_overlap_their_neighbours_wait_for_them(H):
+    """Each call reads what the one before it wrote; with programmatic launches their kernels overlap, and the results are
+    those of launches one behind the other."""
+    T, k = 1500, 4
+    d = _fin_inputs(T, H, 16, k, 12, True, seed=40)
+    r, w, b = ref.rnd(T, H, seed=41), ref.rnd(H, seed=42), ref.rnd(H, seed=43)
+    f32 = dict(dtype=torch.float32, device="cuda")
+
+    def run(n):
+        outs, ws = [], _ws(H)
+        for i in range(n):
+            x, stream = torch.empty_like(r), torch.empty_like(r)
+            dy, dysh, dx, dr = torch.zeros_like(d["y"]), torch.empty_like(r), torch.empty_like(r), torch.empty_like(r)
+            dw, dz, dgw = torch.empty(T, k, **f32), torch.empty(T, **f32), torch.empty(H, **f32)
+            nw, nb = torch.empty(H, **f32), torch.empty(H, **f32)
+            res = r * (i + 1)
+            moe.moe_add_layernorm(d["x"], res, w, b, 1e-5, stream, x)
+            moe.moe_finalize_bwd(x, d["y"], d["pr"], d["w"], d["ysh"], x, d["gw"], dy, dw, dysh, dz, dgw, ws)
+            moe.moe_permute_bwd(dy, d["pr"], None, None, dysh, dz, d["gw"], dx, None, ws)
+            moe.moe_add_layernorm_bwd(dx, stream, w, 1e-5, dysh, dr, None, nw, nb, ws)
+            outs.append((dy, dw, dysh, dz, dgw, dx, dr, nw, nb))
+        torch.cuda.synchronize()
+        assert _status(ws) == 0
+        return outs
+
+    moe.moe_set_pdl(False)
+    try:
+        want = run(6)
+    finally:
+        moe.moe_set_pdl(True)
+    for _ in range(4):
+        for got, exp in zip(run(6), want):
+            assert all(torch.equal(g, e) for g, e in zip(got, exp))
+
+
 def test_binding_refuses_what_it_would_misread():
     d = _fin_inputs(4, 64, 8, 2, gated=True)
     ws = _ws()
