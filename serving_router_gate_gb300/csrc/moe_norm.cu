@@ -160,7 +160,37 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rm
 
 // The layer norm, laid out like the RMS norm: the mean's reduction, then that of the squares of
 // the deviations from it.  CTAS CTAs an SM: the second reduction wants more rows on their way
-// than the registers would leave by themselves.
+// than the registers would leave by themselves.  An fp32 stream that lies on 32 bytes is read and
+// written 32 bytes a lane: with 16 a request covers half of each of its sectors (8192 rows of 7168
+// with E4M3 rows 116 us against 123, 4778 of 12288 119 against 132).
+enum { NM_BF16, NM_F32, NM_F32_WIDE };
+
+template <int STREAM>
+__device__ __forceinline__ void nm_stream_load(const void* res, int64_t off, float f[8]) {
+    if (STREAM == NM_F32_WIDE)
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                     : "l"(static_cast<const float*>(res) + off)
+                     : "memory");
+    else
+        nm_load_res<STREAM == NM_F32>(res, off, f);
+}
+
+template <int STREAM>
+__device__ __forceinline__ void nm_stream_store(void* res, int64_t off, const float f[8]) {
+    if (STREAM == NM_F32_WIDE) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(res) + off),
+                     "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+                     : "memory");
+    } else if (STREAM == NM_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(res) + off);
+        p[0] = make_float4(f[0], f[1], f[2], f[3]);
+        p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(res) + off) = pack8(f);
+    }
+}
+
 constexpr int nm_threads(int threads) { return threads > 32 ? threads : NM_WARPS * 32; }
 
 // Sum of v over a row's WARPS warps (red: one word each), the same in every thread.
@@ -177,7 +207,7 @@ __device__ __forceinline__ float nm_row_sum(float v, float* red) {
     return tot;
 }
 
-template <int VPT, int THREADS, bool F32, int CTAS>
+template <int VPT, int THREADS, int STREAM, int CTAS>
 __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ float red_mean[2][WARPS];
@@ -202,7 +232,7 @@ __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kerne
             nm_load8(a.x + base + 8 * v, f[j]);
             if (a.residual) {
                 float r[8];
-                nm_load_res<F32>(a.residual, base + 8 * v, r);
+                nm_stream_load<STREAM>(a.residual, base + 8 * v, r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) f[j][i] += r[i];
             }
@@ -229,15 +259,7 @@ __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kerne
         for (int j = 0; j < VPT; ++j) {
             const int v = first + j * THREADS;
             if (v >= vec) continue;
-            if (a.residual_out) {
-                if (F32) {
-                    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.residual_out) + base + 8 * v);
-                    p[0] = make_float4(f[j][0], f[j][1], f[j][2], f[j][3]);
-                    p[1] = make_float4(f[j][4], f[j][5], f[j][6], f[j][7]);
-                } else {
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.residual_out) + base + 8 * v) = pack8(f[j]);
-                }
-            }
+            if (a.residual_out) nm_stream_store<STREAM>(a.residual_out, base + 8 * v, f[j]);
             float w[8], b[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             nm_load8(a.weight + 8 * v, w);
             if (a.bias) nm_load8(a.bias + 8 * v, b);
@@ -270,31 +292,32 @@ __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kerne
     }
 }
 
-template <int VPT, int THREADS, bool F32, int CTAS>
+template <int VPT, int THREADS, int STREAM, int CTAS>
 cudaError_t launch_layernorm_size(const NormLaunch& L, int num_sms, cudaStream_t s) {
     constexpr int ROWS = THREADS == 32 ? NM_WARPS : 1;
     const unsigned grid = (unsigned)std::min<int64_t>((L.T + ROWS - 1) / ROWS, (int64_t)num_sms * NM_CTAS);
-    return launch_k("add_layernorm", add_layernorm_kernel<VPT, THREADS, F32, CTAS>, dim3(grid), dim3(THREADS * ROWS), 0,
+    return launch_k("add_layernorm", add_layernorm_kernel<VPT, THREADS, STREAM, CTAS>, dim3(grid), dim3(THREADS * ROWS), 0,
                     s, L);
 }
 
-template <bool F32>
+template <int STREAM>
 cudaError_t launch_layernorm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
-    // 58.7 M elements with E4M3 rows, fp32 / bf16 stream, us (114 / 79 at the copy rate): 512 66 / 51,
-    // 1024 116 / 81, 1408 117 / 98, 2048 116 / 81, 4096 113 / 85, 5120 117 / 85, 6144 117 / 92, 7168
-    // 122 / 93 (three CTAs of 448 threads 121 / 100, four of 224 127 / 103), 8192 122 / 96, 16384 135 / 104.
+    // 58.7 M elements with E4M3 rows, fp32 (on 32 bytes) / bf16 stream, us (114 / 79 at the copy rate):
+    // 512 66 / 51, 1024 116 / 81, 1408 117 / 98, 2048 114 / 81, 4096 113 / 85, 5120 116 / 85, 6144 114 /
+    // 92, 7168 116 / 93, 8192 116 / 96, 16384 127 / 104.  At 7168 three CTAs of 448 threads, bf16: 100,
+    // four of 224: 103.
     const int vec = L.H / 8;
-    if (vec <= 32) return launch_layernorm_size<1, 32, F32, 6>(L, num_sms, s);
-    if (vec <= 64) return launch_layernorm_size<2, 32, F32, 6>(L, num_sms, s);
-    if (vec <= 128) return launch_layernorm_size<1, 128, F32, 16>(L, num_sms, s);
-    if (vec <= 256) return launch_layernorm_size<2, 128, F32, 12>(L, num_sms, s);
-    if (vec <= 512) return launch_layernorm_size<2, 256, F32, 6>(L, num_sms, s);
-    if (vec <= 640) return launch_layernorm_size<2, 320, F32, 5>(L, num_sms, s);
-    if (vec <= 768) return launch_layernorm_size<2, 384, F32, 4>(L, num_sms, s);
-    if (vec <= 896) return launch_layernorm_size<4, 224, F32, 5>(L, num_sms, s);
-    if (vec <= 1024) return launch_layernorm_size<2, 512, F32, 3>(L, num_sms, s);
-    if (vec <= 1536) return launch_layernorm_size<4, 384, F32, 3>(L, num_sms, s);
-    return launch_layernorm_size<4, 512, F32, 2>(L, num_sms, s);
+    if (vec <= 32) return launch_layernorm_size<1, 32, STREAM, 6>(L, num_sms, s);
+    if (vec <= 64) return launch_layernorm_size<2, 32, STREAM, 6>(L, num_sms, s);
+    if (vec <= 128) return launch_layernorm_size<1, 128, STREAM, 16>(L, num_sms, s);
+    if (vec <= 256) return launch_layernorm_size<2, 128, STREAM, 12>(L, num_sms, s);
+    if (vec <= 512) return launch_layernorm_size<2, 256, STREAM, 6>(L, num_sms, s);
+    if (vec <= 640) return launch_layernorm_size<2, 320, STREAM, 5>(L, num_sms, s);
+    if (vec <= 768) return launch_layernorm_size<2, 384, STREAM, 4>(L, num_sms, s);
+    if (vec <= 896) return launch_layernorm_size<4, 224, STREAM, 5>(L, num_sms, s);
+    if (vec <= 1024) return launch_layernorm_size<2, 512, STREAM, 3>(L, num_sms, s);
+    if (vec <= 1536) return launch_layernorm_size<4, 384, STREAM, 3>(L, num_sms, s);
+    return launch_layernorm_size<4, 512, STREAM, 2>(L, num_sms, s);
 }
 
 template <int VPT, int THREADS, bool F32>
@@ -330,7 +353,9 @@ cudaError_t launch_add_rmsnorm(const NormLaunch& L, int num_sms, cudaStream_t s)
 }
 
 cudaError_t launch_add_layernorm(const NormLaunch& L, int num_sms, cudaStream_t s) {
-    return L.f32 ? launch_layernorm_type<true>(L, num_sms, s) : launch_layernorm_type<false>(L, num_sms, s);
+    if (!L.f32) return launch_layernorm_type<NM_BF16>(L, num_sms, s);
+    const bool wide = ((reinterpret_cast<uintptr_t>(L.residual) | reinterpret_cast<uintptr_t>(L.residual_out)) & 31) == 0;
+    return wide ? launch_layernorm_type<NM_F32_WIDE>(L, num_sms, s) : launch_layernorm_type<NM_F32>(L, num_sms, s);
 }
 
 }  // namespace moe

@@ -8,19 +8,22 @@
 // The row's statistics are taken again from r: the row has to be read for d anyway.  All
 // sums are binary32; dr is rounded once for each of its outputs.
 //
-// Bound: HBM (8 bytes an element with a bf16 stream) and not far behind it the issue rate:
-// the two passes over a row take about 14 instructions an element, half of them conversions,
-// so the arithmetic is done on pairs (f32x2), the weight lies in shared memory in binary32,
-// and every address of a row is a base and a constant.  A row belongs to a group of warps,
-// each thread to the same columns of every row of its group, so the weight's sums stay in
-// registers to the end of a persistent grid; a CTA's groups then add theirs in order, and a
-// second kernel adds the CTAs'.  A thread copies its own columns of the rows to come into
-// shared memory (cp.async): the copies need no barrier, and a row's one barrier (the layer
-// norm's two: the mean comes first, so that a row far from zero keeps its variance) joins its
-// warps' sums.
+// Bound: HBM (8 bytes an element with a bf16 stream and its gradient) and not far behind it
+// the issue rate: 21 instructions an element in all (RMS, bf16), a third of them conversions, a
+// third what a row costs beside its elements.  So the arithmetic is done on pairs (f32x2) and
+// every address of a row is a base and a constant.  A row belongs to a group of warps, each
+// thread to the same columns of every row of its group, so the weight's sums stay in registers
+// to the end of a persistent grid; a CTA's groups then add theirs in order, and a second kernel
+// adds the CTAs'.  A thread copies its own columns of the rows to come into shared memory
+// (cp.async): the copies need no barrier, and a row's one barrier (the layer norm's two: the mean
+// comes first, so that a row far from zero keeps its variance) joins its warps' sums.
 //
 // Narrow rows keep r, dy and the weight in registers from one pass to the next; rows of more
 // columns a thread read them again (the weight from shared memory, in binary32).
+//
+// 16384 rows of 7168 with a stream's gradient: RMS, bf16 138.5 us, 6.8 TB/s, 1.01 of this card's
+// copy rate; fp32 310 us, 0.91; layer norm, bf16 166 us, 0.84; fp32 271 us, 1.04.  4096 of 2048,
+// fp32, layer norm 26.7 us, 0.75; 777 of 1408, bf16 8 us, of which the second kernel 3.
 #include <algorithm>
 #include <atomic>
 

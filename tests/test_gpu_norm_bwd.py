@@ -234,6 +234,31 @@ def test_bwd_on_another_stream_and_in_graphs(ln, H):
             assert all(a is None or torch.equal(a, b) for a, b in zip(out, want))
 
 
+def _on_16_bytes(t):
+    """A copy of t that starts 16 bytes behind a 32-byte boundary."""
+    buf = torch.empty(t.numel() + 64, dtype=t.dtype, device="cuda")
+    at = (-buf.data_ptr() % 32 + 16) // t.element_size()
+    out = buf[at:at + t.numel()].view(t.shape)
+    assert out.data_ptr() % 32 == 16
+    return out.copy_(t)
+
+
+@pytest.mark.parametrize("H", [264, 2048, 7176])
+@pytest.mark.parametrize("f32", [False, True])
+def test_operands_on_16_bytes(H, f32):
+    r, w, b, dy = _inputs(37, H, f32, seed=14)
+    x, ds = ref.rnd(37, H, seed=25), ref.rnd(37, H, seed=26, std=0.01, dtype=r.dtype)
+    want = _ln(x, r, w, b, True)
+    ro, y = _on_16_bytes(torch.zeros_like(r)), _on_16_bytes(torch.zeros_like(x))
+    moe.moe_add_layernorm(_on_16_bytes(x), _on_16_bytes(r), _on_16_bytes(w), _on_16_bytes(b), EPS, ro, y)
+    assert torch.equal(ro, want[0]) and torch.equal(y, want[1])
+    for ln in (False, True):
+        want = _run(ln, dy, r, w, ds)
+        got = [_on_16_bytes(torch.zeros_like(t)) if t is not None else None for t in want]
+        _bwd(ln, _on_16_bytes(dy), _on_16_bytes(r), _on_16_bytes(w), _on_16_bytes(ds), *got, _ws(H))
+        assert all(g is None or torch.equal(g, t) for g, t in zip(got, want))
+
+
 @pytest.mark.parametrize("ln", [False, True])
 def test_bwd_two_calls_at_once_beside_other_work(ln):
     """Two streams with a workspace each, and a third that keeps the GPU busy: the CTAs' sums are added whoever gets to
