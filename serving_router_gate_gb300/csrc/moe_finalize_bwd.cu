@@ -247,16 +247,15 @@ __global__ void __launch_bounds__(FB_WARPS * 32) gate_weight_kernel(const float*
 // its token's pairs that have a row, then takes U vectors of 8 values a lane at a time, with
 // PB_LOADS of the pairs' vectors in flight before they are used.  MAXK: k at most; DW: with
 // the weights' gradients, a lane's share of every pair's dot product stays in a register.
-// U and the CTAs an SM are those that measured best.  Up to 8 pairs, without DW 2 and 3 (8191
-// tokens of 7168, half of 8 pairs: 121 us; 1 and 4: 122, 2 and 2: 130), with it 1 and 4, which
-// leaves 64 registers for 32 warps an SM (4096 tokens of 7168, 8 pairs: 106 us; 2 and 3: 118, 1
-// and 3: 119, 2 and 2: 138).  Up to 4 pairs 1 and 5 (16384 tokens of 2048, 4 pairs, DW: 68 us; 2
-// and 3: 69, 1 and 4: 74), up to 2 pairs 2 and 4 (16384 tokens of 4096, 2 pairs, DW: 88 us; 4
-// and 2: 89, 4 and 3: 95, as for 8 pairs: 100).
+// U and the registers (through CTAS CTAs of WARPS warps an SM) are those that measured best: enough
+// loads in flight against enough warps.  16384 tokens of 2048, us: 4 pairs with DW 62.9 (U 2, 28
+// warps an SM; 24 warps 66.5; U 1, 40 warps 66.9), without 50.8 (U 2, 24; U 1, 36 52.9); 2 pairs
+// with DW 43.0 (U 2, 28; 32 46.5; U 1, 36 44.4); 8 pairs with DW 104 (U 1, 32; 36 over 110; U 2, 24
+// 106.6), without 88.2 (U 2, 24; U 1, 32 90.6, but 4096 tokens 25.5 against 27.5).
 constexpr int PB_LOADS = 8;
 
-template <int MAXK, bool DW, int U, int CTAS>
-__global__ void __launch_bounds__(FB_WARPS * 32, CTAS) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a,
+template <int MAXK, bool DW, int U, int CTAS, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) permute_bwd_kernel(const __grid_constant__ PermuteBwdLaunch a,
                                                                   int split) {
     constexpr int BATCH = PB_LOADS / U < MAXK ? PB_LOADS / U : MAXK;
     __shared__ int32_t s_row[FB_WARPS][MAXK], s_pair[FB_WARPS][MAXK];
@@ -417,10 +416,17 @@ cudaError_t launch_permute_bwd(const PermuteBwdLaunch& L, int num_sms, cudaStrea
     const auto go = [&](auto kernel) {
         return launch_k("permute_bwd", kernel, dim3(grid), dim3(warps * 32), 0, s, L, split);
     };
-    if (L.k <= 2) return L.dw ? go(permute_bwd_kernel<2, true, 2, 4>) : go(permute_bwd_kernel<2, false, 2, 4>);
-    if (L.k <= 4) return L.dw ? go(permute_bwd_kernel<4, true, 1, 5>) : go(permute_bwd_kernel<4, false, 1, 5>);
-    if (L.k <= 8) return L.dw ? go(permute_bwd_kernel<8, true, 1, 4>) : go(permute_bwd_kernel<8, false, 2, 3>);
-    return L.dw ? go(permute_bwd_kernel<32, true, 1, 2>) : go(permute_bwd_kernel<32, false, 2, 3>);
+    if (L.k > 8) return L.dw ? go(permute_bwd_kernel<32, true, 1, 2, 8>) : go(permute_bwd_kernel<32, false, 2, 3, 8>);
+    if (warps > 2) {  // a token over four or eight warps
+        if (L.k <= 2) return L.dw ? go(permute_bwd_kernel<2, true, 2, 4, 8>) : go(permute_bwd_kernel<2, false, 2, 4, 8>);
+        if (L.k <= 4) return L.dw ? go(permute_bwd_kernel<4, true, 1, 5, 8>) : go(permute_bwd_kernel<4, false, 1, 5, 8>);
+        return L.dw ? go(permute_bwd_kernel<8, true, 1, 4, 8>) : go(permute_bwd_kernel<8, false, 2, 3, 8>);
+    }
+    if (L.k <= 2) return L.dw ? go(permute_bwd_kernel<2, true, 2, 14, 2>) : go(permute_bwd_kernel<2, false, 2, 16, 2>);
+    if (L.k <= 4) return L.dw ? go(permute_bwd_kernel<4, true, 2, 14, 2>) : go(permute_bwd_kernel<4, false, 2, 12, 2>);
+    if (L.dw || L.T < 40LL * num_sms)
+        return L.dw ? go(permute_bwd_kernel<8, true, 1, 16, 2>) : go(permute_bwd_kernel<8, false, 1, 16, 2>);
+    return go(permute_bwd_kernel<8, false, 2, 12, 2>);
 }
 
 }  // namespace moe
