@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid
         }
     }
     if (!a.dgate_w) return;
-    float4* const part = reinterpret_cast<float4*>(a.part + (int64_t)blockIdx.x * a.H);
+    float4* const part = reinterpret_cast<float4*>(gridDim.x > 1 ? a.part + (int64_t)blockIdx.x * a.H : a.dgate_w);
     for (int g = 0; g < groups; ++g) {
         if (groups > 1) __syncthreads();
         if (g != group) continue;
@@ -377,7 +377,8 @@ cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& given, int num_sms, cud
     cudaError_t e;
     if (L.gate_first) {
         const int gw = (L.H + 511) / 512, groups = std::max(1, GB_CTA_WARPS / gw);
-        parts = (int)std::min<int64_t>((L.T + groups - 1) / groups, std::min(num_sms, kBwdPartials));
+        // as many tokens as a CTA has groups go to one CTA, whose sums need no other kernel
+        parts = L.T <= groups ? 1 : (int)std::min<int64_t>((L.T + groups - 1) / groups, std::min(num_sms, kBwdPartials));
         e = launch_k("gate_bwd", gate_bwd_kernel, dim3(parts), dim3(gw * groups * 32),
                      groups > 1 ? (size_t)L.H * 4 : 0, s, L, gw, groups);
         if (e != cudaSuccess) return e;
@@ -399,7 +400,7 @@ cudaError_t launch_finalize_bwd(const FinalizeBwdLaunch& given, int num_sms, cud
                      dim3((L.H / 8 + FB_WARPS * 32 - 1) / (FB_WARPS * 32), parts), dim3(FB_WARPS * 32), 0, s, L.dgate,
                      L.x, L.T, L.H, L.part);
     }
-    if (e != cudaSuccess || !L.dgate_w) return e;
+    if (e != cudaSuccess || !L.dgate_w || (L.gate_first && parts == 1)) return e;
     return launch_sum_partials(L.part, parts, L.H, L.H, L.dgate_w, nullptr, s);
 }
 

@@ -102,8 +102,9 @@ def test_bwd_in_place(ln, f32, H):
 
 
 @pytest.mark.parametrize("ln", [False, True])
-def test_bwd_single_outputs_and_repeats(ln):
-    r, w, _, dy = _inputs(400, 640, False, seed=3)
+@pytest.mark.parametrize("T", [1, 3, 400])
+def test_bwd_single_outputs_and_repeats(T, ln):
+    r, w, _, dy = _inputs(T, 640, False, seed=3)
     want = _run(ln, dy, r, w, None)
     ws = _ws(640)
     for i in range(4 if ln else 3):
