@@ -160,9 +160,14 @@ _lib = _load()
 # The marshalling runs on every call, before any kernel of a small batch can start: it
 # passes plain integers (ctypes converts them by argtypes) and asks torch for the raw
 # stream handle instead of a Stream object (2 us less per call on a Grace core).
-def _stream(stream):
+def _stream(stream, t=None):
+    """The raw handle of stream, or of the current device's current one, which has to be t's device (if given): a kernel
+    of another device would fault on t."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        dev = torch._C._cuda_getDevice()
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream
 
 
@@ -572,7 +577,7 @@ def moe_add_layernorm(x, residual, weight, bias, eps, residual_out, y, q=None, s
                                 _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True),
                                 _ptr(y, "y", _bf16, (T, H), allow_none=True),
                                 _ptr(q, "q", torch.uint8, (T, H), allow_none=True),
-                                _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream))
+                                _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream, x))
     _check("moe_add_layernorm", st)
 
 
@@ -603,7 +608,7 @@ def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream
     dstream or r) = dstream + the norm's part; dx the same in bf16 (it may be dy); dweight [H] fp32.  Outputs may be
     None; ws (moe_workspace_size_bwd) is needed with dweight only."""
     st = _lib.moe_add_rmsnorm_bwd(*_norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight), *_ws(ws),
-                                  _stream(stream))
+                                  _stream(stream, dy))
     _check("moe_add_rmsnorm_bwd", st)
 
 
@@ -611,7 +616,7 @@ def moe_add_layernorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, dbias, w
     """The gradient of moe_add_layernorm's y at its stream r, arguments as moe_add_rmsnorm_bwd; dbias [H] fp32 or None."""
     st = _lib.moe_add_layernorm_bwd(*_norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight),
                                     _ptr(dbias, "dbias", _f32, (weight.shape[0],), allow_none=True), *_ws(ws),
-                                    _stream(stream))
+                                    _stream(stream, dy))
     _check("moe_add_layernorm_bwd", st)
 
 
@@ -624,7 +629,6 @@ def moe_finalize_bwd(dout, y, pair_row, topk_w, y_shared, x, shared_gate_w, dy, 
     T, H = dout.shape
     k = pair_row.shape[1]
     rows_cap = dy.shape[0]
-    wp, wb = _ws(ws)
     st = _lib.moe_finalize_bwd(
         _ptr(dout, "dout", _bf16, (T, H)), _ptr(y, "y", _bf16, (rows_cap, H), allow_none=True), rows_cap,
         _ptr(pair_row, "pair_row", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), T, k, H,
@@ -632,7 +636,8 @@ def moe_finalize_bwd(dout, y, pair_row, topk_w, y_shared, x, shared_gate_w, dy, 
         _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), _ptr(dy, "dy", _bf16, (rows_cap, H)),
         _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True),
         _ptr(dy_shared, "dy_shared", _bf16, (T, H), allow_none=True), _ptr(dgate, "dgate", _f32, (T,), allow_none=True),
-        _ptr(dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True), wp, wb, _stream(stream))
+        _ptr(dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True), _ptr(ws, "ws", torch.uint8), ws.numel(),
+        _stream(stream, dout))
     _check("moe_finalize_bwd", st)
 
 
@@ -643,14 +648,14 @@ def moe_permute_bwd(dx_perm, pair_row, topk_w, x, dx_add, dgate, shared_gate_w, 
     T, k = pair_row.shape
     rows_cap, H = dx_perm.shape
     f32 = dx_add is not None and dx_add.dtype is _f32
-    wp, wb = _ws(ws)
     st = _lib.moe_permute_bwd(
         _ptr(dx_perm, "dx_perm", _bf16, (rows_cap, H)), rows_cap, _ptr(pair_row, "pair_row", _i32, (T, k)),
         _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), _ptr(x, "x", _bf16, (T, H), allow_none=True),
         _ptr(dx_add, "dx_add", _f32 if f32 else _bf16, (T, H), allow_none=True), f32,
         _ptr(dgate, "dgate", _f32, (T,), allow_none=True),
         _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), T, k, H, _ptr(dx, "dx", _bf16, (T, H)),
-        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True), wp, wb, _stream(stream))
+        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True), _ptr(ws, "ws", torch.uint8), ws.numel(),
+        _stream(stream, dx_perm))
     _check("moe_permute_bwd", st)
 
 
@@ -660,11 +665,11 @@ def moe_route_bwd(topk_ids, topk_w, dtopk_w, logits, renorm, dlogits, ws, stream
     may be logits."""
     T, k = topk_ids.shape
     E = dlogits.shape[1]
-    wp, wb = _ws(ws)
     st = _lib.moe_route_bwd(_ptr(topk_ids, "topk_ids", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k)),
                             _ptr(dtopk_w, "dtopk_w", _f32, (T, k)),
                             _ptr(logits, "logits", _f32, (T, E), allow_none=True), T, E, k, int(bool(renorm)),
-                            _ptr(dlogits, "dlogits", _f32, (T, E)), wp, wb, _stream(stream))
+                            _ptr(dlogits, "dlogits", _f32, (T, E)), _ptr(ws, "ws", torch.uint8), ws.numel(),
+                            _stream(stream, topk_ids))
     _check("moe_route_bwd", st)
 
 

@@ -14,10 +14,10 @@ from typing import Optional
 
 import torch
 
-from . import (MOE_NONLOCAL_SKIP, moe_add_layernorm, moe_add_rmsnorm, moe_forward, moe_forward_fp8, moe_forward_nvfp4, moe_forward_w4,
-               moe_forward_w8a8, moe_forward_w8a8_rows, moe_permute, moe_quantize_fp8_rows, moe_quantize_nvfp4_rows,
-               moe_quantize_w4_rows, moe_route, moe_route_grouped, moe_workspace_init, moe_workspace_size,
-               moe_workspace_size_w4, nvfp4_sf_row_bytes)
+from . import (MOE_NONLOCAL_SKIP, moe_add_layernorm, moe_add_rmsnorm, moe_forward, moe_forward_fp8,
+               moe_forward_nvfp4, moe_forward_w4, moe_forward_w8a8, moe_forward_w8a8_rows, moe_permute,
+               moe_quantize_fp8_rows, moe_quantize_nvfp4_rows, moe_quantize_w4_rows, moe_route, moe_route_grouped,
+               moe_workspace_init, moe_workspace_size, moe_workspace_size_w4, nvfp4_sf_row_bytes)
 
 
 class MoELayer:

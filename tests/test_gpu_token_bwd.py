@@ -461,6 +461,23 @@ def test_on_another_stream_and_in_graphs():
     assert _status(ws2) == 0
 
 
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Before anything is launched: the current device is made to look like another one than the tensors'."""
+    x, w, ws = ref.rnd(2, 64), ref.rnd(64), _ws()
+    i, f = torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, 1, device="cuda")
+    n = moe.moe_get_launch_count()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda: moe.moe_add_layernorm(x, x, w, w, 1e-5, x, x),
+                 lambda: moe.moe_add_rmsnorm_bwd(x, x, w, 1e-5, None, x, None, None, None),
+                 lambda: moe.moe_add_layernorm_bwd(x, x, w, 1e-5, None, x, None, None, None, None),
+                 lambda: moe.moe_finalize_bwd(x, x, i, f, None, None, None, x, f, None, None, None, ws),
+                 lambda: moe.moe_permute_bwd(x, i, None, None, None, None, None, x, None, ws),
+                 lambda: moe.moe_route_bwd(i, f, f, None, True, torch.empty_like(f), ws)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert moe.moe_get_launch_count() == n
+
+
 def test_no_rows_at_all():
     """A rank that holds no expert of the batch: no rows, every pair -1."""
     bf = dict(dtype=torch.bfloat16, device="cuda")
