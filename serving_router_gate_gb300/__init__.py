@@ -161,14 +161,14 @@ _lib = _load()
 # passes plain integers (ctypes converts them by argtypes) and asks torch for the raw
 # stream handle instead of a Stream object (2 us less per call on a Grace core).
 def _stream(stream, t=None):
-    """The raw handle of stream, or of the current device's current one, which has to be t's device (if given): a kernel
-    of another device would fault on t."""
-    if stream is None:
-        dev = torch._C._cuda_getDevice()
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{dev}")
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream
+    """The raw handle of stream, or of the current device's current one.  The current device has to be t's (if given): the
+    kernel is launched there and would fault on another device's t."""
+    if stream is not None and t is None:
+        return stream.cuda_stream
+    dev = torch._C._cuda_getDevice()
+    if t is not None and t.get_device() != dev:
+        raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _ptr(t, name, dtype=None, shape=None, allow_none=False):

@@ -472,7 +472,8 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
                  lambda: moe.moe_add_layernorm_bwd(x, x, w, 1e-5, None, x, None, None, None, None),
                  lambda: moe.moe_finalize_bwd(x, x, i, f, None, None, None, x, f, None, None, None, ws),
                  lambda: moe.moe_permute_bwd(x, i, None, None, None, None, None, x, None, ws),
-                 lambda: moe.moe_route_bwd(i, f, f, None, True, torch.empty_like(f), ws)):
+                 lambda: moe.moe_route_bwd(i, f, f, None, True, torch.empty_like(f), ws),
+                 lambda: moe.moe_route_bwd(i, f, f, None, True, torch.empty_like(f), ws, torch.cuda.default_stream(0))):
         with pytest.raises(ValueError, match="current device"):
             call()
     assert moe.moe_get_launch_count() == n
