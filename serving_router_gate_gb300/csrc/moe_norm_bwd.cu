@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
     constexpr int NS = LN ? 4 : 2;                               // a row's sums: d^2, g d (and g)
     constexpr int DY = NP * 512, DS = DY + NP * 64 * C;          // a slot's dy and dstream
     __shared__ alignas(16) float red[2][NB_WARPS * NS];
-    __shared__ float red_mean[2][LN ? NB_WARPS : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.gw, gwarp = warp - group * p.gw;
     const int slot_bytes = DS + (p.ds_ring ? NP * 512 : 0);
@@ -132,6 +131,8 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
 #pragma unroll
     for (int k = 0; k < DYC; ++k) dy_valid |= (uint32_t)(dy_col + k * 256 < a.H) << k;
     const float inv_h = 1.f / (float)a.H;
+    const auto columns = [&](int w) { return (float)max(0, min(a.H - w * NP * 32 * C, NP * 32 * C)); };  // of warp w
+    const float inv_n = 1.f / columns(gwarp);
     const int64_t stride = (int64_t)gridDim.x * p.groups;
     const int64_t first = (int64_t)group * gridDim.x + blockIdx.x;
     const auto group_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.gw * 32) : "memory"); };
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         if (F32) __syncwarp();
         const char* slot = ring + at;
         f2 r[NP][P], g[NP][P];  // NB_REGISTERS: kept from one pass to the next
-        float mean = 0.f;       // negated
+        float mean = 0.f;       // of the warp's columns
         if (LN) {
             f2 sum = 0;
 #pragma unroll
@@ -197,11 +198,9 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
 #pragma unroll
                 for (int i = 0; i < P; ++i) sum = f2_add(sum, r[k][i]);
             }
-            float m[1] = {f2_sum(sum)};
-            group_sums<1>(m, red_mean[it], p.gw, group * p.gw, warp, lane, group_sync);
-            mean = m[0] * -inv_h;
+            mean = warp_sum(f2_sum(sum)) * inv_n;
         }
-        const f2 off = f2_make(mean, mean);
+        const f2 off = f2_make(-mean, -mean);
         f2 sd = 0, sg = 0, sgd = 0;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
@@ -222,10 +221,33 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         float sums[NS] = {};
         sums[0] = f2_sum(sd);
         sums[1] = f2_sum(sgd);
-        if (LN) sums[NS - 2] = f2_sum(sg);
-        group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync);
+        float e = 0.f;  // the warp's mean less the row's
+        if (LN) {
+            sums[NS - 2] = f2_sum(sg);
+            sums[NS - 1] = lane == 0 ? mean : 0.f;
+        }
+        if constexpr (LN) {
+            float first_mean = mean;
+            group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync, [&](float (&v)[NS], int w, const float* q) {
+                first_mean = q[NS - 1];
+                const float n = columns(w), ew = v[NS - 1] - first_mean;
+                v[0] = fmaf(n * ew, ew, v[0]);
+                v[1] = fmaf(ew, v[NS - 2], v[1]);
+                v[NS - 1] = n * ew;
+            });
+            if (p.gw > 1) {
+                const float m = sums[NS - 1] * inv_h;  // the row's mean less the first warp's
+                e = (mean - first_mean) - m;
+                sums[0] = fmaf(-m, sums[NS - 1], sums[0]);
+                if (sums[0] < 0.f) sums[0] = 0.f;  // NaN stays
+                sums[1] = fmaf(-m, sums[NS - 2], sums[1]);
+            }
+        } else {
+            group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync);
+        }
         const float rstd = rsqrtf(fmaf(sums[0], inv_h, a.eps));
-        const float mg = LN ? -sums[NS - 2] * inv_h : 0.f, mgd = -rstd * rstd * (sums[1] * inv_h);
+        const float mgd = -rstd * rstd * (sums[1] * inv_h), mg = LN ? fmaf(e, mgd, -sums[NS - 2] * inv_h) : 0.f;
+        const f2 e_rstd2 = f2_make(e * rstd, e * rstd);
         const f2 rstd2 = f2_make(rstd, rstd), mg2 = f2_make(mg, mg), mgd2 = f2_make(mgd, mgd);
         const int64_t out = row * a.H + col;
 #pragma unroll
@@ -243,7 +265,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
             for (int i = 0; i < P; ++i) {
                 const f2 wi = HOLD ? held_w[HOLD ? k : 0][i] : w[i];
                 const f2 d = LN && !HOLD ? f2_add(r[k][i], off) : r[k][i];
-                dw[k][i] = f2_fma(g[k][i], f2_mul(d, rstd2), dw[k][i]);
+                dw[k][i] = f2_fma(g[k][i], LN ? f2_fma(d, rstd2, e_rstd2) : f2_mul(d, rstd2), dw[k][i]);
                 if (LN) db[LN ? k : 0][i] = f2_add(db[LN ? k : 0][i], g[k][i]);
                 const f2 gw = LN ? f2_fma(g[k][i], wi, mg2) : f2_mul(g[k][i], wi);
                 o[i] = f2_fma(rstd2, f2_fma(d, mgd2, gw), o[i]);

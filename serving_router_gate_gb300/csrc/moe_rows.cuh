@@ -83,9 +83,16 @@ __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
 // The sums of N values over a group of gw <= 16 warps, the same in every thread; warp is the
 // warp in its CTA and first the group's first one.  red: N floats a warp of the CTA, 16-byte
 // aligned; sync: the group's barrier.  A caller alternates between two arrays.
-template <int N, typename Sync>
+//
+// join(v, w, q), for gw > 1: makes the sums of the group's warp w, v, ready to be added to the
+// others'; q: those of the group's first warp.
+struct JoinNothing {
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&)[N], int, const float*) const {}
+};
+template <int N, typename Sync, typename Join = JoinNothing>
 __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int gw, int first, int warp, int lane,
-                                           const Sync& sync) {
+                                           const Sync& sync, const Join& join = Join()) {
     float mine = lane_sums<N, false>(v, lane);
     if (gw == 1) {
 #pragma unroll
@@ -105,6 +112,7 @@ __device__ __forceinline__ void group_sums(float (&v)[N], float* red, int gw, in
     } else {
         v[0] = q[0];
     }
+    join(v, w, red + first * N);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = w < gw ? v[i] : 0.f;
     mine = lane_sums<N, true>(v, lane);
