@@ -15,15 +15,24 @@
 // thread to the same columns of every row of its group, so the weight's sums stay in registers
 // to the end of a persistent grid; a CTA's groups then add theirs in order, and a second kernel
 // adds the CTAs'.  A thread copies its own columns of the rows to come into shared memory
-// (cp.async): the copies need no barrier, and a row's one barrier (the layer norm's two: the mean
-// comes first, so that a row far from zero keeps its variance) joins its warps' sums.
+// (cp.async): the copies need no barrier, and a row's one barrier joins its warps' sums.
+//
+// The layer norm's row needs its mean before its squares, or a row far from zero loses its
+// variance.  A warp takes the mean c of its own n columns and sums about that; with e = c - c0, c0
+// the first warp's c, the row's sums are
+//
+//   m = sum(n e) / H  (the row's mean is c0 + m),  sum(d^2) = sum(ss + n e^2) - H m^2,
+//   sum(g d) = sum(sgd + e sg) - m sum(sg)
+//
+// where H m^2 is at most H / n of the result, 16, whatever c0 is: one
+// barrier instead of two (28672 rows of 2048, bf16, 85 -> 79 us).
 //
 // Narrow rows keep r, dy and the weight in registers from one pass to the next; rows of more
 // columns a thread read them again (the weight from shared memory, in binary32).
 //
-// 16384 rows of 7168 with a stream's gradient: RMS, bf16 138.5 us, 6.8 TB/s, 1.01 of this card's
-// copy rate; fp32 310 us, 0.91; layer norm, bf16 166 us, 0.84; fp32 271 us, 1.04.  4096 of 2048,
-// fp32, layer norm 26.7 us, 0.75; 777 of 1408, bf16 8 us, of which the second kernel 3.
+// 16384 rows of 7168 with a stream's gradient: RMS, bf16 139 us, 6.8 TB/s, 1.01 of this card's
+// copy rate, layer norm 155 us, 0.91; 8192 rows, fp32: 123 us, 1.0, and 124 us.  4096 of 2048,
+// fp32, layer norm 26.7 us, 0.75; 777 of 1408, bf16 7.6 us, of which the second kernel 3.
 #include <algorithm>
 #include <atomic>
 
@@ -35,16 +44,17 @@ namespace {
 
 constexpr int NB_WARPS = 16;           // warps of a CTA at most, one CTA an SM
 constexpr int NB_SMEM = 227 * 1024 - 1024;  // of a CTA, less the static arrays
-// bytes of an fp32 stream's rows, one for each of a CTA's groups, and where there are few rows
-constexpr int NB_F32_ROWS = 48 * 1024, NB_F32_FEW = 64 * 1024;
 
 // What a kernel keeps: the row's r, dy and the weight in registers from one pass to the next, or
-// the weight in shared memory in binary32, or nothing.
-enum { NB_REGISTERS, NB_SHARED, NB_NOTHING };
+// the weight in shared memory in binary32 (NB_SHARED_R: and r in registers; NB_SHARED_DS: the ring
+// has no room for dstream), or nothing (and no room for dstream).
+enum { NB_REGISTERS, NB_SHARED, NB_SHARED_R, NB_SHARED_DS, NB_NOTHING };
+// Warps of a CTA that leave NB_SHARED_R its registers.  Layer norm, bf16, 9600 rows of 6144 80 us, 91
+// with r read again; 5000 of 12288 87 / 100.
+constexpr int NB_R_WARPS = 12;
 
 struct NormBwdPlan {
     int gw, groups, slots;   // warps of a group, groups of a CTA, rows that a group's ring holds
-    bool ds_ring;            // dstream goes through the ring
     float* out;              // a CTA's column sums: CTA i's of dweight at i * out_stride, of dbias
     int64_t out_stride, out_bias;  // out_bias behind
 };
@@ -108,17 +118,19 @@ __device__ __forceinline__ void nb_put_f32(void* p, const f2 f[2]) {
 // NP pieces a thread: 8 columns of a bf16 stream, or 4 of an fp32 one (16 bytes either way, so
 // that a warp's copies and stores cover whole lines).  A warp's pieces lie side by side.
 template <int NP, bool F32, bool LN, int KEEP>
-__global__ void __launch_bounds__(NB_WARPS * 32, 1)
+__global__ void __launch_bounds__((KEEP == NB_SHARED_R ? NB_R_WARPS : NB_WARPS) * 32, 1)
     norm_bwd_kernel(const __grid_constant__ NormBwdLaunch a, const __grid_constant__ NormBwdPlan p) {
     extern __shared__ uint4 smem[];  // [NB_SHARED: gw * NP pieces of weight], [warp][slot] r, dy, dstream
-    constexpr bool HOLD = KEEP == NB_REGISTERS, W_SMEM = KEEP == NB_SHARED;
+    constexpr bool HOLD = KEEP == NB_REGISTERS, W_SMEM = !HOLD && KEEP != NB_NOTHING;
+    constexpr bool HOLD_R = HOLD || KEEP == NB_SHARED_R, DS_RING = KEEP != NB_SHARED_DS && KEEP != NB_NOTHING;
+    constexpr int DB = LN ? 2 : 4;                               // as many as leave the sums their registers
     constexpr int C = F32 ? 4 : 8, P = C / 2, SB = F32 ? 4 : 2;  // columns, pairs of a piece; bytes of a stream value
     constexpr int NS = LN ? 4 : 2;                               // a row's sums: d^2, g d (and g)
     constexpr int DY = NP * 512, DS = DY + NP * 64 * C;          // a slot's dy and dstream
     __shared__ alignas(16) float red[2][NB_WARPS * NS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.gw, gwarp = warp - group * p.gw;
-    const int slot_bytes = DS + (p.ds_ring ? NP * 512 : 0);
+    const int slot_bytes = DS + (DS_RING && a.dstream ? NP * 512 : 0);
     const int col = (gwarp * NP * 32 + lane) * C;                // of piece 0; piece k: + k * 32 * C
     uint32_t valid = 0;
 #pragma unroll
@@ -152,7 +164,9 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
             for (int k = 0; k < NP; ++k) {
                 if (!(valid >> k & 1)) continue;
                 cp_async16(s + lane * 16 + k * 512, r + k * 512);
-                if (p.ds_ring) cp_async16(s + lane * 16 + DS + k * 512, ds + k * 512);
+                if (DS_RING && a.dstream) cp_async16(s + lane * 16 + DS + k * 512, ds + k * 512);
+                if (!DS_RING && a.dstream && lane % 8 == 0)  // 6000 rows of 9728, layer norm: 198 -> 154 us
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(ds + k * 512));
             }
 #pragma unroll
             for (int k = 0; k < DYC; ++k)
@@ -206,7 +220,7 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         for (int k = 0; k < NP; ++k) {
             if (!(valid >> k & 1)) continue;
             f2 w[P];
-            if (!LN || !HOLD) nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
+            if (!LN || !HOLD_R) nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
             nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g[k]);
             if (!HOLD) read_weight(k, w);
 #pragma unroll
@@ -221,20 +235,19 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         float sums[NS] = {};
         sums[0] = f2_sum(sd);
         sums[1] = f2_sum(sgd);
-        float e = 0.f;  // the warp's mean less the row's
-        if (LN) {
+        float e = 0.f;  // the warp's mean less the row's: d = r - the warp's mean + e
+        if constexpr (LN) {
             sums[NS - 2] = f2_sum(sg);
             sums[NS - 1] = lane == 0 ? mean : 0.f;
-        }
-        if constexpr (LN) {
-            float first_mean = mean;
-            group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync, [&](float (&v)[NS], int w, const float* q) {
+            float first_mean = mean;  // c0
+            const auto join = [&](float (&v)[NS], int w, const float* q) {
                 first_mean = q[NS - 1];
                 const float n = columns(w), ew = v[NS - 1] - first_mean;
                 v[0] = fmaf(n * ew, ew, v[0]);
                 v[1] = fmaf(ew, v[NS - 2], v[1]);
                 v[NS - 1] = n * ew;
-            });
+            };
+            group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync, join);
             if (p.gw > 1) {
                 const float m = sums[NS - 1] * inv_h;  // the row's mean less the first warp's
                 e = (mean - first_mean) - m;
@@ -250,21 +263,28 @@ __global__ void __launch_bounds__(NB_WARPS * 32, 1)
         const f2 e_rstd2 = f2_make(e * rstd, e * rstd);
         const f2 rstd2 = f2_make(rstd, rstd), mg2 = f2_make(mg, mg), mgd2 = f2_make(mgd, mgd);
         const int64_t out = row * a.H + col;
+        uint4 ds[DB];  // not DS_RING: so many pieces of dstream in flight
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
+            if (!DS_RING && k % DB == 0 && a.dstream)
+#pragma unroll
+                for (int b = 0; b < DB; ++b)
+                    if (valid >> (k + b) & 1)
+                        ds[b] = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.dstream) + out * SB +
+                                                                (k + b) * 512);
             if (!(valid >> k & 1)) continue;
             f2 w[P], o[P] = {};
+            if (!HOLD_R) nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
             if (!HOLD) {
-                nb_stream<F32>(slot + lane * 16 + k * 512, r[k]);
                 nb_bf16<C>(slot + lane * 2 * C + DY + k * 64 * C, g[k]);
                 read_weight(k, w);
             }
-            if (p.ds_ring) nb_stream<F32>(slot + lane * 16 + DS + k * 512, o);
-            else if (a.dstream) nb_stream<F32>(static_cast<const char*>(a.dstream) + out * SB + k * 512, o);
+            if (DS_RING && a.dstream) nb_stream<F32>(slot + lane * 16 + DS + k * 512, o);
+            else if (!DS_RING && a.dstream) nb_stream<F32>(&ds[k % DB], o);
 #pragma unroll
             for (int i = 0; i < P; ++i) {
                 const f2 wi = HOLD ? held_w[HOLD ? k : 0][i] : w[i];
-                const f2 d = LN && !HOLD ? f2_add(r[k][i], off) : r[k][i];
+                const f2 d = LN && !HOLD_R ? f2_add(r[k][i], off) : r[k][i];
                 dw[k][i] = f2_fma(g[k][i], LN ? f2_fma(d, rstd2, e_rstd2) : f2_mul(d, rstd2), dw[k][i]);
                 if (LN) db[LN ? k : 0][i] = f2_add(db[LN ? k : 0][i], g[k][i]);
                 const f2 gw = LN ? f2_fma(g[k][i], wi, mg2) : f2_mul(g[k][i], wi);
@@ -373,32 +393,42 @@ cudaError_t launch_norm_bwd_kernel(const NormBwdLaunch& L, const NormBwdPlan& p,
 
 template <bool F32, bool LN>
 cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
-    // 16 columns a thread, or 32, which shares what a row costs beside its elements among more
-    // of them and lets two groups of warps work on a CTA's rows where 16 allow one; us with 16 /
-    // 32, 58.7 M elements: bf16, RMS 4096 77 / 78, 5120 84 / 80 (10 warps / 15), 7168 76 / 78;
-    // bf16, layer norm 1024 55 / 63, 1408 78 / 85, 2048 86 / 83, 4096 91 / 83, 7168 103 / 92;
-    // fp32, layer norm 4096 153 / 170, 5120 145 / 173, 7168 163 / 147.
+    // 16 columns a thread, or 32: those share what a row costs beside its elements among more of
+    // them and let more groups of warps work on a CTA's rows, where groups of 16 columns leave many
+    // of the 16 warps idle.  us with 16 / 32, 58.7 M elements: bf16, RMS 4096 77 / 78, 5120 84 / 80 (10
+    // warps / 15), 7168 76 / 78; bf16, layer norm 2560 82 / 86, 4096 81 / 83, 5120 - / 83, 7168 85 / 78,
+    // 8192 83 / 86, but 1408 rows of 4096 15 / 18; fp32, layer norm 4096 132 / 123, 5120 122 / 135, without
+    // dstream 120 / 98.
     const int narrow = (L.H + 511) / 512;  // warps of a group, 16 columns a thread
-    const bool wide = F32 ? L.H > 6144 : LN ? L.H > 2048 : narrow > NB_WARPS || NB_WARPS / narrow * narrow < 14;
+    const int idle = narrow > NB_WARPS ? NB_WARPS : NB_WARPS % narrow;
+    const bool few = L.T * std::min(narrow, NB_WARPS) < 160LL * num_sms;
+    const bool wide = !LN ? (F32 ? L.H > 6144 : idle > 2)
+                      : !F32 ? idle > 1 && !(few && narrow <= NB_WARPS)
+                             : narrow > NB_WARPS || (L.dstream ? narrow == 7 || narrow == 8 : idle > 2);
     const int columns = wide ? 32 : 16;
     NormBwdPlan p;
     p.gw = (L.H + columns * 32 - 1) / (columns * 32);
     const size_t stream = (size_t)p.gw * 32 * columns * (F32 ? 4 : 2), weight = wide ? (size_t)p.gw * 128 * columns : 0;
     const size_t slot = stream + (size_t)p.gw * 64 * columns;  // a row of a group, without dstream
-    // dstream stays out of the ring where it leaves no room for two rows
-    p.ds_ring = L.dstream && 2 * (slot + stream) <= NB_SMEM;
-    const size_t row = slot + (p.ds_ring ? stream : 0);
-    // The rows that an SM holds: past about 50 KB on their way the memory slows down with an
-    // fp32 stream (28672 rows of 2048, RMS: 2 groups of 2 rows 142 us, of 3 163, 4 groups of 2
-    // 153), and a little with a bf16 one (4 groups of 2 76 us, of 3 78, of 4 82); the layer norm
-    // takes longer over a row and wants the third (fp32, 14336 rows of 4096: 153 us against 193).
+    // dstream stays out of the ring where that leaves no room for two rows and the weight
+    const bool ds_out = L.dstream && weight + 2 * (slot + stream) > NB_SMEM;
+    const size_t row = slot + (L.dstream && !ds_out ? stream : 0);
     // Few rows an SM want fewer groups than a long run of them: a start of fewer copies and fewer
     // sums to add at the end, and no SM without rows.  12 warps instead of 16 (RMS: always), us:
     // bf16, RMS 4096 rows of 2048 16.6 / 18.1, 8192 of 1024 16.9 / 18.7; layer norm 4096 of 2048
     // 20.1 / 21.7, but 28672 99 / 86.
-    const bool few = L.T < 40LL * num_sms;
-    p.groups = (!wide && p.gw <= 4 && (few || !LN) ? 12 : NB_WARPS) / p.gw;
-    if (F32) p.groups = std::max(1, std::min(p.groups, (int)((few ? NB_F32_FEW : NB_F32_ROWS) / row)));
+    p.groups = (!wide && p.gw <= 4 && (!LN || few || (F32 && p.gw == 1)) ? 12 : NB_WARPS) / p.gw;
+    // An fp32 stream's rows on their way: with too many the memory slows down.  us of 123 at the
+    // copy rate, groups x rows of each: RMS 28672 rows of 2048 3 x 2 122, 4 x 2 153; 22937 of 2560 1 x 2
+    // 154, 2 x 3 129; layer norm 57344 of 1024 6 x 2 125, 4 x 3 129, 22937 of 2560 2 x 2 127, 2 x 3 122;
+    // 9600 of 6144 1 x 2 124, 1 x 3 132.  Without dstream, of 88: RMS 2048 3 x 2 91, 3 x 3 103, 5120 1 x 2
+    // 100, 1 x 3 89; layer norm 2048 4 x 2 93, 4 x 3 100, 8192 1 x 2 97, 1 x 3 93.
+    int most = 3;
+    if (F32) {
+        const size_t ring = (LN ? 160 : L.dstream && p.gw > 1 ? 120 : 96) * 1024, start = LN && !wide ? 120 * 1024 : ring;
+        p.groups = std::max(1, std::min(p.groups, (int)(start / (2 * row))));
+        most = LN && p.groups > 3 ? 2 : (int)std::min<size_t>(3, std::max<size_t>(2, ring / (p.groups * row)));
+    }
     // As many rows as one CTA has groups go to one CTA, whose sums need no second kernel (4 rows of
     // 512, layer norm 3.6 us against 4.4 on the GPU, and a launch less for the host).
     const bool one = L.T <= p.groups && L.dweight && (!LN || L.dbias);
@@ -407,14 +437,19 @@ cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream
     p.out = one ? L.dweight : L.part;
     p.out_bias = one ? (int64_t)(reinterpret_cast<intptr_t>(L.dbias) - reinterpret_cast<intptr_t>(L.dweight)) / 4 : L.H;
     p.out_stride = 2 * (int64_t)L.H;
-    const bool w_smem = wide && weight + 2 * p.groups * row <= NB_SMEM;
+    const bool w_smem = wide && (!F32 || weight + 2 * row <= NB_SMEM);
     const size_t below = w_smem ? weight : 0;
-    p.slots = (int)std::min<size_t>(F32 && !LN ? 2 : 3, (NB_SMEM - below) / (p.groups * row));
+    p.slots = (int)std::min<size_t>(most, (NB_SMEM - below) / (p.groups * row));
     const size_t smem = std::max(below + p.groups * p.slots * row, (size_t)8 * L.H);  // the groups' sums take 8 * H
     constexpr int NP = F32 ? 4 : 2;
     if (!wide) return launch_norm_bwd_kernel<NP, F32, LN, NB_REGISTERS>(L, p, grid, one, smem, s);
-    if (w_smem) return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_SHARED>(L, p, grid, one, smem, s);
-    return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_NOTHING>(L, p, grid, one, smem, s);
+    if constexpr (F32)
+        if (!w_smem) return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_NOTHING>(L, p, grid, one, smem, s);
+    if (ds_out) return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_SHARED_DS>(L, p, grid, one, smem, s);
+    if constexpr (LN && !F32)
+        if (p.gw * p.groups <= NB_R_WARPS)
+            return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_SHARED_R>(L, p, grid, one, smem, s);
+    return launch_norm_bwd_kernel<2 * NP, F32, LN, NB_SHARED>(L, p, grid, one, smem, s);
 }
 
 }  // namespace

@@ -85,6 +85,38 @@ def test_bwd_many_rows_an_sm(H, f32, ln):
     _check(ln, dy, r, w, None, _run(ln, dy, r, w, None))
 
 
+@pytest.mark.parametrize("T, H", [(3600, 3584), (2400, 5632), (310, 9728), (310, 12288), (310, 13312), (310, 16384)])
+@pytest.mark.parametrize("stream", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("ln", [False, True])
+def test_bwd_wide_rows(T, H, stream, f32, ln):
+    """With a stream's gradient and without: the widest leave it no room in shared memory."""
+    r, w, _, dy = _inputs(T, H, f32, seed=14)
+    ds = ref.rnd(T, H, seed=15, std=0.01, dtype=r.dtype) if stream else None
+    _check(ln, dy, r, w, ds, _run(ln, dy, r, w, ds))
+
+
+@pytest.mark.parametrize("H", [520, 1024, 2048, 5000, 7168, 8200, 16384])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("kind", ["first", "last", "ramp"])
+def test_bwd_parts_of_a_row_far_from_each_other(H, f32, kind):
+    """The layer norm's means of a row's parts are joined to the row's."""
+    r, w, _, dy = _inputs(7, H, True, seed=16)
+    col = torch.arange(H, device="cuda")
+    r = r + {"first": 500.0 * (col < 512), "last": 500.0 * (col >= H - 8), "ramp": 0.25 * col}[kind]
+    r = r if f32 else r.to(torch.bfloat16)
+    _check(True, dy, r, w, None, _run(True, dy, r, w, None))
+
+
+@pytest.mark.parametrize("H", [64, 2048, 7168])
+@pytest.mark.parametrize("f32", [False, True])
+def test_bwd_rows_of_one_value(H, f32):
+    """No variance at all: the deviations are 0 and rstd is 1 / sqrt(eps)."""
+    r = torch.full((5, H), 3.25, device="cuda", dtype=torch.float32 if f32 else torch.bfloat16)
+    _, w, _, dy = _inputs(5, H, f32, seed=17)
+    _check(True, dy, r, w, None, _run(True, dy, r, w, None))
+
+
 @pytest.mark.parametrize("ln", [False, True])
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("H", [256, 1024, 7168])
