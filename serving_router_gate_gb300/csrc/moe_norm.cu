@@ -27,6 +27,7 @@
 #include <algorithm>
 
 #include "moe_internal.cuh"
+#include "moe_rows.cuh"
 
 namespace moe {
 namespace {
@@ -158,11 +159,15 @@ __global__ void __launch_bounds__(THREADS > 32 ? THREADS : NM_WARPS * 32) add_rm
     }
 }
 
-// The layer norm, laid out like the RMS norm: the mean's reduction, then that of the squares of
-// the deviations from it.  CTAS CTAs an SM: the second reduction wants more rows on their way
-// than the registers would leave by themselves.  An fp32 stream that lies on 32 bytes is read and
-// written 32 bytes a lane: with 16 a request covers half of each of its sectors (8192 rows of 7168
-// with E4M3 rows 116 us against 123, 4778 of 12288 119 against 132).
+// The layer norm, laid out like the RMS norm: the mean's reduction, then that of the deviations from
+// it and of their squares.  A mean is off by up to 2^-18 of the row's absolute mean (no chain of its
+// sum is longer than 64 additions), which 1 / sqrt(eps) would carry into rows of little variance far
+// from zero: an fp32 row of 10000.3 gave y up to half a weight off its bias.  The deviations' own
+// mean takes that error out of the mean and of the variance, to 2^-18 of itself, for one addition
+// more an element.  CTAS CTAs an SM: the second reduction wants more rows on their way than the
+// registers would leave by themselves.  An fp32 stream that lies on 32 bytes is read and written 32
+// bytes a lane: with 16 a request covers half of each of its sectors (8192 rows of 7168 with E4M3
+// rows 116 us against 123, 4778 of 12288 119 against 132).
 enum { NM_BF16, NM_F32, NM_F32_WIDE };
 
 template <int STREAM>
@@ -193,25 +198,31 @@ __device__ __forceinline__ void nm_stream_store(void* res, int64_t off, const fl
 
 constexpr int nm_threads(int threads) { return threads > 32 ? threads : NM_WARPS * 32; }
 
-// Sum of v over a row's WARPS warps (red: one word each), the same in every thread.
-template <int WARPS>
-__device__ __forceinline__ float nm_row_sum(float v, float* red) {
+// Sums of v's N values over a row's WARPS warps (red: N words each), the same in every thread.
+template <int WARPS, int N>
+__device__ __forceinline__ void nm_row_sums(float (&v)[N], float* red) {
+    const int lane = threadIdx.x & 31;
+    const float mine = lane_sums<N, false>(v, lane);
+    if (WARPS == 1) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (WARPS == 1) return v;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, mine, i * (32 / N));
+        return;
+    }
+    if (lane % (32 / N) == 0) red[(threadIdx.x >> 5) * N + lane / (32 / N)] = mine;
     __syncthreads();
-    float tot = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) tot += red[w];
-    return tot;
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += red[w * N + i];
 }
 
 template <int VPT, int THREADS, int STREAM, int CTAS>
 __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kernel(const __grid_constant__ NormLaunch a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ float red_mean[2][WARPS];
-    __shared__ float red_sum[2][WARPS];
+    __shared__ float red_sum[2][2 * WARPS];
     __shared__ uint32_t red_max[2][WARPS];
     constexpr bool ALONE = THREADS == 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kerne
     for (int64_t row = ALONE ? (int64_t)blockIdx.x * NM_WARPS + warp : blockIdx.x; row < a.T; row += rows, it ^= 1) {
         const int64_t base = row * a.H;
         float f[VPT][8];
-        float sum = 0.f;
+        float sum[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = first + j * THREADS;
@@ -237,23 +248,37 @@ __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kerne
                 for (int i = 0; i < 8; ++i) f[j][i] += r[i];
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += f[j][i];
+            for (int i = 0; i < 8; ++i) sum[0] += f[j][i];
         }
-        const float mean = nm_row_sum<WARPS>(sum, red_mean[it]) / (float)a.H;
-        float ss = 0.f;
+        nm_row_sums<WARPS>(sum, red_mean[it]);
+        const float near = sum[0] / (float)a.H;
+        const f2 to_near = f2_make(-near, -near);
+        f2 ss = 0, sd = 0;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (first + j * THREADS >= vec) continue;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(f[j][i] - mean, f[j][i] - mean, ss);
+            for (int i = 0; i < 8; i += 2) {
+                const f2 d = f2_add(f2_make(f[j][i], f[j][i + 1]), to_near);
+                ss = f2_fma(d, d, ss);
+                sd = f2_add(sd, d);
+            }
         }
-        const float tot = nm_row_sum<WARPS>(ss, red_sum[it]);
+        float sums[2] = {f2_sum(ss), f2_sum(sd)};
+        nm_row_sums<WARPS>(sums, red_sum[it]);
+        // the mean in two words, near + off = mean + rest; a rest below the error of its own sum is
+        // none, so that a row of equal values leaves no deviation
+        const float off = sums[1] / (float)a.H, mean = near + off;
+        float rest = (near - mean) + off;
+        if (fabsf(rest) <= 0x1p-18f * fabsf(off)) rest = 0.f;
+        const float tot = sums[0] < INFINITY ? fmaxf(fmaf(-off, sums[1], sums[0]), 0.f) : sums[0];  // NaN stays
         // the root's reciprocal in two words, as for the RMS norm
         const float ms = tot / (float)a.H + a.eps;
         const float hi = __frsqrt_rn(ms);
         const float sq = ms * hi, err = fmaf(-sq, hi, 1.f) - fmaf(ms, hi, -sq) * hi;
         float lo = 0.5f * hi * err;
         if (!(fabsf(lo) < hi)) lo = 0.f;  // not finite: an infinite or zero mean square
+        const float shift = -rest * hi;
         uint32_t mx = 0u;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -266,7 +291,7 @@ __global__ void __launch_bounds__(nm_threads(THREADS), CTAS) add_layernorm_kerne
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float d = f[j][i] - mean;
-                f[j][i] = fmaf(fmaf(d, hi, d * lo), w[i], b[i]);
+                f[j][i] = fmaf(fmaf(d, hi, fmaf(d, lo, shift)), w[i], b[i]);
                 mx = max(mx, __float_as_uint(f[j][i]) & 0x7FFFFFFFu);
             }
             if (a.y) *reinterpret_cast<uint4*>(a.y + base + 8 * v) = pack8(f[j]);
@@ -303,9 +328,9 @@ cudaError_t launch_layernorm_size(const NormLaunch& L, int num_sms, cudaStream_t
 template <int STREAM>
 cudaError_t launch_layernorm_type(const NormLaunch& L, int num_sms, cudaStream_t s) {
     // 58.7 M elements with E4M3 rows, fp32 (on 32 bytes) / bf16 stream, us (114 / 79 at the copy rate):
-    // 512 66 / 51, 1024 116 / 81, 1408 117 / 98, 2048 114 / 81, 4096 113 / 85, 5120 116 / 85, 6144 114 /
-    // 92, 7168 116 / 93, 8192 116 / 96, 16384 127 / 104.  At 7168 three CTAs of 448 threads, bf16: 100,
-    // four of 224: 103.
+    // 256 111 / 86, 512 112 / 81, 1024 116 / 86, 1408 116 / 100, 2048 113 / 81, 4096 112 / 85, 5120 114 /
+    // 86, 6144 113 / 92, 7168 115 / 95, 8192 115 / 97, 12288 120 / 97, 16384 129 / 107.  At 7168, bf16, 92
+    // before the deviations' sum was taken, where three CTAs of 448 threads took 100, four of 224 103.
     const int vec = L.H / 8;
     if (vec <= 32) return launch_layernorm_size<1, 32, STREAM, 6>(L, num_sms, s);
     if (vec <= 64) return launch_layernorm_size<2, 32, STREAM, 6>(L, num_sms, s);
