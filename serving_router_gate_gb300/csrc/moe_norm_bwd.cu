@@ -19,13 +19,17 @@
 //
 // The layer norm's row needs its mean before its squares, or a row far from zero loses its
 // variance.  A warp takes the mean c of its own n columns and sums about that; with e = c - c0, c0
-// the first warp's c, the row's sums are
+// the first warp's c, and sd the warp's sum of r - c, what the roundings of c left over, the row's
+// sums are
 //
-//   m = sum(n e) / H  (the row's mean is c0 + m),  sum(d^2) = sum(ss + n e^2) - H m^2,
+//   m = sum(n e + sd) / H  (the row's mean is c0 + m),  sum(d^2) = sum(ss + e (n e + 2 sd)) - H m^2,
 //   sum(g d) = sum(sgd + e sg) - m sum(sg)
 //
 // where H m^2 is at most H / n of the result, 16, whatever c0 is: one
-// barrier instead of two (28672 rows of 2048, bf16, 85 -> 79 us).
+// barrier instead of two (28672 rows of 2048, bf16, 85 -> 79 us).  1 / sqrt(eps) would carry sd into
+// rows of little variance: an fp32 stream takes it along (without it an fp32 row of 100.3 had
+// normalised values of 0.002 in place of 0).  A bf16 stream needs it not: where values of 8 bits lie close enough together
+// for their rounding to matter, their binary32 sum is exact, and the quotient is rounded once.
 //
 // Narrow rows keep r, dy and the weight in registers from one pass to the next; rows of more
 // columns a thread read them again (the weight from shared memory, in binary32).
@@ -125,9 +129,11 @@ __global__ void __launch_bounds__((KEEP == NB_SHARED_R ? NB_R_WARPS : NB_WARPS) 
     constexpr bool HOLD_R = HOLD || KEEP == NB_SHARED_R, DS_RING = KEEP != NB_SHARED_DS && KEEP != NB_NOTHING;
     constexpr int DB = LN ? 2 : 4;                               // as many as leave the sums their registers
     constexpr int C = F32 ? 4 : 8, P = C / 2, SB = F32 ? 4 : 2;  // columns, pairs of a piece; bytes of a stream value
-    constexpr int NS = LN ? 4 : 2;                               // a row's sums: d^2, g d (and g)
+    constexpr int NS = LN ? 4 : 2;                               // a row's sums: d^2, g d (and g, d or c)
     constexpr int DY = NP * 512, DS = DY + NP * 64 * C;          // a slot's dy and dstream
     __shared__ alignas(16) float red[2][NB_WARPS * NS];
+    constexpr bool SD = LN && F32;                               // the deviations' sum is one of the four
+    __shared__ float near[2][SD ? NB_WARPS : 1];                 // and c stands here
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = warp / p.gw, gwarp = warp - group * p.gw;
     const int slot_bytes = DS + (DS_RING && a.dstream ? NP * 512 : 0);
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__((KEEP == NB_SHARED_R ? NB_R_WARPS : NB_WARPS) 
     for (int k = 0; k < DYC; ++k) dy_valid |= (uint32_t)(dy_col + k * 256 < a.H) << k;
     const float inv_h = 1.f / (float)a.H;
     const auto columns = [&](int w) { return (float)max(0, min(a.H - w * NP * 32 * C, NP * 32 * C)); };  // of warp w
-    const float inv_n = 1.f / columns(gwarp);
+    const float n = columns(gwarp), inv_n = 1.f / n;
     const int64_t stride = (int64_t)gridDim.x * p.groups;
     const int64_t first = (int64_t)group * gridDim.x + blockIdx.x;
     const auto group_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(p.gw * 32) : "memory"); };
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__((KEEP == NB_SHARED_R ? NB_R_WARPS : NB_WARPS) 
         if (F32) __syncwarp();
         const char* slot = ring + at;
         f2 r[NP][P], g[NP][P];  // NB_REGISTERS: kept from one pass to the next
-        float mean = 0.f;       // of the warp's columns
+        float mean = 0.f;       // c, of the warp's columns
         if (LN) {
             f2 sum = 0;
 #pragma unroll
@@ -212,10 +218,16 @@ __global__ void __launch_bounds__((KEEP == NB_SHARED_R ? NB_R_WARPS : NB_WARPS) 
 #pragma unroll
                 for (int i = 0; i < P; ++i) sum = f2_add(sum, r[k][i]);
             }
-            mean = warp_sum(f2_sum(sum)) * inv_n;
+            const float total = warp_sum(f2_sum(sum));
+            mean = total * inv_n;
+            if (SD) {
+                if (lane == 0) near[it][SD ? warp : 0] = mean;
+            } else {
+                mean = fmaf(fmaf(-mean, n, total), inv_n, mean);
+            }
         }
         const f2 off = f2_make(-mean, -mean);
-        f2 sd = 0, sg = 0, sgd = 0;
+        f2 ss = 0, sg = 0, sgd = 0, sd = 0;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
             if (!(valid >> k & 1)) continue;
@@ -227,34 +239,37 @@ __global__ void __launch_bounds__((KEEP == NB_SHARED_R ? NB_R_WARPS : NB_WARPS) 
             for (int i = 0; i < P; ++i) {
                 if (LN) r[k][i] = f2_add(r[k][i], off);
                 const f2 gw = f2_mul(g[k][i], HOLD ? held_w[HOLD ? k : 0][i] : w[i]);
-                sd = f2_fma(r[k][i], r[k][i], sd);
+                ss = f2_fma(r[k][i], r[k][i], ss);
                 sgd = f2_fma(gw, r[k][i], sgd);
-                if (LN) sg = f2_add(sg, gw);
+                if (LN) {
+                    sg = f2_add(sg, gw);
+                    if (SD) sd = f2_add(sd, r[k][i]);
+                }
             }
         }
         float sums[NS] = {};
-        sums[0] = f2_sum(sd);
+        sums[0] = f2_sum(ss);
         sums[1] = f2_sum(sgd);
-        float e = 0.f;  // the warp's mean less the row's: d = r - the warp's mean + e
+        float e = 0.f;  // the warp's c less the row's mean: d = r - c + e
         if constexpr (LN) {
             sums[NS - 2] = f2_sum(sg);
-            sums[NS - 1] = lane == 0 ? mean : 0.f;
-            float first_mean = mean;  // c0
+            sums[NS - 1] = SD ? f2_sum(sd) : lane == 0 && p.gw > 1 ? mean : 0.f;
+            float first_c = mean;
             const auto join = [&](float (&v)[NS], int w, const float* q) {
-                first_mean = q[NS - 1];
-                const float n = columns(w), ew = v[NS - 1] - first_mean;
-                v[0] = fmaf(n * ew, ew, v[0]);
+                const float* const c = near[it] + (SD ? group * p.gw : 0);
+                first_c = SD ? c[0] : q[NS - 1];
+                const float n = columns(w), ew = (SD ? c[w < p.gw ? w : 0] : v[NS - 1]) - first_c;
+                const float left = SD ? v[NS - 1] : 0.f;
+                v[0] = fmaf(ew, fmaf(n, ew, 2.f * left), v[0]);
                 v[1] = fmaf(ew, v[NS - 2], v[1]);
-                v[NS - 1] = n * ew;
+                v[NS - 1] = fmaf(n, ew, left);
             };
             group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync, join);
-            if (p.gw > 1) {
-                const float m = sums[NS - 1] * inv_h;  // the row's mean less the first warp's
-                e = (mean - first_mean) - m;
-                sums[0] = fmaf(-m, sums[NS - 1], sums[0]);
-                if (sums[0] < 0.f) sums[0] = 0.f;  // NaN stays
-                sums[1] = fmaf(-m, sums[NS - 2], sums[1]);
-            }
+            const float m = sums[NS - 1] * inv_h;  // the row's mean less the first warp's c
+            e = (mean - first_c) - m;
+            sums[0] = fmaf(-m, sums[NS - 1], sums[0]);
+            if (sums[0] < 0.f) sums[0] = 0.f;  // NaN stays
+            sums[1] = fmaf(-m, sums[NS - 2], sums[1]);
         } else {
             group_sums<NS>(sums, red[it], p.gw, group * p.gw, warp, lane, group_sync);
         }

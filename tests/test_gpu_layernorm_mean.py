@@ -65,3 +65,50 @@ def test_layernorm_of_rows_far_from_zero(H, q8):
     if q8:
         val = q.view(torch.float8_e4m3fn).double() * sc.double()[:, None]
         ref.inside(val, want, 2.0 ** -4 * (want.abs() + tol) + 2.0 ** -10 * sc.double()[:, None] + tol, "E4M3 values")
+
+
+def _bf16_rows(H, seed):
+    """Rows of one value, and of one value but for a few columns a bf16 step apart; one row about zero."""
+    r = torch.zeros(7, H, device="cuda")
+    r[:4] = torch.tensor(VALUES, device="cuda")[:, None]
+    r[4], r[5], r[6] = 10000.3, -333.3, ref.rnd(H, seed=seed + 2)
+    r = r.to(torch.bfloat16)
+    r.view(torch.int16)[4, ::3] += 1
+    r.view(torch.int16)[5, H // 2] += 1
+    return r
+
+
+@pytest.mark.parametrize("H", WIDTHS)
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("stream", [False, True])
+def test_gradients_of_rows_far_from_zero(H, f32, stream):
+    """A bf16 stream: the sums of rows of one value are exact.  Elsewhere the mean is off by its last rounding and one
+    more, 2^-23 A at most, which is 2^-16 of 2^-7 A rstd in the normalised values."""
+    x, res = _rows(H, 3)
+    r = res + x.float() if f32 else _bf16_rows(H, 3)
+    w, _ = _vec(H, 7)
+    dy = ref.rnd(7, H, seed=11, std=0.01)
+    ds = ref.rnd(7, H, seed=12, std=0.01, dtype=r.dtype) if stream else None
+    dr, dx = torch.empty_like(r), torch.empty_like(dy)
+    dw, db = torch.empty(H, device="cuda"), torch.empty(H, device="cuda")
+    ws = torch.zeros(moe.moe_workspace_size_bwd(H), dtype=torch.uint8, device="cuda")
+    moe.moe_add_layernorm_bwd(dy, r, w, EPS, ds, dr, dx, dw, db, ws)
+    d, rstd, K = _norm(r.double())
+    if not f32:
+        A = r.double().abs().amax(1, keepdim=True)
+        K = torch.where((d == 0.0).all(1, keepdim=True), 1.0, 1.0 + 2.0 ** -7 * A * rstd)
+    g = dy.double() * w.double()
+    mean = lambda t: t.mean(1, keepdim=True)  # noqa: E731
+    want = rstd * (g - mean(g) - d * rstd * rstd * mean(g * d))
+    amag = mean((g * d).abs()) + mean(g.abs()) / rstd
+    mag = rstd * K * (g.abs() + mean(g.abs()) + (d.abs() + 1.0 / rstd) * rstd * rstd * amag)
+    if stream:
+        want, mag = want + ds.double(), mag + ds.double().abs()
+    tol = TERM * mag
+    rnd = ref.BF * (want.abs() + tol)
+    ref.inside(dr, want, tol + (0.0 if f32 else rnd), "dr")
+    ref.inside(dx, want, tol + rnd, "dx")
+    xh = d * rstd
+    wmag = (dy.double().abs() * K * (xh.abs() + 1.0)).sum(0)
+    ref.inside(dw, (dy.double() * xh).sum(0), (TERM + 129 * ref.U) * wmag, "dweight")
+    ref.inside(db, dy.double().sum(0), 129 * ref.U * dy.double().abs().sum(0), "dbias")
