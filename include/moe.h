@@ -464,7 +464,9 @@ MOE_API moe_status_t moe_add_layernorm(const moe_bf16_t *x, const void *residual
  *   moe_route_bwd            from the routing weights to the logits
  *   moe_add_rmsnorm_bwd, moe_add_layernorm_bwd   from the norm's output to its input
  * Every sum is binary32 and has a fixed order: a call repeats itself bit for bit (on one
- * kind of GPU: the weight gradients are cut by its number of SMs).  bf16 outputs are
+ * kind of GPU: the weight gradients are cut by its number of SMs).  A row of an output does
+ * not depend on the batch that it stands in, with one exception: the dot products behind
+ * moe_permute_bwd's dtopk_w are cut by T and the number of SMs.  bf16 outputs are
  * rounded once.  T = 0 writes nothing but the weight gradients, which are then 0.
  * Outputs are written, not added to, and overlap nothing except where a call says so. */
 

@@ -25,11 +25,12 @@
 //   m = sum(n e + sd) / H  (the row's mean is c0 + m),  sum(d^2) = sum(ss + e (n e + 2 sd)) - H m^2,
 //   sum(g d) = sum(sgd + e sg) - m sum(sg)
 //
-// where H m^2 is at most H / n of the result, 16, whatever c0 is: one
-// barrier instead of two (28672 rows of 2048, bf16, 85 -> 79 us).  1 / sqrt(eps) would carry sd into
+// where H m^2 is at most H / n of the result, 16, whatever c0 is: one barrier instead of two
+// (28672 rows of 2048, bf16, 85 -> 79 us).  1 / sqrt(eps) would carry sd into
 // rows of little variance: an fp32 stream takes it along (without it an fp32 row of 100.3 had
-// normalised values of 0.002 in place of 0).  A bf16 stream needs it not: where values of 8 bits lie close enough together
-// for their rounding to matter, their binary32 sum is exact, and the quotient is rounded once.
+// normalised values of 0.002 in place of 0).  A bf16 stream needs it not: where values of 8 bits lie
+// close enough together for their rounding to matter, their binary32 sum is exact, and the quotient
+// is rounded once.
 //
 // Narrow rows keep r, dy and the weight in registers from one pass to the next; rows of more
 // columns a thread read them again (the weight from shared memory, in binary32).
@@ -410,15 +411,16 @@ template <bool F32, bool LN>
 cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream_t s) {
     // 16 columns a thread, or 32: those share what a row costs beside its elements among more of
     // them and let more groups of warps work on a CTA's rows, where groups of 16 columns leave many
-    // of the 16 warps idle.  us with 16 / 32, 58.7 M elements: bf16, RMS 4096 77 / 78, 5120 84 / 80 (10
-    // warps / 15), 7168 76 / 78; bf16, layer norm 2560 82 / 86, 4096 81 / 83, 5120 - / 83, 7168 85 / 78,
-    // 8192 83 / 86, but 1408 rows of 4096 15 / 18; fp32, layer norm 4096 132 / 123, 5120 122 / 135, without
+    // of the 16 warps idle.  The choice decides the order of a row's sums, so it does not depend on T.
+    // us with 16 / 32, 58.7 M elements: bf16, RMS 4096 77 / 78, 5120 84 / 80 (10
+    // warps / 15), 7168 76 / 78; bf16, layer norm 2560 82 / 86, 2816 96 / 82, 3584 89 / 84, 4096 81 / 83,
+    // 4608 114 / 83, 5632 97 / 85, 7168 92 / 86, 8192 83 / 86, but 777 rows of 2816 10.4 / 13.9, 4608 14.2 /
+    // 16.1, 7168 19.0 / 20.4; fp32, layer norm 4096 132 / 123, 5120 122 / 135, without
     // dstream 120 / 98.
     const int narrow = (L.H + 511) / 512;  // warps of a group, 16 columns a thread
     const int idle = narrow > NB_WARPS ? NB_WARPS : NB_WARPS % narrow;
-    const bool few = L.T * std::min(narrow, NB_WARPS) < 160LL * num_sms;
     const bool wide = !LN ? (F32 ? L.H > 6144 : idle > 2)
-                      : !F32 ? idle > 1 && !(few && narrow <= NB_WARPS)
+                      : !F32 ? idle > 1
                              : narrow > NB_WARPS || (L.dstream ? narrow == 7 || narrow == 8 : idle > 2);
     const int columns = wide ? 32 : 16;
     NormBwdPlan p;
@@ -432,7 +434,13 @@ cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream
     // sums to add at the end, and no SM without rows.  12 warps instead of 16 (RMS: always), us:
     // bf16, RMS 4096 rows of 2048 16.6 / 18.1, 8192 of 1024 16.9 / 18.7; layer norm 4096 of 2048
     // 20.1 / 21.7, but 28672 99 / 86.
+    const bool few = L.T * narrow < 160LL * num_sms;
     p.groups = (!wide && p.gw <= 4 && (!LN || few || (F32 && p.gw == 1)) ? 12 : NB_WARPS) / p.gw;
+    const int64_t rows = (L.T + num_sms - 1) / num_sms;  // of an SM
+    // bf16, layer norm, 32 columns: a group for every six rows.  us with 1 / 2 / 3 / 5 groups: 300 rows of
+    // 4608 9.5 / 12.5, of 7168 12.8 / 14.7; 777 of 2816 13.9 / 11.9 / 12.9 / 14.8; 2048 of 2816 25.6 / 19.1 / 20.0 /
+    // 20.0, of 3584 26.4 / 22.1 / 20.9 / 24.1; 6000 of 2816 63.2 / 40.8 / 36.6 / 33.3.
+    if (LN && !F32 && wide) p.groups = (int)std::max<int64_t>(1, std::min<int64_t>(p.groups, (rows + 2) / 6));
     // An fp32 stream's rows on their way: with too many the memory slows down.  us of 123 at the
     // copy rate, groups x rows of each: RMS 28672 rows of 2048 3 x 2 122, 4 x 2 153; 22937 of 2560 1 x 2
     // 154, 2 x 3 129; layer norm 57344 of 1024 6 x 2 125, 4 x 3 129, 22937 of 2560 2 x 2 127, 2 x 3 122;
@@ -447,7 +455,7 @@ cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream
     // As many rows as one CTA has groups go to one CTA, whose sums need no second kernel (4 rows of
     // 512, layer norm 3.6 us against 4.4 on the GPU, and a launch less for the host).
     const bool one = L.T <= p.groups && L.dweight && (!LN || L.dbias);
-    p.groups = (int)std::min<int64_t>(p.groups, one ? L.T : (L.T + num_sms - 1) / num_sms);
+    p.groups = (int)std::min<int64_t>(p.groups, one ? L.T : rows);
     const int grid = one ? 1 : (int)std::min<int64_t>((L.T + p.groups - 1) / p.groups, std::min(num_sms, kBwdPartials));
     p.out = one ? L.dweight : L.part;
     p.out_bias = one ? (int64_t)(reinterpret_cast<intptr_t>(L.dbias) - reinterpret_cast<intptr_t>(L.dweight)) / 4 : L.H;
