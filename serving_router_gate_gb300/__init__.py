@@ -160,24 +160,32 @@ _lib = _load()
 # The marshalling runs on every call, before any kernel of a small batch can start: it
 # passes plain integers (ctypes converts them by argtypes) and asks torch for the raw
 # stream handle instead of a Stream object (2 us less per call on a Grace core).
-def _stream(stream, t=None):
-    """The raw handle of stream, or of the current device's current one.  The current device has to be t's (if given): the
-    kernel is launched there and would fault on another device's t."""
-    if stream is not None and t is None:
-        return stream.cuda_stream
-    dev = torch._C._cuda_getDevice()
-    if t is not None and t.get_device() != dev:
-        raise ValueError(f"tensors are on cuda:{t.get_device()}, the current device is cuda:{dev}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _stream(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
-def _ptr(t, name, dtype=None, shape=None, allow_none=False):
+def _device(t, name):
+    """t's device, which has to be the current one: the kernels are launched there and would fault on tensors of another
+    (the call's other tensors are held against it by _ptr's dev)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _ptr(t, name, dtype=None, shape=None, allow_none=False, dev=None):
     if t is None:
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -556,12 +564,14 @@ def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y, q=None, scale=Non
     T, H = x.shape
     f32 = residual is not None and residual.dtype is _f32
     rt = _f32 if f32 else _bf16
-    st = _lib.moe_add_rmsnorm(_ptr(x, "x", _bf16, (T, H)), _ptr(residual, "residual", rt, (T, H), allow_none=True),
-                              f32, _ptr(weight, "weight", _bf16, (H,)), eps, T, H,
-                              _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True),
-                              _ptr(y, "y", _bf16, (T, H), allow_none=True),
-                              _ptr(q, "q", torch.uint8, (T, H), allow_none=True),
-                              _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream))
+    dev = _device(x, "x")
+    st = _lib.moe_add_rmsnorm(_ptr(x, "x", _bf16, (T, H)),
+                              _ptr(residual, "residual", rt, (T, H), allow_none=True, dev=dev), f32,
+                              _ptr(weight, "weight", _bf16, (H,), dev=dev), eps, T, H,
+                              _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True, dev=dev),
+                              _ptr(y, "y", _bf16, (T, H), allow_none=True, dev=dev),
+                              _ptr(q, "q", torch.uint8, (T, H), allow_none=True, dev=dev),
+                              _ptr(scale, "scale", _f32, (T,), allow_none=True, dev=dev), _stream(stream))
     _check("moe_add_rmsnorm", st)
 
 
@@ -571,13 +581,15 @@ def moe_add_layernorm(x, residual, weight, bias, eps, residual_out, y, q=None, s
     T, H = x.shape
     f32 = residual is not None and residual.dtype is _f32
     rt = _f32 if f32 else _bf16
-    st = _lib.moe_add_layernorm(_ptr(x, "x", _bf16, (T, H)), _ptr(residual, "residual", rt, (T, H), allow_none=True),
-                                f32, _ptr(weight, "weight", _bf16, (H,)),
-                                _ptr(bias, "bias", _bf16, (H,), allow_none=True), eps, T, H,
-                                _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True),
-                                _ptr(y, "y", _bf16, (T, H), allow_none=True),
-                                _ptr(q, "q", torch.uint8, (T, H), allow_none=True),
-                                _ptr(scale, "scale", _f32, (T,), allow_none=True), _stream(stream, x))
+    dev = _device(x, "x")
+    st = _lib.moe_add_layernorm(_ptr(x, "x", _bf16, (T, H)),
+                                _ptr(residual, "residual", rt, (T, H), allow_none=True, dev=dev), f32,
+                                _ptr(weight, "weight", _bf16, (H,), dev=dev),
+                                _ptr(bias, "bias", _bf16, (H,), allow_none=True, dev=dev), eps, T, H,
+                                _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True, dev=dev),
+                                _ptr(y, "y", _bf16, (T, H), allow_none=True, dev=dev),
+                                _ptr(q, "q", torch.uint8, (T, H), allow_none=True, dev=dev),
+                                _ptr(scale, "scale", _f32, (T,), allow_none=True, dev=dev), _stream(stream))
     _check("moe_add_layernorm", st)
 
 
@@ -589,17 +601,20 @@ def moe_workspace_size_bwd(H) -> int:
     return int(n)
 
 
-def _norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight):
+def _norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight):
     T, H = dy.shape
     f32 = r.dtype is _f32
     rt = _f32 if f32 else _bf16
-    return (_ptr(dy, "dy", _bf16, (T, H)), _ptr(r, "r", rt, (T, H)), f32, _ptr(weight, "weight", _bf16, (H,)), eps, T, H,
-            _ptr(dstream, "dstream", rt, (T, H), allow_none=True), _ptr(dr, "dr", rt, (T, H), allow_none=True),
-            _ptr(dx, "dx", _bf16, (T, H), allow_none=True), _ptr(dweight, "dweight", _f32, (H,), allow_none=True))
+    return (_ptr(dy, "dy", _bf16, (T, H)), _ptr(r, "r", rt, (T, H), dev=dev), f32,
+            _ptr(weight, "weight", _bf16, (H,), dev=dev), eps, T, H,
+            _ptr(dstream, "dstream", rt, (T, H), allow_none=True, dev=dev),
+            _ptr(dr, "dr", rt, (T, H), allow_none=True, dev=dev),
+            _ptr(dx, "dx", _bf16, (T, H), allow_none=True, dev=dev),
+            _ptr(dweight, "dweight", _f32, (H,), allow_none=True, dev=dev))
 
 
-def _ws(ws):
-    return _ptr(ws, "ws", torch.uint8, allow_none=True), 0 if ws is None else ws.numel()
+def _ws(dev, ws):
+    return _ptr(ws, "ws", torch.uint8, allow_none=True, dev=dev), 0 if ws is None else ws.numel()
 
 
 def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream=None):
@@ -607,16 +622,18 @@ def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream
     dstream [T, H] of r's type, the gradient that reaches r past the norm, or None; dr [T, H] of r's type (it may be
     dstream or r) = dstream + the norm's part; dx the same in bf16 (it may be dy); dweight [H] fp32.  Outputs may be
     None; ws (moe_workspace_size_bwd) is needed with dweight only."""
-    st = _lib.moe_add_rmsnorm_bwd(*_norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight), *_ws(ws),
-                                  _stream(stream, dy))
+    dev = _device(dy, "dy")
+    st = _lib.moe_add_rmsnorm_bwd(*_norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight), *_ws(dev, ws),
+                                  _stream(stream))
     _check("moe_add_rmsnorm_bwd", st)
 
 
 def moe_add_layernorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, dbias, ws, stream=None):
     """The gradient of moe_add_layernorm's y at its stream r, arguments as moe_add_rmsnorm_bwd; dbias [H] fp32 or None."""
-    st = _lib.moe_add_layernorm_bwd(*_norm_bwd_args(dy, r, weight, eps, dstream, dr, dx, dweight),
-                                    _ptr(dbias, "dbias", _f32, (weight.shape[0],), allow_none=True), *_ws(ws),
-                                    _stream(stream, dy))
+    dev = _device(dy, "dy")
+    st = _lib.moe_add_layernorm_bwd(*_norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight),
+                                    _ptr(dbias, "dbias", _f32, (weight.shape[0],), allow_none=True, dev=dev),
+                                    *_ws(dev, ws), _stream(stream))
     _check("moe_add_layernorm_bwd", st)
 
 
@@ -629,15 +646,20 @@ def moe_finalize_bwd(dout, y, pair_row, topk_w, y_shared, x, shared_gate_w, dy, 
     T, H = dout.shape
     k = pair_row.shape[1]
     rows_cap = dy.shape[0]
+    dev = _device(dout, "dout")
     st = _lib.moe_finalize_bwd(
-        _ptr(dout, "dout", _bf16, (T, H)), _ptr(y, "y", _bf16, (rows_cap, H), allow_none=True), rows_cap,
-        _ptr(pair_row, "pair_row", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), T, k, H,
-        _ptr(y_shared, "y_shared", _bf16, (T, H), allow_none=True), _ptr(x, "x", _bf16, (T, H), allow_none=True),
-        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), _ptr(dy, "dy", _bf16, (rows_cap, H)),
-        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True),
-        _ptr(dy_shared, "dy_shared", _bf16, (T, H), allow_none=True), _ptr(dgate, "dgate", _f32, (T,), allow_none=True),
-        _ptr(dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True), _ptr(ws, "ws", torch.uint8), ws.numel(),
-        _stream(stream, dout))
+        _ptr(dout, "dout", _bf16, (T, H)), _ptr(y, "y", _bf16, (rows_cap, H), allow_none=True, dev=dev), rows_cap,
+        _ptr(pair_row, "pair_row", _i32, (T, k), dev=dev),
+        _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True, dev=dev), T, k, H,
+        _ptr(y_shared, "y_shared", _bf16, (T, H), allow_none=True, dev=dev),
+        _ptr(x, "x", _bf16, (T, H), allow_none=True, dev=dev),
+        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True, dev=dev),
+        _ptr(dy, "dy", _bf16, (rows_cap, H), dev=dev),
+        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True, dev=dev),
+        _ptr(dy_shared, "dy_shared", _bf16, (T, H), allow_none=True, dev=dev),
+        _ptr(dgate, "dgate", _f32, (T,), allow_none=True, dev=dev),
+        _ptr(dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True, dev=dev),
+        _ptr(ws, "ws", torch.uint8, dev=dev), ws.numel(), _stream(stream))
     _check("moe_finalize_bwd", st)
 
 
@@ -648,14 +670,16 @@ def moe_permute_bwd(dx_perm, pair_row, topk_w, x, dx_add, dgate, shared_gate_w, 
     T, k = pair_row.shape
     rows_cap, H = dx_perm.shape
     f32 = dx_add is not None and dx_add.dtype is _f32
+    dev = _device(dx_perm, "dx_perm")
     st = _lib.moe_permute_bwd(
-        _ptr(dx_perm, "dx_perm", _bf16, (rows_cap, H)), rows_cap, _ptr(pair_row, "pair_row", _i32, (T, k)),
-        _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True), _ptr(x, "x", _bf16, (T, H), allow_none=True),
-        _ptr(dx_add, "dx_add", _f32 if f32 else _bf16, (T, H), allow_none=True), f32,
-        _ptr(dgate, "dgate", _f32, (T,), allow_none=True),
-        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), T, k, H, _ptr(dx, "dx", _bf16, (T, H)),
-        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True), _ptr(ws, "ws", torch.uint8), ws.numel(),
-        _stream(stream, dx_perm))
+        _ptr(dx_perm, "dx_perm", _bf16, (rows_cap, H)), rows_cap, _ptr(pair_row, "pair_row", _i32, (T, k), dev=dev),
+        _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True, dev=dev),
+        _ptr(x, "x", _bf16, (T, H), allow_none=True, dev=dev),
+        _ptr(dx_add, "dx_add", _f32 if f32 else _bf16, (T, H), allow_none=True, dev=dev), f32,
+        _ptr(dgate, "dgate", _f32, (T,), allow_none=True, dev=dev),
+        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True, dev=dev), T, k, H,
+        _ptr(dx, "dx", _bf16, (T, H), dev=dev), _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True, dev=dev),
+        _ptr(ws, "ws", torch.uint8, dev=dev), ws.numel(), _stream(stream))
     _check("moe_permute_bwd", st)
 
 
@@ -665,11 +689,12 @@ def moe_route_bwd(topk_ids, topk_w, dtopk_w, logits, renorm, dlogits, ws, stream
     may be logits."""
     T, k = topk_ids.shape
     E = dlogits.shape[1]
-    st = _lib.moe_route_bwd(_ptr(topk_ids, "topk_ids", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k)),
-                            _ptr(dtopk_w, "dtopk_w", _f32, (T, k)),
-                            _ptr(logits, "logits", _f32, (T, E), allow_none=True), T, E, k, int(bool(renorm)),
-                            _ptr(dlogits, "dlogits", _f32, (T, E)), _ptr(ws, "ws", torch.uint8), ws.numel(),
-                            _stream(stream, topk_ids))
+    dev = _device(topk_ids, "topk_ids")
+    st = _lib.moe_route_bwd(_ptr(topk_ids, "topk_ids", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k), dev=dev),
+                            _ptr(dtopk_w, "dtopk_w", _f32, (T, k), dev=dev),
+                            _ptr(logits, "logits", _f32, (T, E), allow_none=True, dev=dev), T, E, k, int(bool(renorm)),
+                            _ptr(dlogits, "dlogits", _f32, (T, E), dev=dev), _ptr(ws, "ws", torch.uint8, dev=dev),
+                            ws.numel(), _stream(stream))
     _check("moe_route_bwd", st)
 
 
