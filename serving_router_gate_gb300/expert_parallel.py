@@ -241,16 +241,25 @@ class EPMoELayer:
             return self.peer.reduce(stream)
         return ep_reduce_output(self.partial(x, stream), self.group)
 
+    def _write(self, T: int, run, stream) -> None:
+        """run(slot) and this rank's flag.  A call that is refused leaves the epoch where it was: one ahead of the other
+        ranks' it would read their other slots from then on."""
+        slot = self.peer.begin(T)
+        try:
+            run(slot)
+        except BaseException:
+            self.peer.epoch -= 1
+            raise
+        self.peer.signal(stream)
+
     def write_partial(self, x: torch.Tensor, stream=None) -> None:
         """Peer reduction, first half: this rank's partial into its slot, then its flag."""
-        self.layer.forward(x, stream, out=self.peer.begin(x.shape[0]))
-        self.peer.signal(stream)
+        self._write(x.shape[0], lambda slot: self.layer.forward(x, stream, out=slot), stream)
 
     def write_block_partial(self, x: torch.Tensor, residual: torch.Tensor, stream=None) -> None:
         """write_partial with the norm in front (block())."""
         self.layer.check_block()
-        self.layer.block(x, residual, stream, out=self.peer.begin(x.shape[0]))
-        self.peer.signal(stream)
+        self._write(x.shape[0], lambda slot: self.layer.block(x, residual, stream, out=slot), stream)
 
     def block(self, x: torch.Tensor, residual: torch.Tensor, stream=None) -> torch.Tensor:
         """MoELayer.block over the ranks: every rank adds x to its copy of residual [T, H] in place, and the
