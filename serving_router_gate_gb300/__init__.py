@@ -166,26 +166,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _device(t, name):
-    """t's device, which has to be the current one: the kernels are launched there and would fault on tensors of another
-    (the call's other tensors are held against it by _ptr's dev)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = t.get_device()
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
-    return dev
-
-
-def _ptr(t, name, dtype=None, shape=None, allow_none=False, dev=None):
+def _ptr(t, name, dtype=None, shape=None, allow_none=False):
     if t is None:
         if allow_none:
             return None
         raise ValueError(f"{name} is required")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dev is not None and t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
@@ -193,6 +180,38 @@ def _ptr(t, name, dtype=None, shape=None, allow_none=False, dev=None):
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
+
+
+# Calls whose tensors are held against the current device (a kernel is launched there and would fault
+# on another's): _device of one of them, the others' pointers by _on, the stream by _stream_on.  The
+# device's number takes the place of is_cuda, so the check costs next to nothing.
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors are on cuda:{dev}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return dev
+
+
+def _on(dev, t, name, dtype, shape=None, allow_none=False):
+    if t is None:
+        if allow_none:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, is on {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _stream_on(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _check(fn, status):
@@ -565,13 +584,13 @@ def moe_add_rmsnorm(x, residual, weight, eps, residual_out, y, q=None, scale=Non
     f32 = residual is not None and residual.dtype is _f32
     rt = _f32 if f32 else _bf16
     dev = _device(x, "x")
-    st = _lib.moe_add_rmsnorm(_ptr(x, "x", _bf16, (T, H)),
-                              _ptr(residual, "residual", rt, (T, H), allow_none=True, dev=dev), f32,
-                              _ptr(weight, "weight", _bf16, (H,), dev=dev), eps, T, H,
-                              _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True, dev=dev),
-                              _ptr(y, "y", _bf16, (T, H), allow_none=True, dev=dev),
-                              _ptr(q, "q", torch.uint8, (T, H), allow_none=True, dev=dev),
-                              _ptr(scale, "scale", _f32, (T,), allow_none=True, dev=dev), _stream(stream))
+    st = _lib.moe_add_rmsnorm(_on(dev, x, "x", _bf16, (T, H)),
+                              _on(dev, residual, "residual", rt, (T, H), allow_none=True), f32,
+                              _on(dev, weight, "weight", _bf16, (H,)), eps, T, H,
+                              _on(dev, residual_out, "residual_out", rt, (T, H), allow_none=True),
+                              _on(dev, y, "y", _bf16, (T, H), allow_none=True),
+                              _on(dev, q, "q", torch.uint8, (T, H), allow_none=True),
+                              _on(dev, scale, "scale", _f32, (T,), allow_none=True), _stream_on(dev, stream))
     _check("moe_add_rmsnorm", st)
 
 
@@ -582,14 +601,14 @@ def moe_add_layernorm(x, residual, weight, bias, eps, residual_out, y, q=None, s
     f32 = residual is not None and residual.dtype is _f32
     rt = _f32 if f32 else _bf16
     dev = _device(x, "x")
-    st = _lib.moe_add_layernorm(_ptr(x, "x", _bf16, (T, H)),
-                                _ptr(residual, "residual", rt, (T, H), allow_none=True, dev=dev), f32,
-                                _ptr(weight, "weight", _bf16, (H,), dev=dev),
-                                _ptr(bias, "bias", _bf16, (H,), allow_none=True, dev=dev), eps, T, H,
-                                _ptr(residual_out, "residual_out", rt, (T, H), allow_none=True, dev=dev),
-                                _ptr(y, "y", _bf16, (T, H), allow_none=True, dev=dev),
-                                _ptr(q, "q", torch.uint8, (T, H), allow_none=True, dev=dev),
-                                _ptr(scale, "scale", _f32, (T,), allow_none=True, dev=dev), _stream(stream))
+    st = _lib.moe_add_layernorm(_on(dev, x, "x", _bf16, (T, H)),
+                                _on(dev, residual, "residual", rt, (T, H), allow_none=True), f32,
+                                _on(dev, weight, "weight", _bf16, (H,)),
+                                _on(dev, bias, "bias", _bf16, (H,), allow_none=True), eps, T, H,
+                                _on(dev, residual_out, "residual_out", rt, (T, H), allow_none=True),
+                                _on(dev, y, "y", _bf16, (T, H), allow_none=True),
+                                _on(dev, q, "q", torch.uint8, (T, H), allow_none=True),
+                                _on(dev, scale, "scale", _f32, (T,), allow_none=True), _stream_on(dev, stream))
     _check("moe_add_layernorm", st)
 
 
@@ -605,16 +624,16 @@ def _norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight):
     T, H = dy.shape
     f32 = r.dtype is _f32
     rt = _f32 if f32 else _bf16
-    return (_ptr(dy, "dy", _bf16, (T, H)), _ptr(r, "r", rt, (T, H), dev=dev), f32,
-            _ptr(weight, "weight", _bf16, (H,), dev=dev), eps, T, H,
-            _ptr(dstream, "dstream", rt, (T, H), allow_none=True, dev=dev),
-            _ptr(dr, "dr", rt, (T, H), allow_none=True, dev=dev),
-            _ptr(dx, "dx", _bf16, (T, H), allow_none=True, dev=dev),
-            _ptr(dweight, "dweight", _f32, (H,), allow_none=True, dev=dev))
+    return (_on(dev, dy, "dy", _bf16, (T, H)), _on(dev, r, "r", rt, (T, H)), f32,
+            _on(dev, weight, "weight", _bf16, (H,)), eps, T, H,
+            _on(dev, dstream, "dstream", rt, (T, H), allow_none=True),
+            _on(dev, dr, "dr", rt, (T, H), allow_none=True),
+            _on(dev, dx, "dx", _bf16, (T, H), allow_none=True),
+            _on(dev, dweight, "dweight", _f32, (H,), allow_none=True))
 
 
 def _ws(dev, ws):
-    return _ptr(ws, "ws", torch.uint8, allow_none=True, dev=dev), 0 if ws is None else ws.numel()
+    return _on(dev, ws, "ws", torch.uint8, allow_none=True), 0 if ws is None else ws.numel()
 
 
 def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream=None):
@@ -624,7 +643,7 @@ def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream
     None; ws (moe_workspace_size_bwd) is needed with dweight only."""
     dev = _device(dy, "dy")
     st = _lib.moe_add_rmsnorm_bwd(*_norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight), *_ws(dev, ws),
-                                  _stream(stream))
+                                  _stream_on(dev, stream))
     _check("moe_add_rmsnorm_bwd", st)
 
 
@@ -632,8 +651,8 @@ def moe_add_layernorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, dbias, w
     """The gradient of moe_add_layernorm's y at its stream r, arguments as moe_add_rmsnorm_bwd; dbias [H] fp32 or None."""
     dev = _device(dy, "dy")
     st = _lib.moe_add_layernorm_bwd(*_norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight),
-                                    _ptr(dbias, "dbias", _f32, (weight.shape[0],), allow_none=True, dev=dev),
-                                    *_ws(dev, ws), _stream(stream))
+                                    _on(dev, dbias, "dbias", _f32, (weight.shape[0],), allow_none=True),
+                                    *_ws(dev, ws), _stream_on(dev, stream))
     _check("moe_add_layernorm_bwd", st)
 
 
@@ -648,18 +667,18 @@ def moe_finalize_bwd(dout, y, pair_row, topk_w, y_shared, x, shared_gate_w, dy, 
     rows_cap = dy.shape[0]
     dev = _device(dout, "dout")
     st = _lib.moe_finalize_bwd(
-        _ptr(dout, "dout", _bf16, (T, H)), _ptr(y, "y", _bf16, (rows_cap, H), allow_none=True, dev=dev), rows_cap,
-        _ptr(pair_row, "pair_row", _i32, (T, k), dev=dev),
-        _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True, dev=dev), T, k, H,
-        _ptr(y_shared, "y_shared", _bf16, (T, H), allow_none=True, dev=dev),
-        _ptr(x, "x", _bf16, (T, H), allow_none=True, dev=dev),
-        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True, dev=dev),
-        _ptr(dy, "dy", _bf16, (rows_cap, H), dev=dev),
-        _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True, dev=dev),
-        _ptr(dy_shared, "dy_shared", _bf16, (T, H), allow_none=True, dev=dev),
-        _ptr(dgate, "dgate", _f32, (T,), allow_none=True, dev=dev),
-        _ptr(dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True, dev=dev),
-        _ptr(ws, "ws", torch.uint8, dev=dev), ws.numel(), _stream(stream))
+        _on(dev, dout, "dout", _bf16, (T, H)), _on(dev, y, "y", _bf16, (rows_cap, H), allow_none=True), rows_cap,
+        _on(dev, pair_row, "pair_row", _i32, (T, k)),
+        _on(dev, topk_w, "topk_w", _f32, (T, k), allow_none=True), T, k, H,
+        _on(dev, y_shared, "y_shared", _bf16, (T, H), allow_none=True),
+        _on(dev, x, "x", _bf16, (T, H), allow_none=True),
+        _on(dev, shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True),
+        _on(dev, dy, "dy", _bf16, (rows_cap, H)),
+        _on(dev, dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True),
+        _on(dev, dy_shared, "dy_shared", _bf16, (T, H), allow_none=True),
+        _on(dev, dgate, "dgate", _f32, (T,), allow_none=True),
+        _on(dev, dshared_gate_w, "dshared_gate_w", _f32, (H,), allow_none=True),
+        _on(dev, ws, "ws", torch.uint8), ws.numel(), _stream_on(dev, stream))
     _check("moe_finalize_bwd", st)
 
 
@@ -672,14 +691,14 @@ def moe_permute_bwd(dx_perm, pair_row, topk_w, x, dx_add, dgate, shared_gate_w, 
     f32 = dx_add is not None and dx_add.dtype is _f32
     dev = _device(dx_perm, "dx_perm")
     st = _lib.moe_permute_bwd(
-        _ptr(dx_perm, "dx_perm", _bf16, (rows_cap, H)), rows_cap, _ptr(pair_row, "pair_row", _i32, (T, k), dev=dev),
-        _ptr(topk_w, "topk_w", _f32, (T, k), allow_none=True, dev=dev),
-        _ptr(x, "x", _bf16, (T, H), allow_none=True, dev=dev),
-        _ptr(dx_add, "dx_add", _f32 if f32 else _bf16, (T, H), allow_none=True, dev=dev), f32,
-        _ptr(dgate, "dgate", _f32, (T,), allow_none=True, dev=dev),
-        _ptr(shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True, dev=dev), T, k, H,
-        _ptr(dx, "dx", _bf16, (T, H), dev=dev), _ptr(dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True, dev=dev),
-        _ptr(ws, "ws", torch.uint8, dev=dev), ws.numel(), _stream(stream))
+        _on(dev, dx_perm, "dx_perm", _bf16, (rows_cap, H)), rows_cap, _on(dev, pair_row, "pair_row", _i32, (T, k)),
+        _on(dev, topk_w, "topk_w", _f32, (T, k), allow_none=True),
+        _on(dev, x, "x", _bf16, (T, H), allow_none=True),
+        _on(dev, dx_add, "dx_add", _f32 if f32 else _bf16, (T, H), allow_none=True), f32,
+        _on(dev, dgate, "dgate", _f32, (T,), allow_none=True),
+        _on(dev, shared_gate_w, "shared_gate_w", _bf16, (H,), allow_none=True), T, k, H,
+        _on(dev, dx, "dx", _bf16, (T, H)), _on(dev, dtopk_w, "dtopk_w", _f32, (T, k), allow_none=True),
+        _on(dev, ws, "ws", torch.uint8), ws.numel(), _stream_on(dev, stream))
     _check("moe_permute_bwd", st)
 
 
@@ -690,11 +709,11 @@ def moe_route_bwd(topk_ids, topk_w, dtopk_w, logits, renorm, dlogits, ws, stream
     T, k = topk_ids.shape
     E = dlogits.shape[1]
     dev = _device(topk_ids, "topk_ids")
-    st = _lib.moe_route_bwd(_ptr(topk_ids, "topk_ids", _i32, (T, k)), _ptr(topk_w, "topk_w", _f32, (T, k), dev=dev),
-                            _ptr(dtopk_w, "dtopk_w", _f32, (T, k), dev=dev),
-                            _ptr(logits, "logits", _f32, (T, E), allow_none=True, dev=dev), T, E, k, int(bool(renorm)),
-                            _ptr(dlogits, "dlogits", _f32, (T, E), dev=dev), _ptr(ws, "ws", torch.uint8, dev=dev),
-                            ws.numel(), _stream(stream))
+    st = _lib.moe_route_bwd(_on(dev, topk_ids, "topk_ids", _i32, (T, k)), _on(dev, topk_w, "topk_w", _f32, (T, k)),
+                            _on(dev, dtopk_w, "dtopk_w", _f32, (T, k)),
+                            _on(dev, logits, "logits", _f32, (T, E), allow_none=True), T, E, k, int(bool(renorm)),
+                            _on(dev, dlogits, "dlogits", _f32, (T, E)), _on(dev, ws, "ws", torch.uint8),
+                            ws.numel(), _stream_on(dev, stream))
     _check("moe_route_bwd", st)
 
 

@@ -17,6 +17,10 @@ class Tensor:
     def __init__(self, dtype, *shape):
         self.dtype, self.shape, self.dev = dtype, torch.Size(shape), 0
 
+    @property
+    def device(self):
+        return f"cuda:{self.dev}"
+
     def get_device(self):
         return self.dev
 
