@@ -189,7 +189,9 @@ __global__ void __launch_bounds__(GB_WARPS * 32, 1) gate_bwd_kernel(const __grid
     }
 }
 
-// The same for any H, without the gate weight's gradient: a warp to a token, its rows read twice.
+// The same for any H, without the gate weight's gradient: a warp to a token, its rows read twice.  With
+// the pairs' kernel, this and the weight's one behind the other, 2 pairs: 4096 tokens of 12288 197 us of 120.6
+// at the copy rate, 2048 of 16384 184 of 80.4 (4096 of 8192 in gate_bwd_kernel 94.3 of 80.4).
 __global__ void __launch_bounds__(FB_WARPS * 32) gate_rows_kernel(const __grid_constant__ FinalizeBwdLaunch a) {
     pdl_wait();
     pdl_trigger();
@@ -251,7 +253,10 @@ __global__ void __launch_bounds__(FB_WARPS * 32) gate_weight_kernel(const float*
 // loads in flight against enough warps.  16384 tokens of 2048, us: 4 pairs with DW 62.9 (U 2, 28
 // warps an SM; 24 warps 66.5; U 1, 40 warps 66.9), without 50.8 (U 2, 24; U 1, 36 52.9); 2 pairs
 // with DW 43.0 (U 2, 28; 32 46.5; U 1, 36 44.4); 8 pairs with DW 104 (U 1, 32; 36 over 110; U 2, 24
-// 106.6), without 88.2 (U 2, 24; U 1, 32 90.6, but 4096 tokens 25.5 against 27.5).
+// 106.6), without 88.2 (U 2, 24; U 1, 32 90.6, but 4096 tokens 25.5 against 27.5).  With DW the forms of up
+// to 4 and of up to 8 pairs spill for that, 16 to 64 bytes a thread; 24 warps are what spills nothing.
+// More than 8 pairs: 4096 tokens of 2048, 16 pairs 46.1 without DW (42.7 at the copy rate), 58.9 with (45.3);
+// 32 pairs 86.9 (82.9), 102.4 (85.6); 16384 tokens, 9 pairs 97.9 (100.5), 158 (110.7: the dots of 32 are joined).
 constexpr int PB_LOADS = 8;
 
 template <int MAXK, bool DW, int U, int CTAS, int WARPS>

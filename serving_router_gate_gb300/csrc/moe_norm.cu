@@ -331,6 +331,8 @@ cudaError_t launch_layernorm_type(const NormLaunch& L, int num_sms, cudaStream_t
     // 256 111 / 86, 512 112 / 81, 1024 116 / 86, 1408 116 / 100, 2048 113 / 81, 4096 112 / 85, 5120 114 /
     // 86, 6144 113 / 92, 7168 115 / 95, 8192 115 / 97, 12288 120 / 97, 16384 129 / 107.  At 7168, bf16, 92
     // before the deviations' sum was taken, where three CTAs of 448 threads took 100, four of 224 103.
+    // The forms of 512, 1024 and 5120 spill 4 to 44 bytes a thread (loads to 100) for the CTAs they have;
+    // with fewer, and nothing spilt: 512 five 111 / 85, 1024 twelve 114 / 91, 5120 four 114 / 95.
     const int vec = L.H / 8;
     if (vec <= 32) return launch_layernorm_size<1, 32, STREAM, 6>(L, num_sms, s);
     if (vec <= 64) return launch_layernorm_size<2, 32, STREAM, 6>(L, num_sms, s);

@@ -5,8 +5,9 @@
 //   dr = dstream + rstd * (g - [layer norm: sum(g) / H] - d * rstd^2 * sum(g d) / H)
 //   dweight = sum over rows of dy * d * rstd,  dbias = sum over rows of dy
 //
-// The row's statistics are taken again from r: the row has to be read for d anyway.  All
-// sums are binary32; dr is rounded once for each of its outputs.
+// The row's statistics are taken again from r: the row has to be read for d anyway.  (A bf16 stream
+// holds r rounded: the gradient is taken there, where the forward normalised the unrounded sum.)
+// All sums are binary32; dr is rounded once for each of its outputs.
 //
 // Bound: HBM (8 bytes an element with a bf16 stream and its gradient) and not far behind it
 // the issue rate: 21 instructions an element in all (RMS, bf16), a third of them conversions, a
@@ -36,8 +37,10 @@
 // columns a thread read them again (the weight from shared memory, in binary32).
 //
 // 16384 rows of 7168 with a stream's gradient: RMS, bf16 139 us, 6.8 TB/s, 1.01 of this card's
-// copy rate, layer norm 155 us, 0.91; 8192 rows, fp32: 123 us, 1.0, and 124 us.  4096 of 2048,
-// fp32, layer norm 26.7 us, 0.75; 777 of 1408, bf16 7.6 us, of which the second kernel 3.
+// copy rate, layer norm 156 us, 0.90; 8192 rows, fp32: 123 us, 1.0, and 124 us.  4096 of 2048,
+// fp32, layer norm 26.5 us, 0.76; 777 of 1408, bf16 7.3 us, of which the second kernel 3.5.  The
+// layer norm's bf16 rows issue 29 to 30 instructions an element in 50 to 57 % of their cycles: their
+// 14 to 16 warps an SM wait for shared memory and for their own latency, no pipe is full.
 #include <algorithm>
 #include <atomic>
 
@@ -412,16 +415,21 @@ cudaError_t launch_norm_bwd_type(const NormBwdLaunch& L, int num_sms, cudaStream
     // 16 columns a thread, or 32: those share what a row costs beside its elements among more of
     // them and let more groups of warps work on a CTA's rows, where groups of 16 columns leave many
     // of the 16 warps idle.  The choice decides the order of a row's sums, so it does not depend on T.
-    // us with 16 / 32, 58.7 M elements: bf16, RMS 4096 77 / 78, 5120 84 / 80 (10
-    // warps / 15), 7168 76 / 78; bf16, layer norm 2560 82 / 86, 2816 96 / 82, 3584 89 / 84, 4096 81 / 83,
-    // 4608 114 / 83, 5632 97 / 85, 7168 92 / 86, 8192 83 / 86, but 777 rows of 2816 10.4 / 13.9, 4608 14.2 /
-    // 16.1, 7168 19.0 / 20.4; fp32, layer norm 4096 132 / 123, 5120 122 / 135, without
-    // dstream 120 / 98.
+    // us with 16 / 32, 58.7 M elements and dstream:
+    // bf16, RMS: 4096 77 / 78, 5120 84 / 80 (10 warps / 15), 7168 76 / 78.
+    // bf16, layer norm: 2560 82 / 86, 2816 96 / 82, 3584 89 / 84, 4096 81 / 83, 4608 114 / 83, 5632 97 / 85,
+    // 6656 97 / 90, 7168 92 / 86, 8192 83 / 86; but 777 rows of 2816 10.4 / 13.9, 4608 14.2 / 16.1, 7168
+    // 19.0 / 20.4.
+    // fp32, layer norm, 29.4 M elements: with dstream 7 and 8 warps of 16 columns have room for one
+    // group in the ring below, 32 columns for two of half the warps: 2560 70 / 94, 2816 68 / 87, 3136 94 /
+    // 82, 3584 84 / 74, 4096 77 / 69, 4608 76 / 98, 5632 69 / 88, 7168 67 / 74, 8192 68 / 72; without it, by the
+    // idle warps: 2560 55 / 57, 2816 61 / 56, 3584 57 / 58, 4096 54 / 55, 4608 72 / 60, 5632 63 / 56, 6144 59 /
+    // 54, 6656 63 / 76, 7168 59 / 71.
     const int narrow = (L.H + 511) / 512;  // warps of a group, 16 columns a thread
     const int idle = narrow > NB_WARPS ? NB_WARPS : NB_WARPS % narrow;
     const bool wide = !LN ? (F32 ? L.H > 6144 : idle > 2)
                       : !F32 ? idle > 1
-                             : narrow > NB_WARPS || (L.dstream ? narrow == 7 || narrow == 8 : idle > 2);
+                             : narrow > NB_WARPS || (L.dstream ? narrow == 7 || narrow == 8 : idle > 3);
     const int columns = wide ? 32 : 16;
     NormBwdPlan p;
     p.gw = (L.H + columns * 32 - 1) / (columns * 32);
