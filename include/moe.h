@@ -447,9 +447,10 @@ MOE_API moe_status_t moe_add_rmsnorm(const moe_bf16_t *x, const void *residual, 
 /* moe_add_layernorm -- the same with a layer norm:
  *     r = residual + x, d = r - sum(r) / H
  *     y = d / sqrt(sum(d^2) / H + eps) * weight + bias
- * bias [H] bf16, 16-byte aligned, or NULL (0).  The mean is taken before the squares, so
- * a row far from zero keeps its variance.  With eps > 0 a row of equal values gives
- * y = bias.  Everything else as moe_add_rmsnorm. */
+ * bias [H] bf16, 16-byte aligned, or NULL (0).  The mean is taken before the squares, and
+ * its rounding error out of both, so a row far from zero keeps its deviations and its
+ * variance.  With eps > 0 a row of equal values gives y = bias.  Everything else as
+ * moe_add_rmsnorm. */
 MOE_API moe_status_t moe_add_layernorm(const moe_bf16_t *x, const void *residual, int residual_f32,
                                    const moe_bf16_t *weight, const moe_bf16_t *bias, float eps, int64_t T, int H,
                                    void *residual_out, moe_bf16_t *y, uint8_t *q, float *scale, moe_stream_t stream);
@@ -463,6 +464,10 @@ MOE_API moe_status_t moe_add_layernorm(const moe_bf16_t *x, const void *residual
  *   moe_permute_bwd          from the experts' inputs to the tokens
  *   moe_route_bwd            from the routing weights to the logits
  *   moe_add_rmsnorm_bwd, moe_add_layernorm_bwd   from the norm's output to its input
+ * What the experts' own gradients need beside these the forward calls do not keep:
+ * moe_grouped_fc1 writes h = SwiGLU(gate, up), not gate and up, and moe_forward keeps h and
+ * the experts' outputs y in its workspace.  A training step calls the stages
+ * (moe_grouped_fc1, moe_grouped_fc2, moe_finalize) or its own products, and holds y itself.
  * Every sum is binary32 and has a fixed order: a call repeats itself bit for bit (on one
  * kind of GPU: the weight gradients are cut by its number of SMs).  A row of an output does
  * not depend on the batch that it stands in, with one exception: the dot products behind
@@ -481,6 +486,11 @@ MOE_API size_t moe_workspace_size_bwd(int H);
  *   dy       [T, H] bf16          gradient of y
  *   r        [T, H] bf16 (r_f32 = 0) or fp32 (1): the stream moe_add_rmsnorm wrote to
  *            residual_out (or its x, without a residual)
+ *            With a bf16 stream that is the rounded sum, and the gradient is taken there: mean,
+ *            rstd and deviations are those of the given r, where the forward's were those of the
+ *            unrounded one.  They are apart by r's rounding, up to 2^-8 |r|, which is little in rows
+ *            about zero and can be as much as the deviations far from it: such rows want an
+ *            fp32 stream
  *   dstream  [T, H] of r's type, or NULL: gradient that reaches r past the norm
  *   dr       [T, H] of r's type out, or NULL: the gradient of the residual and of x
  *   dx       [T, H] bf16 out, or NULL: the same values
@@ -554,7 +564,8 @@ MOE_API moe_status_t moe_permute_bwd(const moe_bf16_t *dx_perm, int64_t rows_cap
  *            non-local pairs in place: keep a copy)
  *   dtopk_w  [T, k] fp32     summed over the ranks where experts are spread over several
  *   logits   [T, E] fp32     x . gate_w with logit_bias added (needed with renorm = 0 only, else
- *            not read and may be NULL)
+ *            not read and may be NULL); moe_route writes ids and weights alone, so the caller
+ *            computes them
  *   dlogits  [T, E] fp32 out; it may be logits
  *   ws       only its status word is used
  * gate_w's gradient is dlogits^T x, x's part dlogits gate_w, logit_bias's the column sums.  An id

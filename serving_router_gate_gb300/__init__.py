@@ -640,7 +640,8 @@ def moe_add_rmsnorm_bwd(dy, r, weight, eps, dstream, dr, dx, dweight, ws, stream
     """The gradient of moe_add_rmsnorm's y at its stream r (residual_out): dy [T, H] bf16; r [T, H] bf16 or fp32;
     dstream [T, H] of r's type, the gradient that reaches r past the norm, or None; dr [T, H] of r's type (it may be
     dstream or r) = dstream + the norm's part; dx the same in bf16 (it may be dy); dweight [H] fp32.  Outputs may be
-    None; ws (moe_workspace_size_bwd) is needed with dweight only."""
+    None; ws (moe_workspace_size_bwd) is needed with dweight only.  With a bf16 stream r is the rounded sum, and the
+    gradient is taken there, where the forward normalised the unrounded one."""
     dev = _device(dy, "dy")
     st = _lib.moe_add_rmsnorm_bwd(*_norm_bwd_args(dev, dy, r, weight, eps, dstream, dr, dx, dweight), *_ws(dev, ws),
                                   _stream_on(dev, stream))
