@@ -1,5 +1,5 @@
-// moe_rows.cuh -- for the gradient kernels: arithmetic on pairs of binary32 values, and the sums
-// of a row's values over the lanes of a warp and over a group of warps, in a fixed order.
+// moe_rows.cuh -- for the layer norm and the gradient kernels: arithmetic on pairs of binary32 values,
+// and the sums of a row's values over the lanes of a warp and over a group of warps, in a fixed order.
 #pragma once
 
 #include "moe_internal.cuh"
